@@ -181,17 +181,18 @@ def prepare(case, seed):
 
 def prepare_own(s, grad_type, dev):
     """The handle, pointer arrays, workspace and hyperparameters that a program keeps from step to step."""
-    from fsdp_sharded_mixed_zero_amd import zero
+    from fsdp_sharded_mixed_zero_amd import tensors, zero
 
-    s["list"] = zero.zero_tensors(s["params"], s["ms"], s["vs"], master=s.get("masters"), m_scale=s.get("m_scales"),
-                                  v_scale=s.get("v_scales"), group=s["group"], grad_dtype=grad_type)
+    s["list"] = tensors.zero_tensors(s["params"], s["ms"], s["vs"], master=s.get("masters"),
+                                     m_scale=s.get("m_scales"), v_scale=s.get("v_scales"), group=s["group"],
+                                     grad_dtype=grad_type)
     if "grads" in s:
         s["grad_ptrs"] = zero.pointer_array(s["grads"])
     if s["case"]["op"] == "sqnorm":
-        s["ws"] = torch.empty(zero.zero_tensors_sqnorm_workspace_bytes(s["list"]) // 8, dtype=torch.float64, device=dev)
+        s["ws"] = torch.empty(tensors.zero_tensors_sqnorm_workspace_bytes(s["list"]) // 8, dtype=torch.float64, device=dev)
     if "m32s" in s:
         s["m32_ptrs"], s["v32_ptrs"] = zero.pointer_array(s["m32s"]), zero.pointer_array(s["v32s"])
-    s["hparams"] = [zero.hparams(**h) for h in s["hp"]]
+    s["hparams"] = tensors.group_array([zero.hparams(**h) for h in s["hp"]])
 
 
 # ------------------------------------------------------------------- one pass
@@ -199,16 +200,16 @@ def prepare_own(s, grad_type, dev):
 def run(state):
     op = state["case"]["op"]
     if own:
-        from fsdp_sharded_mixed_zero_amd import zero
+        from fsdp_sharded_mixed_zero_amd import tensors
 
         if op == "sqnorm":
-            zero.zero_tensors_sqnorm(state["list"], state["grad_ptrs"], state["out"], False, state["ws"])
+            tensors.zero_tensors_sqnorm(state["list"], state["grad_ptrs"], state["out"], False, state["ws"])
         elif op == "import8":
-            zero.zero_tensors_state_import(state["list"], state["m32_ptrs"], state["v32_ptrs"])
+            tensors.zero_tensors_state_import(state["list"], state["m32_ptrs"], state["v32_ptrs"])
         elif op == "export8":
-            zero.zero_tensors_state_export(state["list"], state["m32_ptrs"], state["v32_ptrs"])
+            tensors.zero_tensors_state_export(state["list"], state["m32_ptrs"], state["v32_ptrs"])
         else:
-            zero.zero_tensors_adamw_step(state["list"], state["grad_ptrs"], state["hparams"], state["rank_sq"], RANKS)
+            tensors.zero_tensors_adamw_step(state["list"], state["grad_ptrs"], state["hparams"], state["rank_sq"], RANKS)
     else:
         {"sqnorm": plain_sqnorm, "import8": plain_import, "export8": plain_export, "adamw32": plain_adamw32,
          "adamw8": plain_adamw8}[op](state)
