@@ -23,7 +23,7 @@ own = False
 
 BLOCK = 256                 # elements that share one scale
 TOP = 448.0                 # largest e4m3 value
-LEAST = 2.0 ** -100         # smallest maximum a scale is formed from
+LEAST, LEAST_ROOT = 2.0 ** -100, 2.0 ** -63     # smallest maxima that scales are formed from: of |m|, of sqrt(v)
 BETA1, BETA2, EPS = 0.9, 0.999, 1e-8
 RANKS = 64                  # partial sums of squares the clip coefficient is formed from
 
@@ -304,7 +304,7 @@ def coded(m, v, s, at):
     """The 8-bit values of the fp64 moments m and v and their blocks' scales."""
     block, place, n = places(s, at)
     tops = (block_max(m.abs(), place, n).float(), block_max(v, place, n).float().double().sqrt().float())
-    tops = [t.clamp(min=LEAST).double() for t in tops]
+    tops = [t.clamp(min=least).double() for t, least in zip(tops, (LEAST, LEAST_ROOT))]
     up = [(TOP / t).float().double()[block] for t in tops]
     mq = rounded8(m * up[0])
     vq = torch.where(v > 0, rounded8(v.sqrt() * up[1]).clamp(min=2.0 ** -9), torch.zeros_like(v))
@@ -378,13 +378,13 @@ def nearest8(x):
     return torch.copysign(grid[(k + tie.long()).clamp(max=126)], x)
 
 
-def exact_codes(x, least):
+def exact_codes(x, root):
     """A tensor's 8-bit values and scales: blocks of 256 in turn, the last one shorter."""
     n = x.numel()
     full = torch.nn.functional.pad(x, (0, -n % BLOCK)).view(-1, BLOCK)
-    top = full.abs().amax(1).float().clamp(min=LEAST)
+    top = full.abs().amax(1).float().clamp(min=LEAST_ROOT if root else LEAST)
     q = nearest8(full * (TOP / top.double()).float().double()[:, None])
-    if least:
+    if root:
         q = torch.where((full > 0) & (q == 0), torch.full_like(q, 2.0 ** -9), q)
     return q.view(-1)[:n], (top.double() / TOP).float()
 
