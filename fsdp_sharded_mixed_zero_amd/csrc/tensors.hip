@@ -9,9 +9,9 @@
 //                           fp32 moments <-> the 8-bit state
 //
 // A unit of work is 1024 consecutive elements of one tensor, four 8-bit
-// blocks, and belongs to one wave. A launch carries the gradient pointers of
-// up to 384 tensors in its arguments; everything that does not change from
-// step to step is in the list's device table.
+// blocks, and belongs to one wave. A launch carries the gradients' addresses
+// in its arguments, as 32-bit offsets of up to 768 tensors; everything that
+// does not change from step to step is in the list's device table.
 #include <cstring>
 
 #include "tensors_internal.h"
@@ -19,14 +19,16 @@
 namespace {
 
 using zero::GroupConst;
+using zero::kSqChunk;
 using zero::kUnitElems;
 using zero::StepConst;
 
-constexpr int kListThreads = 256;                       // four waves, four units
-constexpr int kListWaves = kListThreads / 64;
-constexpr int64_t kListMaxUnits = int64_t(1) << 24;     // units per launch: 2^30 work-items
+constexpr int kListThreads = 64;                        // one wave, one unit
+constexpr int kSqListWaves = 4, kSqListThreads = 64 * kSqListWaves;
+constexpr int64_t kListMaxUnits = int64_t(1) << 23;     // units per launch: at most 2^31 work-items
 
-// What a launch covers: units [u0, u1), which lie in tensors [t0, t0 + n).
+// What a launch covers: units [u0, u1) (chunks, for the norm), which lie in
+// tensors [t0, t0 + n); first[t]: tensor t's first one.
 struct ListRange {
   const int32_t* first;
   const zero_tensor* rec;
@@ -34,23 +36,38 @@ struct ListRange {
   int32_t u0, u1;
 };
 
+// Addresses of a launch's N tensors: element-size steps from the lowest one,
+// so that twice as many fit the arguments as with pointers. A launch ends
+// before a tensor that lies 2^32 elements or more from another of its own.
+constexpr uint32_t kNoTensor = 0xFFFFFFFFu;
+template <int N>
+struct Addresses {
+  uintptr_t base;
+  uint32_t step[N];
+
+  template <typename T>
+  __device__ __forceinline__ T* at(int i) const {
+    const uint32_t s = step[i];
+    return s == kNoTensor ? nullptr : reinterpret_cast<T*>(base + uintptr_t(s) * sizeof(T));
+  }
+};
+
 struct SqArgs {
   ListRange l;
   double* partial;
-  const void* grads[ZERO_TENSORS_PER_LAUNCH];
+  Addresses<ZERO_TENSORS_PER_LAUNCH> grads;
 };
 
 struct StepArgs {
   ListRange l;
   StepConst c;
-  const void* grads[ZERO_TENSORS_PER_LAUNCH];
+  Addresses<ZERO_TENSORS_PER_LAUNCH> grads;
 };
 
-constexpr int kStatePerLaunch = 224;
+constexpr int kStatePerLaunch = 480;
 struct State8Args {
   ListRange l;
-  const float* m[kStatePerLaunch];
-  const float* v[kStatePerLaunch];
+  Addresses<kStatePerLaunch> m, v;
 };
 
 constexpr int kUploadWords = 960;
@@ -65,79 +82,127 @@ static_assert(sizeof(SqArgs) <= 4096 && sizeof(StepArgs) <= 4096 && sizeof(State
 
 // ------------------------------------------------------- finding the tensor
 
-// The tensor that holds unit u: the last t of the launch with first[t] <= u.
-// Each round the 64 lanes probe 64 evenly spaced entries and count those at or
-// below u (the counts ascend), so 384 tensors take two rounds.
-__device__ __forceinline__ int find_tensor(const ListRange& l, int u) {
-  int lo = l.t0, span = l.n;
+// The tensor that holds unit u, the last t of the launch with first[t] <= u,
+// and in *start its first unit. Each round the 64 lanes probe 64 evenly spaced
+// entries and count those at or below u (the counts ascend), so 768 tensors
+// take two rounds.
+__device__ __forceinline__ int find_tensor(const int32_t* first, int t0, int n, int u, int* start) {
+  int lo = t0, span = n, at_lo;
   const int lane = threadIdx.x & 63;
-  while (span > 1) {
-    const int stride = (span + 63) >> 6;
-    const int k = lane * stride;
-    const bool below = k < span && l.first[lo + k] <= u;
-    const int top = (__popcll(__ballot(below)) - 1) * stride;
-    lo += top;
-    span = span - top < stride ? span - top : stride;
-  }
+  do {
+    const int stride = (span + 63) >> 6, k = lane * stride;
+    const int x = k < span ? first[lo + k] : 0x7FFFFFFF;
+    const int lanes = __popcll(__ballot(x <= u)) - 1;
+    at_lo = __builtin_amdgcn_readlane(x, lanes);
+    lo += lanes * stride;
+    span = span - lanes * stride < stride ? span - lanes * stride : stride;
+  } while (span > 1);
+  *start = at_lo;
   return __builtin_amdgcn_readfirstlane(lo);
 }
 
-// This wave's unit, or -1 past the launch's last.
-__device__ __forceinline__ int my_unit(const ListRange& l) {
-  const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x) >> 6);
-  const int64_t u = int64_t(l.u0) + int64_t(blockIdx.x) * kListWaves + wave;
-  return u < l.u1 ? int(u) : -1;
+// A value at a wave-uniform address that the kernel does not write, read by a
+// scalar load (the compiler cannot know that the stores leave it alone).
+template <typename T>
+__device__ __forceinline__ T uniform_load(const T* p) {
+  return *(const __attribute__((address_space(4))) T*)p;
+}
+
+// What a wave works on: its tensor, its unit's first element, how many elements
+// the tensor has from there on, and the block of the unit it takes if it takes
+// only one.
+struct Unit {
+  int t;
+  int64_t base, rest;
+  int block;
+};
+
+// The wave's unit; with SPLIT four waves share one, a block each.
+template <bool SPLIT>
+__device__ __forceinline__ Unit my_unit(const ListRange& l) {
+  const int u = l.u0 + int(SPLIT ? blockIdx.x >> 2 : blockIdx.x);
+  Unit w;
+  w.block = SPLIT ? int(blockIdx.x & 3) : 0;
+  int start;
+  w.t = find_tensor(l.first, l.t0, l.n, u, &start);
+  w.base = int64_t(u - start) * kUnitElems;
+  w.rest = uniform_load(&l.rec[w.t].len) - w.base;
+  return w;
 }
 
 // ------------------------------------------------- four elements of a tensor
 //
-// A lane owns elements e .. e + 3 of a block (e = 4 * lane), of which the first
-// `cnt` exist (cnt < 4 at a tensor's end only). Tensors start at any element,
-// so the vector accesses are declared with their element's alignment: the
-// hardware takes them at any address.
+// A lane owns elements 4 * lane .. 4 * lane + 3 of each block, of which the
+// first `cnt` exist (cnt < 4 at a tensor's end only). Tensors start at any
+// element, so the vector accesses are declared with their element's
+// alignment: the hardware takes them at any address. Everything is read and
+// written once, so the accesses are non-temporal (cached ones: the 32-bit step
+// 20 % slower, the 8-bit step 10 %), except the loads of bytes, whose lines two
+// instructions share where a tensor starts off a boundary (24.3 M elements so:
+// 70.9 us cached, 81.3 us non-temporal; 119 M on boundaries: 363 and 358). The
+// pointers are marked global: one that comes out of memory would be a flat one.
+
+#define ZERO_GLOBAL __attribute__((address_space(1)))
 
 typedef f32x4 f32x4_any __attribute__((aligned(4)));
 typedef u32x2 bf16x4_any __attribute__((aligned(2)));
+typedef u32x4 words4_any __attribute__((aligned(2)));
 typedef unsigned int bytes4_any __attribute__((aligned(1)));
 
+template <typename V>
+__device__ __forceinline__ V stream_load(const void* p) {
+  return __builtin_nontemporal_load((const ZERO_GLOBAL V*)p);
+}
+
+template <typename V>
+__device__ __forceinline__ void stream_store(void* p, V x) {
+  __builtin_nontemporal_store(x, (ZERO_GLOBAL V*)p);
+}
+
+__device__ __forceinline__ f32x4 widen(u32x2 w) { return f32x4{bf16_lo(w[0]), bf16_hi(w[0]), bf16_lo(w[1]), bf16_hi(w[1])}; }
+__device__ __forceinline__ f32x4 widen(f32x4 w) { return w; }
+
 __device__ __forceinline__ f32x4 load4(const float* p, int cnt) {
-  if (cnt >= 4) return *reinterpret_cast<const f32x4_any*>(p);
+  if (cnt >= 4) return stream_load<f32x4_any>(p);
   f32x4 r = {0.f, 0.f, 0.f, 0.f};
-  for (int k = 0; k < cnt; ++k) r[k] = p[k];
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+    if (k < cnt) r[k] = p[k];
   return r;
 }
 
-__device__ __forceinline__ f32x4 load4(const uint16_t* p, int cnt) {
+__device__ __forceinline__ u32x2 load4(const uint16_t* p, int cnt) {
+  if (cnt >= 4) return stream_load<bf16x4_any>(p);
   u32x2 w = {0u, 0u};
-  if (cnt >= 4) {
-    w = *reinterpret_cast<const bf16x4_any*>(p);
-  } else {
-    if (cnt > 0) w[0] = p[0];
-    if (cnt > 1) w[0] |= uint32_t(p[1]) << 16;
-    if (cnt > 2) w[1] = p[2];
-  }
-  return f32x4{bf16_lo(w[0]), bf16_hi(w[0]), bf16_lo(w[1]), bf16_hi(w[1])};
+  if (cnt > 0) w[0] = p[0];
+  if (cnt > 1) w[0] |= uint32_t(p[1]) << 16;
+  if (cnt > 2) w[1] = p[2];
+  return w;
 }
 
 __device__ __forceinline__ uint32_t load4(const uint8_t* p, int cnt) {
-  if (cnt >= 4) return *reinterpret_cast<const bytes4_any*>(p);
+  if (cnt >= 4) return *(const ZERO_GLOBAL bytes4_any*)p;
   uint32_t w = 0;
-  for (int k = 0; k < cnt; ++k) w |= uint32_t(p[k]) << (8 * k);
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+    if (k < cnt) w |= uint32_t(p[k]) << (8 * k);
   return w;
 }
 
 __device__ __forceinline__ void store4(float* p, int cnt, f32x4 x) {
   if (cnt >= 4) {
-    *reinterpret_cast<f32x4_any*>(p) = x;
+    stream_store<f32x4_any>(p, x);
   } else {
-    for (int k = 0; k < cnt; ++k) p[k] = x[k];
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      if (k < cnt) p[k] = x[k];
   }
 }
 
 __device__ __forceinline__ void store4(uint16_t* p, int cnt, f32x4 x) {
   const u32x2 w = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
   if (cnt >= 4) {
-    *reinterpret_cast<bf16x4_any*>(p) = w;
+    stream_store<bf16x4_any>(p, w);
   } else {
     if (cnt > 0) p[0] = uint16_t(w[0]);
     if (cnt > 1) p[1] = uint16_t(w[0] >> 16);
@@ -147,19 +212,24 @@ __device__ __forceinline__ void store4(uint16_t* p, int cnt, f32x4 x) {
 
 __device__ __forceinline__ void store4(uint8_t* p, int cnt, uint32_t w) {
   if (cnt >= 4) {
-    *reinterpret_cast<bytes4_any*>(p) = w;
+    stream_store<bytes4_any>(p, w);
   } else {
-    for (int k = 0; k < cnt; ++k) p[k] = uint8_t(w >> (8 * k));
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      if (k < cnt) p[k] = uint8_t(w >> (8 * k));
   }
 }
 
-// Elements of a tensor of `len` from e on, at most 4, at least 0.
-__device__ __forceinline__ int count4(int64_t len, int64_t e) {
-  const int64_t n = len - e;
+// Of the `rest` elements from a block's first on, how many this lane's four hold.
+__device__ __forceinline__ int count4(int64_t rest) {
+  const int64_t n = rest - 4 * int(threadIdx.x & 63);
   return n >= 4 ? 4 : n > 0 ? int(n) : 0;
 }
 
 // ------------------------------------------------------------- 8-bit moments
+
+constexpr int kBlocks = zero::kUnitBlocks;
+constexpr int kBlock = ZERO_STATE8_BLOCK;
 
 __device__ __forceinline__ f32x4 e4m3_values(uint32_t w) {
   const auto a = __builtin_amdgcn_cvt_pk_f32_fp8(int(w), false), b = __builtin_amdgcn_cvt_pk_f32_fp8(int(w), true);
@@ -168,28 +238,83 @@ __device__ __forceinline__ f32x4 e4m3_values(uint32_t w) {
 
 // The nearest e4m3 values (ties to even), one byte each; a NaN or a value
 // beyond 464 gives the NaN.
-__device__ __forceinline__ uint32_t e4m3_bytes(float a, float b, float c, float d) {
-  const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-  return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, lo, true));
+__device__ __forceinline__ uint32_t e4m3_bytes(f32x4 x) {
+  const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], 0, false);
+  return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], lo, true));
 }
 
-// x to fp32 with all of its low bits folded into one sticky bit (rounding to
-// odd at 21 significant bits): rounding the result to the 4 bits of an e4m3
-// value then gives the correct rounding of x, ties and all.
-__device__ __forceinline__ float sticky_f32(double x) {
-  const uint64_t b = uint64_t(__double_as_longlong(x));
-  const uint64_t hi = (b >> 32) | (uint32_t(b) != 0u ? 1u : 0u);
-  return float(__longlong_as_double((long long)(hi << 32)));
+__device__ __forceinline__ float e4m3_value(uint32_t byte) { return __builtin_amdgcn_cvt_f32_fp8(int(byte), 0); }
+
+template <typename T>
+__device__ __forceinline__ float pick(const T& x, int k) {
+  return k == 0 ? x[0] : k == 1 ? x[1] : k == 2 ? x[2] : x[3];
 }
 
-// The largest x of the wave (x >= 0).
-__device__ __forceinline__ float wave_max(float x) {
+// Bytes `down` and `up` of values just below and just above four exact ones:
+// where they differ, a border lies between, and exact(k) (the exact value's
+// magnitude, or its square with SQ) decides in fp64; a tie goes to the even byte.
+template <bool SQ, typename F>
+__device__ __forceinline__ uint32_t decide(uint32_t down, uint32_t up, F exact) {
+  for (uint32_t diff = down ^ up; diff != 0;) {
+    const int k = (__ffs(int(diff)) - 1) >> 3;
+    const uint32_t byte = 0xFFu << (8 * k);
+    const uint32_t lo = (down >> (8 * k)) & 0xFFu, hi = (up >> (8 * k)) & 0xFFu;
+    double mid = 0.5 * (fabs(double(e4m3_value(lo))) + fabs(double(e4m3_value(hi))));
+    if (SQ) mid *= mid;
+    const double z = exact(k);
+    if (z > mid || (z == mid && (lo & 1u))) down = (down & ~byte) | (up & byte);
+    diff &= ~byte;
+  }
+  return down;
+}
+
+// The fp32 values that are rounded to bytes are off by at most 2^-22 of
+// themselves: the bytes of x * (1 - 2^-21) and x * (1 + 2^-21) agree unless a
+// border is that near (one element in 10^5).
+constexpr float kBelow = 1.f - 0x1p-21f, kAbove = 1.f + 0x1p-21f;
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t x) {
+  return uint32_t(__builtin_amdgcn_update_dpp(0, int(x), CTRL, 0xF, 0xF, true));
+}
+
+__device__ __forceinline__ uint32_t max_u(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// Lane of block b's maximum of |m| after block_maxima (kind 0), or of v (kind 1).
+__device__ __forceinline__ constexpr int lane_of(int b, int kind) {
+  return 16 * (b == 1 ? 2 : b == 2 ? 1 : b) + 8 * kind;
+}
+
+// Wave-wide maxima of eight non-negative floats (as bits, which order alike)
+// per lane: am[b] and av[b] of four blocks. Each exchange folds two values'
+// halves into one register, so eight reductions take 21 instructions and end
+// with the maximum of block b in the eight lanes from lane_of(b, kind) on.
+__device__ __forceinline__ uint32_t block_maxima(const uint32_t am[4], const uint32_t av[4]) {
+  uint32_t r[4], s[2];
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) x = fmaxf(x, __shfl_xor(x, off, 64));
-  return x;
+  for (int i = 0; i < 4; ++i) {   // low half-wave: the pair's first, high half: its second
+    const uint32_t x = i < 2 ? am[2 * i] : av[2 * i - 4], y = i < 2 ? am[2 * i + 1] : av[2 * i - 3];
+    const auto sw = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+    r[i] = max_u(sw[0], sw[1]);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {   // even rows: the pair's first register, odd rows: its second
+    const auto sw = __builtin_amdgcn_permlane16_swap(r[2 * i], r[2 * i + 1], false, false);
+    s[i] = max_u(sw[0], sw[1]);
+  }
+  const uint32_t a = max_u(s[0], dpp<0x128>(s[0])), b = max_u(s[1], dpp<0x128>(s[1]));   // row_ror:8
+  uint32_t x = (threadIdx.x & 8) ? b : a;
+  x = max_u(x, dpp<0x141>(x));   // row_half_mirror
+  x = max_u(x, dpp<0x4E>(x));    // quad_perm [2, 3, 0, 1]
+  return max_u(x, dpp<0xB1>(x)); // quad_perm [1, 0, 3, 2]
 }
 
-// x, or 0 where it is NaN or +infinity.
+// The largest |m| and v of this lane's four. NaN is ignored (fmaxf).
+__device__ __forceinline__ void lane_maxima(const float m[4], const float v[4], uint32_t& am, uint32_t& av) {
+  am = __float_as_uint(fmaxf(fmaxf(fmaxf(fabsf(m[0]), fabsf(m[1])), fmaxf(fabsf(m[2]), fabsf(m[3]))), 0.f));
+  av = __float_as_uint(fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])), 0.f));
+}
+
 __device__ __forceinline__ float finite_or_0(float x) { return x < __builtin_inff() ? x : 0.f; }
 
 constexpr float kE4M3Max = 448.f;
@@ -197,56 +322,94 @@ constexpr float kE4M3Max = 448.f;
 // the root's maximum comes from a square that is normal in fp32.
 constexpr float kLeastMax = 0x1p-100f, kLeastRoot = 0x1p-63f;
 
-// One block of the 8-bit state: this lane's four moments m, v (fp64) to bytes.
-// y[k] = sqrt(v[k]) in units of the block's scale, for the update.
-struct Block8 {
-  uint32_t m, v;
-  float m_scale, v_scale;
-  float y[4];
+__device__ __forceinline__ float lane_f32(float x, int lane) {
+  return __uint_as_float(uint32_t(__builtin_amdgcn_readlane(int(__float_as_uint(x)), lane)));
+}
+
+// Scales of up to four blocks, every lane holding those of its own eight-lane
+// group (lane_of); scale = max / 448, up = 448 / max.
+struct Scales {
+  float scale, up;
 };
 
-__device__ __forceinline__ Block8 block_to_8bit(const double m[4], const double v[4]) {
-  float am = 0.f, av = 0.f;
+// m, v: this lane's moments of NB blocks as fp32. Writes the scales of the
+// blocks that exist.
+template <int NB>
+__device__ __forceinline__ Scales block_scales(const float m[NB][4], const float v[NB][4], float* m_scale,
+                                               float* v_scale, int64_t block0, int64_t n_blocks) {
+  uint32_t am[kBlocks] = {}, av[kBlocks] = {};
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    am = fmaxf(am, finite_or_0(fabsf(float(m[k]))));
-    av = fmaxf(av, finite_or_0(float(v[k])));
-  }
-  am = fmaxf(wave_max(am), kLeastMax);
-  const float as = fmaxf(sqrtf(wave_max(av)), kLeastRoot);
-  Block8 r;
-  r.m_scale = am / kE4M3Max;
-  r.v_scale = as / kE4M3Max;
-  const double im = double(kE4M3Max / am), is = double(kE4M3Max / as), is2 = is * is;
-  r.m = e4m3_bytes(sticky_f32(m[0] * im), sticky_f32(m[1] * im), sticky_f32(m[2] * im), sticky_f32(m[3] * im));
-  // The root in fp32 is off by less than 2^-22; where the 8-bit values of
-  // y * (1 - 2^-21) and y * (1 + 2^-21) differ, a border lies between them and
-  // the squares decide in fp64.
-  double w[4];
-  float lo[4], hi[4];
+  for (int b = 0; b < NB; ++b) lane_maxima(m[b], v[b], am[b], av[b]);
+  uint32_t top = block_maxima(am, av);
+  if (__any(top >= 0x7F800000u)) {   // an infinite moment: the maxima again, without it
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    w[k] = v[k] * is2;
-    r.y[k] = sqrtf(float(w[k]));
-    const float y = v[k] > 0.0 ? fmaxf(r.y[k], 0x1p-9f) : r.y[k];   // not below the least e4m3 value
-    lo[k] = y * (1.f - 0x1p-21f);
-    hi[k] = y * (1.f + 0x1p-21f);
-  }
-  uint32_t down = e4m3_bytes(lo[0], lo[1], lo[2], lo[3]);
-  const uint32_t up = e4m3_bytes(hi[0], hi[1], hi[2], hi[3]);
-  if (down != up) {
-    const f32x4 a = e4m3_values(down), b = e4m3_values(up);
+    for (int b = 0; b < NB; ++b) {
+      float fm[4], fv[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t byte = 0xFFu << (8 * k);
-      if (((down ^ up) & byte) == 0) continue;
-      const double mid = 0.5 * (double(a[k]) + double(b[k]));
-      const bool even = ((down >> (8 * k)) & 1u) == 0;
-      if (w[k] > mid * mid || (w[k] == mid * mid && !even)) down = (down & ~byte) | (up & byte);
+      for (int k = 0; k < 4; ++k) {
+        fm[k] = finite_or_0(fabsf(m[b][k]));
+        fv[k] = finite_or_0(v[b][k]);
+      }
+      lane_maxima(fm, fv, am[b], av[b]);
     }
+    top = block_maxima(am, av);
   }
-  r.v = down;
-  return r;
+  const int lane = threadIdx.x & 63;
+  const bool root = lane & 8;
+  const float x = __uint_as_float(top);
+  const float t = root ? fmaxf(sqrtf(x), kLeastRoot) : fmaxf(x, kLeastMax);
+  const Scales s{t / kE4M3Max, kE4M3Max / t};
+  const int row = lane >> 4, b = row == 1 ? 2 : row == 2 ? 1 : row;
+  const int64_t block = block0 + b;
+  if ((lane & 7) == 0 && b < NB && block < n_blocks) ((ZERO_GLOBAL float*)(root ? v_scale : m_scale))[block] = s.scale;
+  return s;
+}
+
+// m, in units of the scale, to bytes. mf: fp32 of m; exact(k): the fp64 m[k].
+template <typename F>
+__device__ __forceinline__ uint32_t m_bytes(const float mf[4], float up, F exact) {
+  f32x4 lo, hi;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float y = mf[k] * up;
+    lo[k] = y * kBelow;
+    hi[k] = y * kAbove;
+  }
+  const uint32_t down = e4m3_bytes(lo), above = e4m3_bytes(hi);
+  return decide<false>(down, above, [&](int j) { return fabs(exact(j)) * double(up); });
+}
+
+// sqrt(v), in units of the scale, to bytes; y[k]: that root in fp32, for the
+// update (roots below 2^-63 units, 2^-72 of the block's largest, count as zero
+// in y). vf: fp32 of v; exact(k): the fp64 v[k].
+template <typename F>
+__device__ __forceinline__ uint32_t v_bytes(const float vf[4], float up, float y[4], F exact) {
+  const auto square = [&](int j) { return exact(j) * (double(up) * double(up)); };
+  f32x4 lo, hi;
+  if (up < 0x1p52f) {
+    // vf * up^2, rounded three times, then the root within one unit in the
+    // last place: off by less than 2^-22. Where vf is subnormal the root is
+    // under 2^-11 units, half of the least byte's border.
+    const float up2 = up * up;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) y[k] = __builtin_amdgcn_sqrtf(vf[k] * up2);
+  } else {   // a block whose largest root is under 2^-43: up^2 may pass fp32, vf may be subnormal
+#pragma unroll
+    for (int k = 0; k < 4; ++k) y[k] = __builtin_amdgcn_sqrtf(float(square(k)));
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    lo[k] = y[k] * kBelow;
+    hi[k] = y[k] * kAbove;
+  }
+  const uint32_t below = e4m3_bytes(lo), above = e4m3_bytes(hi);
+  uint32_t bytes = decide<true>(below, above, square);
+  // a zero byte (0x80 in `zeros`): a root above zero is stored as the least value
+  for (uint32_t zeros = (bytes - 0x01010101u) & ~bytes & 0x80808080u; zeros != 0; zeros &= zeros - 1) {
+    const int k = (__ffs(int(zeros)) - 1) >> 3;
+    if (((bytes >> (8 * k)) & 0xFFu) == 0 && exact(k) > 0.0) bytes |= 1u << (8 * k);
+  }
+  return bytes;
 }
 
 // ------------------------------------------------------------------ kernels
@@ -255,35 +418,88 @@ __global__ __launch_bounds__(256) void tensors_upload_kernel(const UploadArgs a)
   for (int i = threadIdx.x; i < a.n; i += 256) a.dst[i] = a.w[i];
 }
 
+// Sums of squares. A wave takes a chunk of 4096 elements of one tensor, a lane
+// 16 bytes of it at a time: VE elements. (119 M bf16 gradients: 45 us with the
+// final sum, 5.3 TB/s; in chunks of 2048, 47 us; of 1024, where finding the
+// tensor takes most of a wave's life, 62 us. A short list in one block and one
+// launch instead of two is slower from some 16 thousand elements on: one CU
+// squares them in fp64, 92 thousand in 7.8 us against 5.5.)
 template <typename G>
-__global__ __launch_bounds__(kListThreads) void tensors_sqnorm_kernel(const SqArgs a) {
-  const int u = my_unit(a.l);
-  if (u < 0) return;
-  const int t = find_tensor(a.l, u), lane = threadIdx.x & 63;
-  const G* g = static_cast<const G*>(a.grads[t - a.l.t0]);
-  double acc = 0.0;
-  if (g != nullptr) {
-    const int64_t len = a.l.rec[t].len, base = int64_t(u - a.l.first[t]) * kUnitElems;
+struct SqChunk {
+  static constexpr int VE = 16 / sizeof(G), NV = kSqChunk / (64 * VE);
+  u32x4 x[NV];
+  G end;   // one of the elements after the last whole 16 bytes
+
+  // The chunk's values from g on, of which `rest` exist (none with g null).
+  __device__ __forceinline__ void load(const G* g, int64_t rest) {
+    const int lane = threadIdx.x & 63;
+    const int n = g == nullptr ? 0 : rest < kSqChunk ? int(rest) : kSqChunk;
 #pragma unroll
-    for (int k = 0; k < zero::kUnitBlocks; ++k) {
-      const int64_t e = base + k * ZERO_STATE8_BLOCK + 4 * lane;
-      acc = sq4(load4(g + e, count4(len, e)), acc);
+    for (int b = 0; b < NV; ++b) {
+      const int e = (b * 64 + lane) * VE;
+      x[b] = u32x4{0u, 0u, 0u, 0u};
+      if (e + VE <= n) x[b] = stream_load<words4_any>(g + e);
     }
+    end = G(0);
+    if (lane < n % VE) end = *(const ZERO_GLOBAL G*)(g + (n - n % VE + lane));
   }
+
+  __device__ __forceinline__ double add(double acc) const {
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) acc += __shfl_xor(acc, off, 64);
-  if (lane == 0) a.partial[u] = acc;
+    for (int b = 0; b < NV; ++b) {
+      if constexpr (sizeof(G) == 2) acc = sq8(x[b], acc);
+      else acc = sq4(__builtin_bit_cast(f32x4, x[b]), acc);
+    }
+    if constexpr (sizeof(G) == 2) return sq1(end, acc);
+    else return fma(double(end), double(end), acc);
+  }
+};
+
+// One wave per chunk, one partial per block.
+template <typename G>
+__global__ __launch_bounds__(kSqListThreads) void tensors_sqnorm_kernel(const SqArgs a) {
+  const int64_t u = a.l.u0 + int64_t(blockIdx.x) * kSqListWaves + (threadIdx.x >> 6);
+  double acc = 0.0;
+  if (u < a.l.u1) {
+    int start;
+    const int t = find_tensor(a.l.first, a.l.t0, a.l.n, __builtin_amdgcn_readfirstlane(int(u)), &start);
+    const int64_t base = (u - start) * kSqChunk;
+    const G* g = a.grads.template at<const G>(t - a.l.t0);
+    SqChunk<G> x;
+    x.load(g == nullptr ? g : g + base, uniform_load(&a.l.rec[t].len) - base);
+    acc = x.add(acc);
+  }
+  const double s = block_sum<kSqListThreads>(acc);
+  if (threadIdx.x == 0) a.partial[blockIdx.x] = s;
 }
 
-// The clip coefficient, in the flat updates' order.
+// The clip coefficient, in the flat updates' order. Up to 64 sums are read
+// eight at a time by scalar loads (one at a time: a chain of memory latencies;
+// a lane each and v_readlane: three times the instructions, 576 us against 543
+// for the 32-bit step over 119 M elements).
 __device__ __forceinline__ double list_clip(const StepConst& c) {
-  AdamWArgs a{};
-  a.clip_on = c.clip_on;
-  a.n_ranks = c.n_ranks;
-  a.rank_sq = c.rank_sq;
-  a.max_norm = c.max_norm;
-  a.clip_eps = c.clip_eps;
-  return clip_coefficient(a);
+  if (!c.clip_on) return 1.0;
+  if (c.n_ranks > 64) {
+    AdamWArgs a{};
+    a.clip_on = 1;
+    a.n_ranks = c.n_ranks;
+    a.rank_sq = c.rank_sq;
+    a.max_norm = c.max_norm;
+    a.clip_eps = c.clip_eps;
+    return clip_coefficient(a);
+  }
+  double G = 0.0;
+  int r = 0;
+  for (; r + 8 <= c.n_ranks; r += 8) {
+    double x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = uniform_load(c.rank_sq + r + k);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) G += x[k];
+  }
+  for (; r < c.n_ranks; ++r) G += uniform_load(c.rank_sq + r);
+  const double ratio = c.max_norm / (sqrt(G) + c.clip_eps);
+  return ratio >= 1.0 ? 1.0 : ratio;   // a NaN ratio stays NaN
 }
 
 // The update of one element in fp64 (adamw_exact, with a group's constants).
@@ -298,156 +514,267 @@ __device__ __forceinline__ void exact_update(const zero::AdamWExact& x, double c
   v = float(v1);
 }
 
+// The 8-bit state from block b0 of a unit on: this lane's first byte of each
+// moment, the tensor's scales, the block's index and the number of blocks.
+struct State8 {
+  uint8_t *m, *v;
+  float *m_scale, *v_scale;
+  int64_t block0, n_blocks;
+};
+
+__device__ __forceinline__ State8 state8_of(const ListRange& l, const Unit& w, int b0) {
+  const zero_tensor* r = l.rec + w.t;
+  const int64_t e = w.base + b0 * kBlock + 4 * int(threadIdx.x & 63);
+  return State8{static_cast<uint8_t*>(uniform_load(&r->m)) + e, static_cast<uint8_t*>(uniform_load(&r->v)) + e,
+                uniform_load(&r->m_scale), uniform_load(&r->v_scale), w.base / kBlock + b0,
+                (w.base + w.rest + kBlock - 1) / kBlock};
+}
+
+// The stored scales of NB blocks: of m in lanes 0-3, of the roots in lanes 4-7.
+template <int NB>
+__device__ __forceinline__ float old_scales(const State8& s) {
+  const int lane = threadIdx.x & 63;
+  const int64_t block = s.block0 + (lane & 3);
+  if (lane >= 8 || (lane & 3) >= NB || block >= s.n_blocks) return 0.f;
+  return ((const ZERO_GLOBAL float*)(lane < 4 ? s.m_scale : s.v_scale))[block];
+}
+
+// Calls work.run<NB>(b): NB blocks from b on, all of them full where NB is more
+// than one. A wave with a unit of its own holds a full one's four blocks at
+// once and takes the blocks at a tensor's end in turn.
+template <bool SPLIT, typename W>
+__device__ __forceinline__ void over_unit(const Unit& w, const W& work) {
+  if constexpr (SPLIT) {
+    if (w.block * kBlock < w.rest) work.template run<1>(w.block);
+  } else if (w.rest >= kUnitElems) {
+    work.template run<kBlocks>(0);
+  } else {
+#pragma unroll 1
+    for (int b = 0; b * kBlock < w.rest; ++b) work.template run<1>(b);
+  }
+}
+
+// The 32-bit step of NB blocks from b0 on in one wave: all loads first.
 // P: uint16_t (bf16 parameters and an fp32 master) or float (its own master).
 template <typename P, typename G>
-__global__ __launch_bounds__(kListThreads) void tensors_adamw_kernel(const StepArgs a) {
-  const int u = my_unit(a.l);
-  if (u < 0) return;
-  const int t = find_tensor(a.l, u), lane = threadIdx.x & 63;
-  const G* g = static_cast<const G*>(a.grads[t - a.l.t0]);
-  if (g == nullptr) return;
-  const zero_tensor& r = a.l.rec[t];
-  const int64_t len = r.len, base = int64_t(u - a.l.first[t]) * kUnitElems;
-  constexpr bool kOwnMaster = sizeof(P) == 4;
-  P* param = static_cast<P*>(r.param);
-  float* master = kOwnMaster ? static_cast<float*>(r.param) : r.master;
-  float *ms = static_cast<float*>(r.m), *vs = static_cast<float*>(r.v);
-  const int group = r.group;
-  AdamWArgs k{};
-  k.beta1 = a.c.g[group].beta1;
-  k.omb1 = a.c.g[group].omb1;
-  k.beta2 = a.c.g[group].beta2;
-  k.omb2 = a.c.g[group].omb2;
-  k.lr_wd = a.c.g[group].lr_wd;
-  k.step_size = a.c.g[group].step_size;
-  k.inv_sqrt_bc2 = a.c.g[group].inv_sqrt_bc2;
-  k.eps = a.c.g[group].eps;
-  const double c64 = list_clip(a.c);
-  const float c = float(c64);
-#pragma unroll 1
-  for (int b = 0; b < zero::kUnitBlocks; ++b) {
-    const int64_t e = base + b * ZERO_STATE8_BLOCK + 4 * lane;
-    const int cnt = count4(len, e);
-    if (cnt == 0) break;
-    const f32x4 g4 = load4(g + e, cnt);
-    f32x4 p4 = load4(master + e, cnt), m4 = load4(ms + e, cnt), v4 = load4(vs + e, cnt);
+struct AdamW32 {
+  const StepArgs& a;
+  const Unit& w;
+  const G* grad;
+
+  template <int NB>
+  __device__ __forceinline__ void run(int b0) const {
+    const zero_tensor* r = a.l.rec + w.t;
+    const int64_t e = w.base + b0 * kBlock + 4 * int(threadIdx.x & 63);
+    P* param = static_cast<P*>(uniform_load(&r->param)) + e;
+    float* master = sizeof(P) == 4 ? reinterpret_cast<float*>(param) : uniform_load(&r->master) + e;
+    float *ms = static_cast<float*>(uniform_load(&r->m)) + e, *vs = static_cast<float*>(uniform_load(&r->v)) + e;
+    const G* g = grad + e;
+    const int cnt = NB > 1 ? 4 : count4(w.rest - b0 * kBlock);
+    decltype(load4(g, 4)) g4[NB];
+    f32x4 p4[NB], m4[NB], v4[NB];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float p1, m1, v1;
-      float p = p4[i], m = m4[i], v = v4[i];
-      if (adamw_fast(k, c, g4[i], p, m, v, p1, m1, v1)) {
-        exact_update(a.c.x[group], c64, g4[i], p, m, v);
-        p1 = p, m1 = m, v1 = v;
+    for (int b = 0; b < NB; ++b) {
+      g4[b] = load4(g + b * kBlock, cnt);
+      p4[b] = load4(master + b * kBlock, cnt);
+      m4[b] = load4(ms + b * kBlock, cnt);
+      v4[b] = load4(vs + b * kBlock, cnt);
+    }
+    const int group = uniform_load(&r->group);
+    const GroupConst& k = a.c.g[group];
+    AdamWArgs q{};
+    q.beta1 = k.beta1, q.omb1 = k.omb1, q.beta2 = k.beta2, q.omb2 = k.omb2;
+    q.lr_wd = k.lr_wd, q.step_size = k.step_size, q.inv_sqrt_bc2 = k.inv_sqrt_bc2, q.eps = k.eps;
+    const double c64 = list_clip(a.c);
+    const float c = float(c64);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const f32x4 gw = widen(g4[b]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float p1, m1, v1;
+        float p = p4[b][i], m = m4[b][i], v = v4[b][i];
+        if (adamw_fast(q, c, gw[i], p, m, v, p1, m1, v1)) {
+          exact_update(a.c.x[group], c64, gw[i], p, m, v);
+          p1 = p, m1 = m, v1 = v;
+        }
+        p4[b][i] = p1, m4[b][i] = m1, v4[b][i] = v1;
       }
-      p4[i] = p1, m4[i] = m1, v4[i] = v1;
+      store4(master + b * kBlock, cnt, p4[b]);
+      store4(ms + b * kBlock, cnt, m4[b]);
+      store4(vs + b * kBlock, cnt, v4[b]);
+      if constexpr (sizeof(P) == 2) store4(param + b * kBlock, cnt, p4[b]);
     }
-    store4(master + e, cnt, p4);
-    store4(ms + e, cnt, m4);
-    store4(vs + e, cnt, v4);
-    if constexpr (!kOwnMaster) store4(param + e, cnt, p4);
   }
+};
+
+template <typename P, typename G, bool SPLIT>
+__global__ __launch_bounds__(kListThreads) void tensors_adamw_kernel(const StepArgs a) {
+  const Unit w = my_unit<SPLIT>(a.l);
+  const G* g = a.grads.template at<const G>(w.t - a.l.t0);
+  if (g != nullptr) over_unit<SPLIT>(w, AdamW32<P, G>{a, w, g});
 }
 
+// The 8-bit step of NB blocks from b0 on in one wave: all loads first, then
+// the moments in fp64, the blocks' maxima together, then block by block the
+// bytes and the update.
 template <typename P, typename G>
+struct AdamW8 {
+  const StepArgs& a;
+  const Unit& w;
+  const G* grad;
+
+  template <int NB>
+  __device__ __forceinline__ void run(int b0) const {
+    const int lane = threadIdx.x & 63;
+    const zero_tensor* r = a.l.rec + w.t;
+    const int64_t e = w.base + b0 * kBlock + 4 * lane;
+    P* param = static_cast<P*>(uniform_load(&r->param)) + e;
+    float* master = sizeof(P) == 4 ? reinterpret_cast<float*>(param) : uniform_load(&r->master) + e;
+    const State8 st = state8_of(a.l, w, b0);
+    const G* g = grad + e;
+    const int cnt = NB > 1 ? 4 : count4(w.rest - b0 * kBlock);
+    decltype(load4(g, 4)) g4[NB];
+    f32x4 p4[NB];
+    uint32_t m8[NB], s8[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      g4[b] = load4(g + b * kBlock, cnt);
+      p4[b] = load4(master + b * kBlock, cnt);
+      m8[b] = load4(st.m + b * kBlock, cnt);
+      s8[b] = load4(st.v + b * kBlock, cnt);
+    }
+    const float old = old_scales<NB>(st);
+    const int group = uniform_load(&r->group);
+    const GroupConst& k = a.c.g[group];
+    const zero::AdamWExact& x = a.c.x[group];
+    const double c = list_clip(a.c), c1 = x.omb1 * c, c2 = x.omb2 * (c * c);
+    // beta1 * M * scale + (1 - beta1) * c * g and beta2 * (S * scale)^2 + (1 - beta2) * (c * g)^2
+    const auto first = [&](int b, float value, float gk) {
+      const double scaled = x.beta1 * double(lane_f32(old, b));
+      return fma(double(value), scaled, c1 * double(gk));
+    };
+    const auto second = [&](int b, float value, float gk) {
+      const double s = double(lane_f32(old, 4 + b)), gd = double(gk);
+      return fma(double(value * value), x.beta2 * (s * s), c2 * (gd * gd));   // an e4m3 value's square is exact
+    };
+    float mf[NB][4], vf[NB][4];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const f32x4 mv = e4m3_values(m8[b]), sv = e4m3_values(s8[b]), gv = widen(g4[b]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        mf[b][i] = float(first(b, mv[i], gv[i]));
+        vf[b][i] = float(second(b, sv[i], gv[i]));
+      }
+      __builtin_amdgcn_sched_barrier(0);   // block by block: all four interleaved take 40 registers more
+    }
+    const Scales s = block_scales<NB>(mf, vf, st.m_scale, st.v_scale, st.block0, st.n_blocks);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      // an element's moments again in fp64, where a byte hangs on them
+      const auto exact_m = [&](int j) { return first(b, e4m3_value((m8[b] >> (8 * j)) & 0xFFu), pick(widen(g4[b]), j)); };
+      const auto exact_v = [&](int j) { return second(b, e4m3_value((s8[b] >> (8 * j)) & 0xFFu), pick(widen(g4[b]), j)); };
+      const uint32_t mb = m_bytes(mf[b], lane_f32(s.up, lane_of(b, 0)), exact_m);
+      float y[4];
+      const uint32_t vb = v_bytes(vf[b], lane_f32(s.up, lane_of(b, 1)), y, exact_v);
+      const float v_scale = lane_f32(s.scale, lane_of(b, 1));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float denom = fmaf(y[i] * v_scale, k.inv_sqrt_bc2, k.eps);
+        const float q = mf[b][i] * __builtin_amdgcn_rcpf(denom);   // the reciprocal within one unit in the last place
+        p4[b][i] = fmaf(-k.step_size, q, fmaf(-k.lr_wd, p4[b][i], p4[b][i]));
+      }
+      store4(master + b * kBlock, cnt, p4[b]);
+      if constexpr (sizeof(P) == 2) store4(param + b * kBlock, cnt, p4[b]);
+      store4(st.m + b * kBlock, cnt, mb);
+      store4(st.v + b * kBlock, cnt, vb);
+    }
+  }
+};
+
+template <typename P, typename G, bool SPLIT>
 __global__ __launch_bounds__(kListThreads) void tensors_adamw8_kernel(const StepArgs a) {
-  const int u = my_unit(a.l);
-  if (u < 0) return;
-  const int t = find_tensor(a.l, u), lane = threadIdx.x & 63;
-  const G* g = static_cast<const G*>(a.grads[t - a.l.t0]);
-  if (g == nullptr) return;
-  const zero_tensor& r = a.l.rec[t];
-  const int64_t len = r.len, base = int64_t(u - a.l.first[t]) * kUnitElems;
-  constexpr bool kOwnMaster = sizeof(P) == 4;
-  P* param = static_cast<P*>(r.param);
-  float* master = kOwnMaster ? static_cast<float*>(r.param) : r.master;
-  uint8_t *ms = static_cast<uint8_t*>(r.m), *vs = static_cast<uint8_t*>(r.v);
-  const GroupConst& k = a.c.g[r.group];
-  const zero::AdamWExact& x = a.c.x[r.group];
-  const double c = list_clip(a.c);
-#pragma unroll 1
-  for (int b = 0; b < zero::kUnitBlocks; ++b) {
-    const int64_t e0 = base + b * ZERO_STATE8_BLOCK, e = e0 + 4 * lane, block = e0 / ZERO_STATE8_BLOCK;
-    if (e0 >= len) break;   // uniform: the whole wave takes part in the block's maxima
-    const int cnt = count4(len, e);
-    const f32x4 g4 = load4(g + e, cnt);
-    f32x4 p4 = load4(master + e, cnt);
-    const f32x4 m8 = e4m3_values(load4(ms + e, cnt)), s8 = e4m3_values(load4(vs + e, cnt));
-    const double m_scale = double(r.m_scale[block]), v_scale = double(r.v_scale[block]);
-    double m[4], v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {   // elements past the end are zeros here and leave the maxima alone
-      const double gh = c * double(g4[i]), s = double(s8[i]) * v_scale;
-      m[i] = x.beta1 * (double(m8[i]) * m_scale) + x.omb1 * gh;
-      v[i] = x.beta2 * (s * s) + x.omb2 * (gh * gh);
-    }
-    const Block8 q = block_to_8bit(m, v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float denom = fmaf(q.y[i] * q.v_scale, k.inv_sqrt_bc2, k.eps);
-      p4[i] = fmaf(-k.step_size, float(m[i]) / denom, fmaf(-k.lr_wd, p4[i], p4[i]));
-    }
-    store4(master + e, cnt, p4);
-    if constexpr (!kOwnMaster) store4(param + e, cnt, p4);
-    store4(ms + e, cnt, q.m);
-    store4(vs + e, cnt, q.v);
-    if (lane == 0) {
-      r.m_scale[block] = q.m_scale;
-      r.v_scale[block] = q.v_scale;
-    }
-  }
+  const Unit w = my_unit<SPLIT>(a.l);
+  const G* g = a.grads.template at<const G>(w.t - a.l.t0);
+  if (g != nullptr) over_unit<SPLIT>(w, AdamW8<P, G>{a, w, g});
 }
 
+struct Import8 {
+  const ListRange& l;
+  const Unit& w;
+  const float *m32, *v32;
+
+  template <int NB>
+  __device__ __forceinline__ void run(int b0) const {
+    const int64_t e = w.base + b0 * kBlock + 4 * int(threadIdx.x & 63);
+    const State8 st = state8_of(l, w, b0);
+    const int cnt = NB > 1 ? 4 : count4(w.rest - b0 * kBlock);
+    float m[NB][4], v[NB][4];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const f32x4 m4 = load4(m32 + e + b * kBlock, cnt), v4 = load4(v32 + e + b * kBlock, cnt);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) m[b][i] = m4[i], v[b][i] = v4[i];
+    }
+    const Scales s = block_scales<NB>(m, v, st.m_scale, st.v_scale, st.block0, st.n_blocks);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      float y[4];
+      store4(st.m + b * kBlock, cnt,
+             m_bytes(m[b], lane_f32(s.up, lane_of(b, 0)), [&](int j) { return double(pick(m[b], j)); }));
+      store4(st.v + b * kBlock, cnt,
+             v_bytes(v[b], lane_f32(s.up, lane_of(b, 1)), y, [&](int j) { return double(pick(v[b], j)); }));
+    }
+  }
+};
+
+template <bool SPLIT>
 __global__ __launch_bounds__(kListThreads) void tensors_import_kernel(const State8Args a) {
-  const int u = my_unit(a.l);
-  if (u < 0) return;
-  const int t = find_tensor(a.l, u), lane = threadIdx.x & 63;
-  const float *m32 = a.m[t - a.l.t0], *v32 = a.v[t - a.l.t0];
-  if (m32 == nullptr) return;
-  const zero_tensor& r = a.l.rec[t];
-  const int64_t len = r.len, base = int64_t(u - a.l.first[t]) * kUnitElems;
-#pragma unroll 1
-  for (int b = 0; b < zero::kUnitBlocks; ++b) {
-    const int64_t e0 = base + b * ZERO_STATE8_BLOCK, e = e0 + 4 * lane, block = e0 / ZERO_STATE8_BLOCK;
-    if (e0 >= len) break;
-    const int cnt = count4(len, e);
-    const f32x4 m4 = load4(m32 + e, cnt), v4 = load4(v32 + e, cnt);
-    const double m[4] = {m4[0], m4[1], m4[2], m4[3]}, v[4] = {v4[0], v4[1], v4[2], v4[3]};
-    const Block8 q = block_to_8bit(m, v);
-    store4(static_cast<uint8_t*>(r.m) + e, cnt, q.m);
-    store4(static_cast<uint8_t*>(r.v) + e, cnt, q.v);
-    if (lane == 0) {
-      r.m_scale[block] = q.m_scale;
-      r.v_scale[block] = q.v_scale;
-    }
-  }
+  const Unit w = my_unit<SPLIT>(a.l);
+  const float *m32 = a.m.at<const float>(w.t - a.l.t0), *v32 = a.v.at<const float>(w.t - a.l.t0);
+  if (m32 != nullptr) over_unit<SPLIT>(w, Import8{a.l, w, m32, v32});
 }
 
-__global__ __launch_bounds__(kListThreads) void tensors_export_kernel(const State8Args a) {
-  const int u = my_unit(a.l);
-  if (u < 0) return;
-  const int t = find_tensor(a.l, u), lane = threadIdx.x & 63;
-  float *m32 = const_cast<float*>(a.m[t - a.l.t0]), *v32 = const_cast<float*>(a.v[t - a.l.t0]);
-  if (m32 == nullptr) return;
-  const zero_tensor& r = a.l.rec[t];
-  const int64_t len = r.len, base = int64_t(u - a.l.first[t]) * kUnitElems;
-#pragma unroll 1
-  for (int b = 0; b < zero::kUnitBlocks; ++b) {
-    const int64_t e = base + b * ZERO_STATE8_BLOCK + 4 * lane, block = e / ZERO_STATE8_BLOCK;
-    const int cnt = count4(len, e);
-    if (cnt == 0) break;
-    const f32x4 m8 = e4m3_values(load4(static_cast<const uint8_t*>(r.m) + e, cnt));
-    const f32x4 s8 = e4m3_values(load4(static_cast<const uint8_t*>(r.v) + e, cnt));
-    const float m_scale = r.m_scale[block];
-    const double v_scale = double(r.v_scale[block]), v_scale2 = v_scale * v_scale;
-    f32x4 m4, v4;
+struct Export8 {
+  const ListRange& l;
+  const Unit& w;
+  float *m32, *v32;
+
+  template <int NB>
+  __device__ __forceinline__ void run(int b0) const {
+    const int64_t e = w.base + b0 * kBlock + 4 * int(threadIdx.x & 63);
+    const State8 st = state8_of(l, w, b0);
+    const int cnt = NB > 1 ? 4 : count4(w.rest - b0 * kBlock);
+    uint32_t m8[NB], s8[NB];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      m4[i] = m8[i] * m_scale;
-      v4[i] = float(double(s8[i] * s8[i]) * v_scale2);   // the square of an e4m3 value is exact
+    for (int b = 0; b < NB; ++b) {
+      m8[b] = load4(st.m + b * kBlock, cnt);
+      s8[b] = load4(st.v + b * kBlock, cnt);
     }
-    store4(m32 + e, cnt, m4);
-    store4(v32 + e, cnt, v4);
+    const float old = old_scales<NB>(st);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const f32x4 m = e4m3_values(m8[b]), root = e4m3_values(s8[b]);
+      const float m_scale = lane_f32(old, b);
+      const double s = double(lane_f32(old, 4 + b)), s2 = s * s;
+      f32x4 m4, v4;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        m4[i] = m[i] * m_scale;
+        v4[i] = float(double(root[i] * root[i]) * s2);   // an e4m3 value's square is exact
+      }
+      store4(m32 + e + b * kBlock, cnt, m4);
+      store4(v32 + e + b * kBlock, cnt, v4);
+    }
   }
+};
+
+template <bool SPLIT>
+__global__ __launch_bounds__(kListThreads) void tensors_export_kernel(const State8Args a) {
+  const Unit w = my_unit<SPLIT>(a.l);
+  float *m32 = a.m.at<float>(w.t - a.l.t0), *v32 = a.v.at<float>(w.t - a.l.t0);
+  if (m32 != nullptr) over_unit<SPLIT>(w, Export8{a.l, w, m32, v32});
 }
 
 // ----------------------------------------------------------------- launches
@@ -458,33 +785,82 @@ int launched(const char* who) {
   return zero::ok();
 }
 
-// Calls go(range) for ranges that cover the list's units: at most per_launch
-// tensors and kListMaxUnits units each.
-template <typename F>
-int for_ranges(const zero_tensors_s* h, int per_launch, F go) {
+// The lowest and the highest address of some tensors.
+struct Window {
+  uintptr_t lo = ~uintptr_t(0), hi = 0;
+
+  // Whether p joins without taking the window beyond 32-bit steps of `size`.
+  bool take(const void* p, size_t size) {
+    if (p == nullptr) return true;
+    const uintptr_t a = std::min(lo, uintptr_t(p)), b = std::max(hi, uintptr_t(p));
+    if ((b - a) / size >= kNoTensor) return false;
+    lo = a, hi = b;
+    return true;
+  }
+
+  template <int N>
+  void write(Addresses<N>* out, const void* const* p, int n, size_t size) const {
+    out->base = lo;
+    for (int i = 0; i < n; ++i)
+      out->step[i] = p[i] == nullptr ? kNoTensor : uint32_t((uintptr_t(p[i]) - lo) / size);
+  }
+};
+
+// Calls go(range) for ranges that cover the list's units (chunks): at most `most`
+// tensors, as far as fits(t) lets tensor t join the ones before it, and
+// kListMaxUnits units each. restart() begins a new set of tensors.
+template <typename R, typename F, typename Go>
+int for_ranges(const zero_tensors_s* h, bool chunks, int most, R restart, F fits, Go go) {
   const int32_t n = int32_t(h->t.size());
-  const int32_t* first = static_cast<const int32_t*>(h->table);
+  const std::vector<int32_t>& counts = chunks ? h->chunk : h->first;
+  const int32_t* first = reinterpret_cast<const int32_t*>(static_cast<const char*>(h->table) +
+                                                          (chunks ? zero::table_chunks_at(n) : 0));
   const zero_tensor* rec =
       reinterpret_cast<const zero_tensor*>(static_cast<const char*>(h->table) + zero::table_records_at(n));
-  for (int32_t t0 = 0; t0 < n; t0 += per_launch) {
-    const int32_t t1 = std::min(n, t0 + per_launch);
-    const int64_t end = h->first[size_t(t1)];
-    for (int64_t u = h->first[size_t(t0)]; u < end; u += kListMaxUnits) {
+  for (int32_t t0 = 0; t0 < n;) {
+    restart();
+    int32_t t1 = t0;
+    while (t1 < n && t1 - t0 < most && (h->t[size_t(t1)].len == 0 || fits(t1))) ++t1;
+    const int64_t end = counts[size_t(t1)];
+    for (int64_t u = counts[size_t(t0)]; u < end; u += kListMaxUnits) {
       const ListRange l{first, rec, t0, t1 - t0, int32_t(u), int32_t(std::min(end, u + kListMaxUnits))};
       if (int rc = go(l)) return rc;
     }
+    t0 = t1;
   }
   return zero::ok();
 }
 
-dim3 list_grid(const ListRange& l) { return dim3(unsigned((l.u1 - l.u0 + kListWaves - 1) / kListWaves)); }
+// for_ranges over the gradients' addresses, which go into args.grads.
+template <typename A, typename Go>
+int for_gradients(const zero_tensors_s* h, bool chunks, const void* const* grads, A* args, Go go) {
+  const size_t size = h->grad_type == ZERO_BF16 ? 2 : 4;
+  Window w;
+  return for_ranges(
+      h, chunks, ZERO_TENSORS_PER_LAUNCH, [&] { w = Window(); }, [&](int32_t t) { return w.take(grads[t], size); },
+      [&](const ListRange& l) {
+        args->l = l;
+        w.write(&args->grads, grads + l.t0, l.n, size);
+        return go();
+      });
+}
+
+// Whether four waves share a unit.
+constexpr int64_t kSplitUnits = 1024;
+bool split_units(const ListRange& l) { return l.u1 - l.u0 <= kSplitUnits; }
+
+// Launches kernel(args): one wave per unit, or with `split` four.
+#define ZERO_LIST_LAUNCH(kernel, split, args, stream) \
+  hipLaunchKernelGGL((kernel), dim3(unsigned((args).l.u1 - (args).l.u0) * ((split) ? 4u : 1u)), dim3(kListThreads), 0, stream, args)
 
 template <typename P, typename G>
 void launch_step(bool wide, const StepArgs& a, hipStream_t stream) {
   if (wide)
-    hipLaunchKernelGGL((tensors_adamw_kernel<P, G>), list_grid(a.l), dim3(kListThreads), 0, stream, a);
+    ZERO_LIST_LAUNCH((tensors_adamw_kernel<P, G, true>), true, a, stream);
+  else if (split_units(a.l))
+    ZERO_LIST_LAUNCH((tensors_adamw8_kernel<P, G, true>), true, a, stream);
   else
-    hipLaunchKernelGGL((tensors_adamw8_kernel<P, G>), list_grid(a.l), dim3(kListThreads), 0, stream, a);
+    ZERO_LIST_LAUNCH((tensors_adamw8_kernel<P, G, false>), false, a, stream);
 }
 
 }  // namespace
@@ -501,6 +877,7 @@ int launch_upload(const zero_tensors_s* h, void* table, hipStream_t stream, cons
   const int32_t n = int32_t(h->t.size());
   std::vector<uint32_t> words(table_bytes(n) / 4, 0u);
   std::memcpy(words.data(), h->first.data(), h->first.size() * sizeof(int32_t));
+  std::memcpy(words.data() + table_chunks_at(n) / 4, h->chunk.data(), h->chunk.size() * sizeof(int32_t));
   std::memcpy(words.data() + table_records_at(n) / 4, h->t.data(), h->t.size() * sizeof(zero_tensor));
   for (size_t at = 0; at < words.size(); at += kUploadWords) {
     UploadArgs a;
@@ -515,27 +892,26 @@ int launch_upload(const zero_tensors_s* h, void* table, hipStream_t stream, cons
 
 int launch_sqnorm(const zero_tensors_s* h, const void* const* grads, double* out, int32_t accumulate, double* ws,
                   hipStream_t stream, const char* who) {
-  const int rc = for_ranges(h, ZERO_TENSORS_PER_LAUNCH, [&](const ListRange& l) {
-    SqArgs a;
-    a.l = l;
-    a.partial = ws;
-    std::copy(grads + l.t0, grads + l.t0 + l.n, a.grads);
+  SqArgs a;
+  int64_t done = 0;   // partial sums written
+  const int rc = for_gradients(h, true, grads, &a, [&] {
+    const int64_t chunks = a.l.u1 - a.l.u0, blocks = (chunks + kSqListWaves - 1) / kSqListWaves;
+    a.partial = ws + done;
+    done += blocks;
     if (h->grad_type == ZERO_BF16)
-      hipLaunchKernelGGL(tensors_sqnorm_kernel<uint16_t>, list_grid(l), dim3(kListThreads), 0, stream, a);
+      hipLaunchKernelGGL(tensors_sqnorm_kernel<uint16_t>, dim3(unsigned(blocks)), dim3(kSqListThreads), 0, stream, a);
     else
-      hipLaunchKernelGGL(tensors_sqnorm_kernel<float>, list_grid(l), dim3(kListThreads), 0, stream, a);
+      hipLaunchKernelGGL(tensors_sqnorm_kernel<float>, dim3(unsigned(blocks)), dim3(kSqListThreads), 0, stream, a);
     return launched(who);
   });
-  return rc ? rc : zero_sum_partials(ws, h->first.back(), out, accumulate, stream);
+  return rc ? rc : zero_sum_partials(ws, done, out, accumulate, stream);
 }
 
 int launch_adamw(const zero_tensors_s* h, const void* const* grads, const StepConst& c, hipStream_t stream,
                  const char* who) {
-  return for_ranges(h, ZERO_TENSORS_PER_LAUNCH, [&](const ListRange& l) {
-    StepArgs a;
-    a.l = l;
-    a.c = c;
-    std::copy(grads + l.t0, grads + l.t0 + l.n, a.grads);
+  StepArgs a;
+  a.c = c;
+  return for_gradients(h, false, grads, &a, [&] {
     const bool wide = h->state_bits == 32, bf16 = h->grad_type == ZERO_BF16;
     if (h->param_type == ZERO_BF16)
       bf16 ? launch_step<uint16_t, uint16_t>(wide, a, stream) : launch_step<uint16_t, float>(wide, a, stream);
@@ -547,17 +923,26 @@ int launch_adamw(const zero_tensors_s* h, const void* const* grads, const StepCo
 
 int launch_state8(const zero_tensors_s* h, bool import, const float* const* m, const float* const* v,
                   hipStream_t stream, const char* who) {
-  return for_ranges(h, kStatePerLaunch, [&](const ListRange& l) {
-    State8Args a;
-    a.l = l;
-    std::copy(m + l.t0, m + l.t0 + l.n, a.m);
-    std::copy(v + l.t0, v + l.t0 + l.n, a.v);
-    if (import)
-      hipLaunchKernelGGL(tensors_import_kernel, list_grid(l), dim3(kListThreads), 0, stream, a);
-    else
-      hipLaunchKernelGGL(tensors_export_kernel, list_grid(l), dim3(kListThreads), 0, stream, a);
-    return launched(who);
-  });
+  State8Args a;
+  Window wm, wv;
+  const auto p = [](const float* const* x) { return reinterpret_cast<const void* const*>(x); };
+  return for_ranges(
+      h, false, kStatePerLaunch, [&] { wm = wv = Window(); },
+      [&](int32_t t) { return wm.take(m[t], 4) && wv.take(v[t], 4); },
+      [&](const ListRange& l) {
+        a.l = l;
+        wm.write(&a.m, p(m) + l.t0, l.n, 4);
+        wv.write(&a.v, p(v) + l.t0, l.n, 4);
+        if (import && split_units(l))
+          ZERO_LIST_LAUNCH(tensors_import_kernel<true>, true, a, stream);
+        else if (import)
+          ZERO_LIST_LAUNCH(tensors_import_kernel<false>, false, a, stream);
+        else if (split_units(l))
+          ZERO_LIST_LAUNCH(tensors_export_kernel<true>, true, a, stream);
+        else
+          ZERO_LIST_LAUNCH(tensors_export_kernel<false>, false, a, stream);
+        return launched(who);
+      });
 }
 
 }  // namespace zero

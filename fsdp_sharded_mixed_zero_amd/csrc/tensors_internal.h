@@ -17,17 +17,21 @@ namespace zero {
 constexpr int kUnitBlocks = 4;
 constexpr int kUnitElems = kUnitBlocks * ZERO_STATE8_BLOCK;
 
+// Elements that one wave of the norm takes.
+constexpr int kSqChunk = 4096;
+
 // The device table: first[n + 1], the running count of units (first[t] is the
-// first unit of tensor t, first[n] the total), padded to 16 bytes; then the n
-// records, as the caller described them.
-inline size_t table_records_at(int32_t n) { return (size_t(n) + 1 + 3) / 4 * 16; }
+// first unit of tensor t, first[n] the total), padded to 16 bytes; the same of
+// the norm's chunks; then the n records, as the caller described them.
+inline size_t table_chunks_at(int32_t n) { return (size_t(n) + 1 + 3) / 4 * 16; }
+inline size_t table_records_at(int32_t n) { return 2 * table_chunks_at(n); }
 inline size_t table_bytes(int32_t n) { return table_records_at(n) + size_t(n) * sizeof(zero_tensor); }
 
 }  // namespace zero
 
 struct zero_tensors_s {
   std::vector<zero_tensor> t;
-  std::vector<int32_t> first;
+  std::vector<int32_t> first, chunk;   // running counts of units and of chunks
   std::vector<std::pair<uintptr_t, uintptr_t>> owned;   // byte ranges of the list's buffers, sorted, disjoint
   int32_t param_type = 0, grad_type = 0, state_bits = 0;
   int32_t top_group = 0;      // the largest group in use

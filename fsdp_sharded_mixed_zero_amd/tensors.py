@@ -20,7 +20,7 @@ ZERO_BF16 = 0
 ZERO_F32 = 1
 ZERO_STATE8_BLOCK = 256         # elements of a tensor that share one scale (include/zero_tensors.h)
 ZERO_TENSOR_GROUPS = 8
-ZERO_TENSORS_PER_LAUNCH = 384   # gradient pointers one launch carries
+ZERO_TENSORS_PER_LAUNCH = 768   # tensors one launch carries
 
 
 class zero_tensor(ctypes.Structure):
@@ -65,6 +65,15 @@ def library():
 def state8_blocks(n: int) -> int:
     """Scales that a tensor of n elements needs for each of its 8-bit moments."""
     return -(-int(n) // ZERO_STATE8_BLOCK)
+
+
+def _stream(stream):
+    """As zero._stream; the current stream's handle by the short way (0.2 us
+    against 2.6 us for the stream object, of a call that takes 5)."""
+    if stream is not None:
+        return zero._stream(stream)
+    import torch
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _type_of(dtype, what):
@@ -166,7 +175,7 @@ def zero_tensors(param, m, v, master=None, m_scale=None, v_scale=None, group=Non
         nbytes = library().zero_tensors_table_bytes(h)
         lst.table = torch.empty((nbytes + 7) // 8, dtype=torch.int64, device=device)
         zero._check("zero_tensors_upload", library().zero_tensors_upload(
-            h, lst.table.data_ptr(), nbytes, zero._stream(stream)))
+            h, lst.table.data_ptr(), nbytes, _stream(stream)))
         if not torch.cuda.is_current_stream_capturing():
             torch.cuda.synchronize(device)
     return lst
@@ -185,7 +194,7 @@ def zero_tensors_upload(lst: TensorList, table, table_bytes: int | None = None, 
     if table_bytes is None:
         table_bytes = table.numel() * table.element_size()
     zero._check("zero_tensors_upload", library().zero_tensors_upload(
-        lst.handle, zero._ptr(table), table_bytes, zero._stream(stream)))
+        lst.handle, zero._ptr(table), table_bytes, _stream(stream)))
     lst.table = table
 
 
@@ -210,7 +219,7 @@ def zero_tensors_sqnorm(lst: TensorList, tensor_grads, out, accumulate: bool, wo
         ws_bytes = workspace.numel() * workspace.element_size()
     zero._check("zero_tensors_sqnorm", library().zero_tensors_sqnorm(
         lst.handle, arr, zero._ptr(out), 1 if accumulate else 0, zero._ptr(workspace), ws_bytes,
-        zero._stream(stream)))
+        _stream(stream)))
 
 
 def group_array(hp):
@@ -228,13 +237,13 @@ def zero_tensors_adamw_step(lst: TensorList, tensor_grads, hp, rank_sqnorms, n_r
     if n_ranks > 0:
         zero._need(rank_sqnorms, 8 * n_ranks, "rank sums of squares")
     zero._check("zero_tensors_adamw_step", library().zero_tensors_adamw_step(
-        lst.handle, arr, groups, len(groups), zero._ptr(rank_sqnorms), n_ranks, zero._stream(stream)))
+        lst.handle, arr, groups, len(groups), zero._ptr(rank_sqnorms), n_ranks, _stream(stream)))
 
 
 def _state8(name, lst, m, v, stream):
     import torch
     m, v = (_pointers(lst, x, torch.float32, what) for x, what in ((m, "m"), (v, "v")))
-    zero._check(name, getattr(library(), name)(lst.handle, m, v, zero._stream(stream)))
+    zero._check(name, getattr(library(), name)(lst.handle, m, v, _stream(stream)))
 
 
 def zero_tensors_state_import(lst: TensorList, m, v, stream=None):

@@ -44,9 +44,10 @@ extern "C" {
 /* Hyperparameter groups one list may have. */
 #define ZERO_TENSOR_GROUPS 8
 
-/* Gradient pointers that one launch carries in its arguments; a list of more
- * tensors takes several launches, one after another on the stream. */
-#define ZERO_TENSORS_PER_LAUNCH 384
+/* Tensors whose gradients one launch carries in its arguments. A list of more
+ * tensors takes several launches, one after another on the stream, and so does
+ * one whose gradients lie 2^32 elements or more apart. */
+#define ZERO_TENSORS_PER_LAUNCH 768
 
 /* One tensor of a list; device pointers.
  *   param    the parameter, bf16 or fp32 (the list's param_type); written by
