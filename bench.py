@@ -55,6 +55,11 @@ def parse():
     ap.add_argument("--flat", action="store_true",
                     help="ZeRO-1 flat buffers: gradients and parameters are views into flat buffers, the "
                          "shard is the rank's slice (no pack, no unpack)")
+    ap.add_argument("--per-tensor", action="store_true",
+                    help="the rank's slice as a list of tensors (zero_tensors_sqnorm, zero_tensors_adamw_step): "
+                         "gradients read and parameters written in place, no pack, no unpack")
+    ap.add_argument("--state-bits", type=int, choices=(32, 8), default=32,
+                    help="with --per-tensor: moments in fp32, or in 8 bits (e4m3, one scale per 256 elements)")
     ap.add_argument("--offload", action="store_true",
                     help="ZeRO-Offload: fp32 state in host memory, AdamW on the host cores")
     ap.add_argument("--offload-bucket", type=int, default=1 << 24, metavar="N",
@@ -90,8 +95,12 @@ def kernel_name(raw):
     return name.split("(")[0].split("::")[-1]
 
 
-def update_kernel(accum=1, separate_unpack=False, flat=False, state_arrays=False):
-    """The update kernel of a mode (the roofline's dominant kernel)."""
+def update_kernel(accum=1, separate_unpack=False, flat=False, state_arrays=False, list_bits=0):
+    """The update kernel of a mode (the roofline's dominant kernel).
+    ``list_bits``: 32 or 8 for the step over a list of tensors."""
+    if list_bits:
+        return ("tensors_adamw_kernel<unsigned short, unsigned short>" if list_bits == 32 else
+                "tensors_adamw8_kernel<unsigned short, unsigned short, false>")
     grad = "float" if accum > 1 else "unsigned short"
     if state_arrays:
         return f"adamw_arrays_vec_kernel<{grad}>"
@@ -105,16 +114,25 @@ def ceiling_elems(launch_bytes):
     return max(8, min(int(launch_bytes), 8 << 30) // 4 // 8 * 8)
 
 
-def algorithmic_bytes(wl, accum=1, separate_norm=False, flat=False, separate_unpack=False, state_arrays=False):
+def algorithmic_bytes(wl, accum=1, separate_norm=False, flat=False, separate_unpack=False, state_arrays=False,
+                      list_bits=0):
     """Algorithmic HBM bytes per step of each kernel over the whole shard, for
     the benchmark's mode (fused norm and fused unpack by default, separate
     norm, separate unpack, fp32 accumulation over ``accum`` micro-batches,
-    flat buffers, or three state arrays with the unpack separate)."""
+    flat buffers, three state arrays with the unpack separate, or a list of
+    tensors with moments of ``list_bits`` bits)."""
     from fsdp_sharded_mixed_zero_amd import zero
-    info = zero.zero_layout(wl.sizes, wl.n_d, wl.rank, wl.align).info
+    layout = zero.zero_layout(wl.sizes, wl.n_d, wl.rank, wl.align)
+    info = layout.info
     S = info["shard"]
     real = S - (info["pad_end"] - info["pad_begin"])
     pack = 4 * real + 2 * (S - real)
+    if list_bits:
+        from fsdp_sharded_mixed_zero_amd import tensors
+        blocks = sum(tensors.state8_blocks(s[3]) for s in layout.segments)
+        return S, real, {"tensors_sqnorm_kernel<unsigned short>": 2 * real,
+                         update_kernel(list_bits=list_bits): 28 * real if list_bits == 32
+                         else 16 * real + 16 * blocks}
     if flat:
         return S, real, {"sqnorm_partial_kernel": 2 * S, "adamw_vec_kernel<unsigned short>": 28 * S}
     separate_unpack = separate_unpack or state_arrays
@@ -283,7 +301,7 @@ def pmc_summary(fetch_dir, write_dir, wl, steps=20, warmup=2, separate_unpack=Fa
 
 
 def stats_summary(stats_dir, wl, steps, warmup, accum=1, separate_norm=False, flat=False, separate_unpack=False,
-                  state_arrays=False):
+                  state_arrays=False, list_bits=0):
     """Markdown table of the launches in a rocprofv3 kernel trace of this
     benchmark, with achieved bandwidth from each kernel's algorithmic bytes
     per launch (the step's bytes spread over that kernel's launches per
@@ -291,7 +309,7 @@ def stats_summary(stats_dir, wl, steps, warmup, accum=1, separate_norm=False, fl
     import csv
     import glob
 
-    S, real, algo = algorithmic_bytes(wl, accum, separate_norm, flat, separate_unpack, state_arrays)
+    S, real, algo = algorithmic_bytes(wl, accum, separate_norm, flat, separate_unpack, state_arrays, list_bits)
     # every launch from the trace, in time order; the set-up launches of the
     # sum-of-squares kernels (the other ranks' partial sums) left out
     spans = {}
@@ -325,7 +343,8 @@ def stats_summary(stats_dir, wl, steps, warmup, accum=1, separate_norm=False, fl
                              combine=accum == 1 and not separate_norm and not flat)
     mode = ((f" --accum {accum}" if accum > 1 else "") + (" --separate-norm" if separate_norm else "") +
             (" --flat" if flat else "") + (" --separate-unpack" if separate_unpack else "") +
-            (" --state-arrays" if state_arrays else ""))
+            (" --state-arrays" if state_arrays else "") +
+            (f" --per-tensor --state-bits {list_bits}" if list_bits else ""))
     lines = [f"# Kernel durations: {wl.name}, rank {wl.rank} of N_d={wl.n_d} "
              f"(shard {S} elements{f', buckets of {wl.bucket}' if wl.bucket else ''})", "",
              "Commands (one MI355X; R is the repository root):", "",
@@ -427,7 +446,9 @@ def single_launch_calls(rs, fused):
     """Whether every update call of the step is one kernel launch: its range
     is at most ZERO_ADAMW_LAUNCH_ELEMS elements and, for the update with the
     unpack fused, touches at most ZERO_PIECES_PER_LAUNCH tensor pieces."""
-    from fsdp_sharded_mixed_zero_amd import zero
+    from fsdp_sharded_mixed_zero_amd import tensors, zero
+    if hasattr(rs, "list"):
+        return len(rs.segments) <= tensors.ZERO_TENSORS_PER_LAUNCH
     for b, n in rs.pieces():
         if n > zero.ZERO_ADAMW_LAUNCH_ELEMS:
             return False
@@ -705,8 +726,8 @@ def main():
     if args.stats_summary:
         from fsdp_sharded_mixed_zero_amd import synth
         print(stats_summary(args.stats_summary, synth.WORKLOADS[args.workload], args.steps, args.warmup,
-                            args.accum, args.separate_norm, args.flat, args.separate_unpack, args.state_arrays),
-              end="")
+                            args.accum, args.separate_norm, args.flat, args.separate_unpack, args.state_arrays,
+                            args.state_bits if args.per_tensor else 0), end="")
         return
     if args.update_sweep:
         from fsdp_sharded_mixed_zero_amd import synth
@@ -723,8 +744,12 @@ def main():
     import torch
 
     from fsdp_sharded_mixed_zero_amd import synth, zero
-    from fsdp_sharded_mixed_zero_amd.rank import RankShard
+    from fsdp_sharded_mixed_zero_amd.rank import RankShard, TensorRank
 
+    if args.per_tensor and (args.accum > 1 or args.flat or args.offload or args.state_arrays):
+        sys.exit("--per-tensor is a mode of its own: no accumulation, flat buffers, offload or state arrays")
+    if args.state_bits != 32 and not args.per_tensor:
+        sys.exit("--state-bits 8 needs --per-tensor")
     zero.library()                       # fail loudly if the HIP library is missing
     wl = synth.WORKLOADS[args.workload]
     # the oracle legs run first, before this process touches the GPU, so the
@@ -738,8 +763,11 @@ def main():
     torch.cuda.set_device(0)
     if args.offload:
         return offload_main(args, wl)
-    rs = RankShard(wl, fused_norm=not args.separate_norm, accum_steps=args.accum, flat=args.flat,
-                   fused_unpack=not args.separate_unpack, state_arrays=args.state_arrays)
+    if args.per_tensor:
+        rs = TensorRank(wl, state_bits=args.state_bits)
+    else:
+        rs = RankShard(wl, fused_norm=not args.separate_norm, accum_steps=args.accum, flat=args.flat,
+                       fused_unpack=not args.separate_unpack, state_arrays=args.state_arrays)
     torch.cuda.synchronize()
 
     # Per-phase breakdown first, outside the timed region: events around every
@@ -798,7 +826,7 @@ def main():
     single = single_launch_calls(rs, rs.fused_unpack)
     bucketed, n_streams = rs.bucketed, rs.n_streams
     step_bytes = sum(algo.values())
-    default_kernel = rs.bucket <= 0 and args.accum == 1 and not args.flat
+    default_kernel = rs.bucket <= 0 and args.accum == 1 and not args.flat and not args.per_tensor
     traffic = (measured_traffic(wl.name, update_kernel(args.accum, args.separate_unpack, args.flat,
                                                        args.state_arrays))
                if default_kernel else None)
@@ -817,6 +845,8 @@ def main():
         "dtype": "f32",
         "data": "synthetic",
         "config": {"workload": f"{wl.name} rank {rs.rank} of N_d={wl.n_d}: one rank's shard, " + (
+                               "list of the slice's tensors: sum of squares -> clip+AdamW+bf16 cast in place"
+                               if args.per_tensor else
                                "ZeRO-1 flat buffers: sum of squares -> clip+AdamW+bf16 cast on the rank's slice"
                                if args.flat else
                                "pack + sum of squares -> clip+AdamW+bf16 cast over three state arrays (master, "
@@ -826,10 +856,12 @@ def main():
                    "shard_params": S, "n_d": wl.n_d, "rank": rs.rank, "tensors": len(wl.sizes),
                    "segments_in_shard": len(rs.segments), "adamw_step": wl.step,
                    "bucket": rs.bucket, "streams": rs.n_streams,
-                   "norm": "separate" if args.separate_norm or args.flat else "fused into pack",
+                   "norm": "separate" if args.separate_norm or args.flat or args.per_tensor else "fused into pack",
                    "unpack": ("none (flat buffers)" if args.flat else
+                              "none (parameters written in place)" if args.per_tensor else
                               "separate" if args.separate_unpack or args.state_arrays else "fused into AdamW"),
-                   "state": "three arrays" if args.state_arrays else "tiled (master|m|v in 8192-element tiles)",
+                   "state": f"tensor by tensor, moments in {args.state_bits} bits" if args.per_tensor else
+                            "three arrays" if args.state_arrays else "tiled (master|m|v in 8192-element tiles)",
                    "fp32_grad_accumulation_micro_batches": args.accum if args.accum > 1 else None},
         "adamw_params_per_s": call_elems / (call_ms * 1e-3),
         "step_GBps": round(step_bytes / (ms_per_step * 1e-3) / 1e9, 1),

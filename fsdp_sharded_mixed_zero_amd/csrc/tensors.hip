@@ -608,11 +608,11 @@ struct AdamW32 {
   }
 };
 
-template <typename P, typename G, bool SPLIT>
+template <typename P, typename G>
 __global__ __launch_bounds__(kListThreads) void tensors_adamw_kernel(const StepArgs a) {
-  const Unit w = my_unit<SPLIT>(a.l);
+  const Unit w = my_unit<true>(a.l);
   const G* g = a.grads.template at<const G>(w.t - a.l.t0);
-  if (g != nullptr) over_unit<SPLIT>(w, AdamW32<P, G>{a, w, g});
+  if (g != nullptr) over_unit<true>(w, AdamW32<P, G>{a, w, g});
 }
 
 // The 8-bit step of NB blocks from b0 on in one wave: all loads first, then
@@ -856,7 +856,7 @@ bool split_units(const ListRange& l) { return l.u1 - l.u0 <= kSplitUnits; }
 template <typename P, typename G>
 void launch_step(bool wide, const StepArgs& a, hipStream_t stream) {
   if (wide)
-    ZERO_LIST_LAUNCH((tensors_adamw_kernel<P, G, true>), true, a, stream);
+    ZERO_LIST_LAUNCH((tensors_adamw_kernel<P, G>), true, a, stream);
   else if (split_units(a.l))
     ZERO_LIST_LAUNCH((tensors_adamw8_kernel<P, G, true>), true, a, stream);
   else

@@ -27,6 +27,9 @@ With ``state_arrays=True`` the fp32 master, m and v are three separate
 arrays, the form the pages hold the state in ("第 5 课：ZeRO 与 FSDP" section
 2), updated by zero_adamw_step_arrays, with the unpack as its own pass.
 
+``TensorRank`` holds the rank's slice tensor by tensor instead of as one flat
+shard, with fp32 moments or moments in 8 bits.
+
 With ``flat=True`` the rank holds the ZeRO-1 form (notes on the ZeRO paper,
 section 4.1): the whole gradient and parameter sets live in two flat,
 padded buffers, every tensor is a view into them, and the shard is the rank's
@@ -39,7 +42,7 @@ from __future__ import annotations
 
 import torch
 
-from . import synth, zero
+from . import synth, tensors, zero
 
 
 def other_rank_slices(sizes, shard, rank):
@@ -415,6 +418,116 @@ class RankShard:
         else:
             out["unpack"] = 4 * self.real
         return out
+
+
+class TensorRank(RankShard):
+    """The rank's slice held tensor by tensor: the parts of the model's tensors
+    that the rank owns (the layout's segments) as one list, gradients read
+    and parameters written in place, so there is no pack, no unpack and no flat
+    bf16 shard. The norm is zero_tensors_sqnorm, the update
+    zero_tensors_adamw_step over fp32 masters and moments (``state_bits=32``)
+    or moments in 8 bits (``state_bits=8``: 6.06 instead of 12 bytes of state
+    per parameter; "第 5 课：ZeRO 与 FSDP" section 2 counts K = 12). Master and
+    moments are slices of shard-long arrays; padding is not part of the list.
+
+    ``groups``: hyperparameter sets (zero.hparams without the step's number) by
+    group index, and ``group_of(tensor)``: a tensor's group. By default one
+    group with the workload's hyperparameters."""
+
+    def __init__(self, wl: synth.Workload, rank: int | None = None, device="cuda", fill: bool = True,
+                 state_bits: int = 32, groups=None, group_of=None):
+        if state_bits not in (32, 8):
+            raise ValueError("state_bits is 32 or 8")
+        self.wl = wl
+        self.rank = wl.rank if rank is None else rank
+        self.device = dev = torch.device(device)
+        self.layout = zero.zero_layout(wl.sizes, wl.n_d, self.rank, wl.align)
+        self.info = self.layout.info
+        self.segments = self.layout.segments
+        self.shard = S = self.info["shard"]
+        self.real = S - (self.info["pad_end"] - self.info["pad_begin"])
+        if not self.segments:
+            raise ValueError("the rank's shard holds padding only: there is no tensor to update")
+        self.bucket, self.bucketed, self.n_streams, self.streams = 0, False, 1, []
+        self.flat, self.fused_norm, self.fused_unpack, self.accum_steps = False, False, False, 1
+        self.state, self.state_arrays, self.state_bits = None, True, state_bits
+        self.touched = sorted({s[0] for s in self.segments})
+        self.grads, self.params = [None] * len(wl.sizes), [None] * len(wl.sizes)
+        for i in self.touched:
+            self.grads[i] = torch.empty(wl.sizes[i], dtype=torch.bfloat16, device=dev)
+            self.params[i] = torch.full((wl.sizes[i],), synth.SENTINEL, dtype=torch.int16,
+                                        device=dev).view(torch.bfloat16)
+        self.rank_sq = torch.zeros(wl.n_d, dtype=torch.float64, device=dev)
+        self.master = torch.empty(S, dtype=torch.float32, device=dev)
+        lens = [n for _, _, _, n in self.segments]
+
+        def parts(flat):
+            return [flat[d:d + n] for _, _, d, n in self.segments]
+
+        self.m, self.v = (torch.zeros(S, dtype=torch.float32, device=dev) for _ in range(2))
+        m32, v32 = self.m, self.v
+        scales = {}
+        if state_bits == 8:
+            blocks = [tensors.state8_blocks(n) for n in lens]
+            self.m8, self.v8 = (torch.zeros(S, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)
+                                for _ in range(2))
+            self.m_scale, self.v_scale = (torch.zeros(sum(blocks), dtype=torch.float32, device=dev)
+                                          for _ in range(2))
+            scales = {"m_scale": list(self.m_scale.split(blocks)), "v_scale": list(self.v_scale.split(blocks))}
+        self.blocks = sum(tensors.state8_blocks(n) for n in lens)
+        self.groups = groups
+        self.list = tensors.zero_tensors(
+            [self.params[i][s:s + n] for i, s, _, n in self.segments],
+            parts(self.m8 if state_bits == 8 else self.m), parts(self.v8 if state_bits == 8 else self.v),
+            master=parts(self.master), group=None if group_of is None else [group_of(s[0]) for s in self.segments],
+            **scales)
+        self.grad_ptrs = zero.pointer_array([self.grads[i][s:s + n] for i, s, _, n in self.segments])
+        self.workspace = torch.empty(tensors.zero_tensors_sqnorm_workspace_bytes(self.list) // 8,
+                                     dtype=torch.float64, device=dev)
+        if fill:
+            self.fill_state()
+            self.fill_grads(wl.step)
+            self.fill_other_ranks()
+        if state_bits == 8:      # the fp32 moments were only there to be drawn and imported
+            if fill:
+                tensors.zero_tensors_state_import(self.list, parts(m32), parts(v32))
+                torch.cuda.synchronize(dev)
+            self.m = self.v = None
+
+    def step(self, step, stream=None, timing=None, events=None, before_micro=None, phases=None):
+        """One local step: the list's sum of squares, then the update. Arguments
+        as RankShard.step (phases "sqnorm" and "adamw")."""
+        wl = self.wl
+        if stream is None:
+            stream = torch.cuda.current_stream()
+        on = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+        hp = [self.hparams(step)] if self.groups is None else [zero.hparams(**{**g, "step": step})
+                                                                for g in self.groups]
+
+        def timed(phase, fn):
+            if timing is None or (phases is not None and phase not in phases):
+                fn()
+                return
+            e0 = next(events) if events is not None else torch.cuda.Event(enable_timing=True)
+            e1 = next(events) if events is not None else torch.cuda.Event(enable_timing=True)
+            e0.record(on)
+            fn()
+            e1.record(on)
+            timing.setdefault(phase, []).append((e0, e1))
+
+        timed("sqnorm", lambda: tensors.zero_tensors_sqnorm(
+            self.list, self.grad_ptrs, self.rank_sq[self.rank:self.rank + 1], False, self.workspace,
+            stream=on.cuda_stream))
+        timed("adamw", lambda: tensors.zero_tensors_adamw_step(
+            self.list, self.grad_ptrs, hp, self.rank_sq, wl.n_d, stream=on.cuda_stream))
+
+    def bytes_per_step(self):
+        """Algorithmic HBM bytes of one step: the norm reads 2 bytes per
+        element; the update reads the gradient (2) and writes the parameter
+        (2), and moves the master (8) and the moments (16, or 4 and 16 per
+        block of 256 with 8 bits) both ways."""
+        update = 28 * self.real if self.state_bits == 32 else 16 * self.real + 16 * self.blocks
+        return {"sqnorm": 2 * self.real, "adamw": update}
 
 
 class OffloadRank(RankShard):
