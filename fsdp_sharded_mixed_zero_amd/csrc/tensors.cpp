@@ -69,8 +69,7 @@ extern "C" int zero_tensors(const zero_tensor* tensors, int32_t n, int32_t param
     h->grad_type = grad_type;
     h->state_bits = state_bits;
     h->t.assign(tensors, tensors + n);
-    h->first.resize(size_t(n) + 1);
-    h->chunk.resize(size_t(n) + 1);
+    for (auto& f : h->first) f.resize(size_t(n) + 1);
     std::vector<Range> ranges;
     ranges.reserve(size_t(n) * 6);
     const bool wide = state_bits == 32, own_master = param_type == ZERO_F32;
@@ -78,8 +77,8 @@ extern "C" int zero_tensors(const zero_tensor* tensors, int32_t n, int32_t param
     int rc = ZERO_OK;
     for (int32_t i = 0; i < n && rc == ZERO_OK; ++i) {
       const zero_tensor& t = tensors[i];
-      h->first[size_t(i)] = int32_t(units);
-      h->chunk[size_t(i)] = int32_t(chunks);
+      h->first[0][size_t(i)] = int32_t(units);
+      h->first[1][size_t(i)] = int32_t(chunks);
       if (t.len < 0 || t.len > kMaxTotal || total + t.len > kMaxTotal) {
         rc = fail(ZERO_EINVAL, "%s: length %lld of tensor %d is below 0, or the total beyond 2^40", who,
                   (long long)t.len, i);
@@ -91,7 +90,8 @@ extern "C" int zero_tensors(const zero_tensor* tensors, int32_t n, int32_t param
       }
       h->top_group = std::max(h->top_group, t.group);
       total += t.len;
-      units += (t.len + zero::kUnitElems - 1) / zero::kUnitElems;
+      const int64_t lead = wide && t.len > 0 ? zero::line_phase(uintptr_t(own_master ? t.param : t.master)) : 0;
+      units += (lead + t.len + zero::kUnitElems - 1) / zero::kUnitElems;
       chunks += (t.len + zero::kSqChunk - 1) / zero::kSqChunk;
       if (t.len == 0) continue;
       if (own_master && t.master != nullptr)
@@ -116,8 +116,10 @@ extern "C" int zero_tensors(const zero_tensor* tensors, int32_t n, int32_t param
         ranges.push_back({uintptr_t(b.p), uintptr_t(b.p) + b.bytes, i});
       }
     }
-    h->first[size_t(n)] = int32_t(units);
-    h->chunk[size_t(n)] = int32_t(chunks);
+    h->first[0][size_t(n)] = int32_t(units);
+    h->first[1][size_t(n)] = int32_t(chunks);
+    for (int k = 0; k < 2; ++k)
+      while (((int64_t(h->first[k].back()) - 1) >> h->shift[k]) >= zero::kSlots) ++h->shift[k];
     if (rc == ZERO_OK) {
       std::sort(ranges.begin(), ranges.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
       for (size_t k = 0; k + 1 < ranges.size() && rc == ZERO_OK; ++k)
@@ -146,7 +148,7 @@ extern "C" int zero_tensors(const zero_tensor* tensors, int32_t n, int32_t param
 extern "C" void zero_tensors_free(zero_tensors_t h) { delete h; }
 
 extern "C" size_t zero_tensors_table_bytes(zero_tensors_t h) {
-  return h == nullptr ? 0 : zero::table_bytes(int32_t(h->t.size()));
+  return h == nullptr ? 0 : zero::Table(int32_t(h->t.size())).bytes;
 }
 
 extern "C" int zero_tensors_upload(zero_tensors_t h, void* d_table, size_t bytes, hipStream_t stream) {
@@ -169,7 +171,7 @@ extern "C" int zero_tensors_upload(zero_tensors_t h, void* d_table, size_t bytes
 }
 
 extern "C" size_t zero_tensors_sqnorm_workspace_bytes(zero_tensors_t h) {
-  return h == nullptr ? 0 : std::max<size_t>(1, size_t(h->chunk.back())) * sizeof(double);
+  return h == nullptr ? 0 : std::max<size_t>(1, size_t(h->first[1].back())) * sizeof(double);
 }
 
 extern "C" int zero_tensors_sqnorm(zero_tensors_t h, const void* const* grads, double* d_out, int32_t accumulate,

@@ -28,12 +28,14 @@ constexpr int kSqListWaves = 4, kSqListThreads = 64 * kSqListWaves;
 constexpr int64_t kListMaxUnits = int64_t(1) << 23;     // units per launch: at most 2^31 work-items
 
 // What a launch covers: units [u0, u1) (chunks, for the norm), which lie in
-// tensors [t0, t0 + n); first[t]: tensor t's first one.
+// tensors [t0, t0 + n); first[t]: tensor t's first one; slot: where the search
+// for unit u begins, at u >> shift.
 struct ListRange {
-  const int32_t* first;
+  const int32_t *first, *slot;
   const zero_tensor* rec;
   int32_t t0, n;
   int32_t u0, u1;
+  int32_t n_all, shift;
 };
 
 // Addresses of a launch's N tensors: element-size steps from the lowest one,
@@ -76,36 +78,34 @@ struct UploadArgs {
   int32_t n;
   uint32_t w[kUploadWords];
 };
-static_assert(sizeof(SqArgs) <= 4096 && sizeof(StepArgs) <= 4096 && sizeof(State8Args) <= 4096 &&
-                  sizeof(UploadArgs) <= 4096,
+static_assert(sizeof(SqArgs) <= 4096 && sizeof(StepArgs) <= 4096 &&
+                  sizeof(State8Args) <= 4096 && sizeof(UploadArgs) <= 4096,
               "kernel arguments fit the 4 KiB segment");
 
 // ------------------------------------------------------- finding the tensor
-
-// The tensor that holds unit u, the last t of the launch with first[t] <= u,
-// and in *start its first unit. Each round the 64 lanes probe 64 evenly spaced
-// entries and count those at or below u (the counts ascend), so 768 tensors
-// take two rounds.
-__device__ __forceinline__ int find_tensor(const int32_t* first, int t0, int n, int u, int* start) {
-  int lo = t0, span = n, at_lo;
-  const int lane = threadIdx.x & 63;
-  do {
-    const int stride = (span + 63) >> 6, k = lane * stride;
-    const int x = k < span ? first[lo + k] : 0x7FFFFFFF;
-    const int lanes = __popcll(__ballot(x <= u)) - 1;
-    at_lo = __builtin_amdgcn_readlane(x, lanes);
-    lo += lanes * stride;
-    span = span - lanes * stride < stride ? span - lanes * stride : stride;
-  } while (span > 1);
-  *start = at_lo;
-  return __builtin_amdgcn_readfirstlane(lo);
-}
 
 // A value at a wave-uniform address that the kernel does not write, read by a
 // scalar load (the compiler cannot know that the stores leave it alone).
 template <typename T>
 __device__ __forceinline__ T uniform_load(const T* p) {
   return *(const __attribute__((address_space(4))) T*)p;
+}
+
+// The tensor that holds unit u, the last t with first[t] <= u, and in *start
+// its first unit. The 64 lanes compare 64 consecutive entries, from the slot's
+// tensor on, as often as all of them are at or below u (the counts ascend).
+// (64 entries spaced over a launch's tensors, then the rest between two of them,
+// touch a cache line a lane: the 32-bit step over 868 tensors 544 us against 535.)
+__device__ __forceinline__ int find_tensor(const ListRange& l, int u, int* start) {
+  int lo = l.n_all <= 64 ? 0 : uniform_load(l.slot + (u >> l.shift));
+  const int lane = threadIdx.x & 63;
+  for (;;) {
+    const int x = lo + lane <= l.n_all ? l.first[lo + lane] : 0x7FFFFFFF;
+    const int below = __popcll(__ballot(x <= u));   // at least 1; lane 63's entry is the next round's first
+    *start = __builtin_amdgcn_readlane(x, below - 1);
+    if (below < 64) return __builtin_amdgcn_readfirstlane(lo + below - 1);
+    lo += 63;
+  }
 }
 
 // What a wave works on: its tensor, its unit's first element, how many elements
@@ -124,7 +124,7 @@ __device__ __forceinline__ Unit my_unit(const ListRange& l) {
   Unit w;
   w.block = SPLIT ? int(blockIdx.x & 3) : 0;
   int start;
-  w.t = find_tensor(l.first, l.t0, l.n, u, &start);
+  w.t = find_tensor(l, u, &start);
   w.base = int64_t(u - start) * kUnitElems;
   w.rest = uniform_load(&l.rec[w.t].len) - w.base;
   return w;
@@ -217,6 +217,36 @@ __device__ __forceinline__ void store4(uint8_t* p, int cnt, uint32_t w) {
 #pragma unroll
     for (int k = 0; k < 3; ++k)
       if (k < cnt) p[k] = uint8_t(w >> (8 * k));
+  }
+}
+
+// The same of the elements [lo, cnt) of the four at p: lo > 0 where a unit
+// begins before its tensor.
+template <typename T>
+__device__ __forceinline__ auto load4(const T* p, int lo, int cnt) {
+  auto x = load4(p, lo == 0 ? cnt : 0);
+  if (lo != 0) {
+#pragma unroll
+    for (int k = 1; k < 4; ++k) {
+      if (k < lo || k >= cnt) continue;
+      if constexpr (sizeof(T) == 2) x[k >> 1] |= uint32_t(p[k]) << (16 * (k & 1));
+      else x[k] = p[k];
+    }
+  }
+  return x;
+}
+
+template <typename T>
+__device__ __forceinline__ void store4(T* p, int lo, int cnt, f32x4 x) {
+  if (lo == 0) {
+    store4(p, cnt, x);
+  } else {
+#pragma unroll
+    for (int k = 1; k < 4; ++k) {
+      if (k < lo || k >= cnt) continue;
+      if constexpr (sizeof(T) == 2) p[k] = to_bf16(x[k]);
+      else p[k] = x[k];
+    }
   }
 }
 
@@ -462,7 +492,7 @@ __global__ __launch_bounds__(kSqListThreads) void tensors_sqnorm_kernel(const Sq
   double acc = 0.0;
   if (u < a.l.u1) {
     int start;
-    const int t = find_tensor(a.l.first, a.l.t0, a.l.n, __builtin_amdgcn_readfirstlane(int(u)), &start);
+    const int t = find_tensor(a.l, __builtin_amdgcn_readfirstlane(int(u)), &start);
     const int64_t base = (u - start) * kSqChunk;
     const G* g = a.grads.template at<const G>(t - a.l.t0);
     SqChunk<G> x;
@@ -554,84 +584,82 @@ __device__ __forceinline__ void over_unit(const Unit& w, const W& work) {
   }
 }
 
-// The 32-bit step of NB blocks from b0 on in one wave: all loads first.
-// P: uint16_t (bf16 parameters and an fp32 master) or float (its own master).
-template <typename P, typename G>
-struct AdamW32 {
-  const StepArgs& a;
-  const Unit& w;
-  const G* grad;
-
-  template <int NB>
-  __device__ __forceinline__ void run(int b0) const {
-    const zero_tensor* r = a.l.rec + w.t;
-    const int64_t e = w.base + b0 * kBlock + 4 * int(threadIdx.x & 63);
-    P* param = static_cast<P*>(uniform_load(&r->param)) + e;
-    float* master = sizeof(P) == 4 ? reinterpret_cast<float*>(param) : uniform_load(&r->master) + e;
-    float *ms = static_cast<float*>(uniform_load(&r->m)) + e, *vs = static_cast<float*>(uniform_load(&r->v)) + e;
-    const G* g = grad + e;
-    const int cnt = NB > 1 ? 4 : count4(w.rest - b0 * kBlock);
-    decltype(load4(g, 4)) g4[NB];
-    f32x4 p4[NB], m4[NB], v4[NB];
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      g4[b] = load4(g + b * kBlock, cnt);
-      p4[b] = load4(master + b * kBlock, cnt);
-      m4[b] = load4(ms + b * kBlock, cnt);
-      v4[b] = load4(vs + b * kBlock, cnt);
-    }
-    const int group = uniform_load(&r->group);
-    const GroupConst& k = a.c.g[group];
-    AdamWArgs q{};
-    q.beta1 = k.beta1, q.omb1 = k.omb1, q.beta2 = k.beta2, q.omb2 = k.omb2;
-    q.lr_wd = k.lr_wd, q.step_size = k.step_size, q.inv_sqrt_bc2 = k.inv_sqrt_bc2, q.eps = k.eps;
-    const double c64 = list_clip(a.c);
-    const float c = float(c64);
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const f32x4 gw = widen(g4[b]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float p1, m1, v1;
-        float p = p4[b][i], m = m4[b][i], v = v4[b][i];
-        if (adamw_fast(q, c, gw[i], p, m, v, p1, m1, v1)) {
-          exact_update(a.c.x[group], c64, gw[i], p, m, v);
-          p1 = p, m1 = m, v1 = v;
-        }
-        p4[b][i] = p1, m4[b][i] = m1, v4[b][i] = v1;
-      }
-      store4(master + b * kBlock, cnt, p4[b]);
-      store4(ms + b * kBlock, cnt, m4[b]);
-      store4(vs + b * kBlock, cnt, v4[b]);
-      if constexpr (sizeof(P) == 2) store4(param + b * kBlock, cnt, p4[b]);
-    }
-  }
-};
-
+// The 32-bit step, one wave to a block of 256 elements. P: uint16_t (bf16
+// parameters and an fp32 master) or float (its own master). The blocks lie by
+// the master's 128-byte lines (line_phase): with blocks by the tensor's first
+// element, waves on different XCDs write parts of the same lines, and tensors
+// packed without gaps take 730 us instead of 555 for 119 M elements.
 template <typename P, typename G>
 __global__ __launch_bounds__(kListThreads) void tensors_adamw_kernel(const StepArgs a) {
   const Unit w = my_unit<true>(a.l);
+  const zero_tensor* r = a.l.rec + w.t;
+  P* param = static_cast<P*>(uniform_load(&r->param));
+  float* master = sizeof(P) == 4 ? reinterpret_cast<float*>(param) : uniform_load(&r->master);
+  const int lead = zero::line_phase(uintptr_t(master));
+  const int64_t e0 = w.base + w.block * kBlock - lead, rest = w.base + w.rest - e0;   // the block's first element
   const G* g = a.grads.template at<const G>(w.t - a.l.t0);
-  if (g != nullptr) over_unit<true>(w, AdamW32<P, G>{a, w, g});
+  if (g == nullptr || rest <= 0) return;
+  const int lane = threadIdx.x & 63;
+  const int64_t e = e0 + 4 * lane;
+  const int lo = e < 0 ? e > -4 ? int(-e) : 4 : 0, cnt = e <= -4 ? 0 : count4(rest);
+  float *ms = static_cast<float*>(uniform_load(&r->m)) + e, *vs = static_cast<float*>(uniform_load(&r->v)) + e;
+  g += e;
+  param += e;
+  master += e;
+  const f32x4 g4 = widen(load4(g, lo, cnt));
+  f32x4 p4 = load4(master, lo, cnt), m4 = load4(ms, lo, cnt), v4 = load4(vs, lo, cnt);
+  const int group = uniform_load(&r->group);
+  const GroupConst& k = a.c.g[group];
+  AdamWArgs q{};
+  q.beta1 = k.beta1, q.omb1 = k.omb1, q.beta2 = k.beta2, q.omb2 = k.omb2;
+  q.lr_wd = k.lr_wd, q.step_size = k.step_size, q.inv_sqrt_bc2 = k.inv_sqrt_bc2, q.eps = k.eps;
+  const double c64 = list_clip(a.c);
+  const float c = float(c64);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float p1, m1, v1;
+    float p = p4[i], m = m4[i], v = v4[i];
+    if (adamw_fast(q, c, g4[i], p, m, v, p1, m1, v1)) {
+      exact_update(a.c.x[group], c64, g4[i], p, m, v);
+      p1 = p, m1 = m, v1 = v;
+    }
+    p4[i] = p1, m4[i] = m1, v4[i] = v1;
+  }
+  store4(master, lo, cnt, p4);
+  store4(ms, lo, cnt, m4);
+  store4(vs, lo, cnt, v4);
+  if constexpr (sizeof(P) == 2) store4(param, lo, cnt, p4);
 }
+
+// A value loaded once more: the address passes through an empty asm statement,
+// so the compiler cannot keep what was loaded from it before.
+template <typename T>
+__device__ __forceinline__ T reload(const T* p) {
+  asm volatile("" : "+v"(p));
+  return *(const ZERO_GLOBAL T*)p;
+}
+
+__device__ __forceinline__ float grad_value(uint16_t g) { return __uint_as_float(uint32_t(g) << 16); }
+__device__ __forceinline__ float grad_value(float g) { return g; }
 
 // The 8-bit step of NB blocks from b0 on in one wave: all loads first, then
 // the moments in fp64, the blocks' maxima together, then block by block the
 // bytes and the update.
 template <typename P, typename G>
 struct AdamW8 {
-  const StepArgs& a;
+  const ListRange& l;
+  const StepConst& step;
   const Unit& w;
   const G* grad;
 
   template <int NB>
   __device__ __forceinline__ void run(int b0) const {
     const int lane = threadIdx.x & 63;
-    const zero_tensor* r = a.l.rec + w.t;
+    const zero_tensor* r = l.rec + w.t;
     const int64_t e = w.base + b0 * kBlock + 4 * lane;
     P* param = static_cast<P*>(uniform_load(&r->param)) + e;
     float* master = sizeof(P) == 4 ? reinterpret_cast<float*>(param) : uniform_load(&r->master) + e;
-    const State8 st = state8_of(a.l, w, b0);
+    const State8 st = state8_of(l, w, b0);
     const G* g = grad + e;
     const int cnt = NB > 1 ? 4 : count4(w.rest - b0 * kBlock);
     decltype(load4(g, 4)) g4[NB];
@@ -646,9 +674,9 @@ struct AdamW8 {
     }
     const float old = old_scales<NB>(st);
     const int group = uniform_load(&r->group);
-    const GroupConst& k = a.c.g[group];
-    const zero::AdamWExact& x = a.c.x[group];
-    const double c = list_clip(a.c), c1 = x.omb1 * c, c2 = x.omb2 * (c * c);
+    const GroupConst& k = step.g[group];
+    const zero::AdamWExact& x = step.x[group];
+    const double c = list_clip(step), c1 = x.omb1 * c, c2 = x.omb2 * (c * c);
     // beta1 * M * scale + (1 - beta1) * c * g and beta2 * (S * scale)^2 + (1 - beta2) * (c * g)^2
     const auto first = [&](int b, float value, float gk) {
       const double scaled = x.beta1 * double(lane_f32(old, b));
@@ -672,9 +700,17 @@ struct AdamW8 {
     const Scales s = block_scales<NB>(mf, vf, st.m_scale, st.v_scale, st.block0, st.n_blocks);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      // an element's moments again in fp64, where a byte hangs on them
-      const auto exact_m = [&](int j) { return first(b, e4m3_value((m8[b] >> (8 * j)) & 0xFFu), pick(widen(g4[b]), j)); };
-      const auto exact_v = [&](int j) { return second(b, e4m3_value((s8[b] >> (8 * j)) & 0xFFu), pick(widen(g4[b]), j)); };
+      // An element's moments again in fp64, where a byte hangs on them: from
+      // memory, so that the gradients and bytes need no registers until here
+      // (16 to 24 of 150, and with them the fourth wave of a SIMD).
+      const auto exact_m = [&](int j) {
+        const int at = b * kBlock + j;
+        return j < cnt ? first(b, e4m3_value(reload(st.m + at)), grad_value(reload(g + at))) : 0.0;
+      };
+      const auto exact_v = [&](int j) {
+        const int at = b * kBlock + j;
+        return j < cnt ? second(b, e4m3_value(reload(st.v + at)), grad_value(reload(g + at))) : 0.0;
+      };
       const uint32_t mb = m_bytes(mf[b], lane_f32(s.up, lane_of(b, 0)), exact_m);
       float y[4];
       const uint32_t vb = v_bytes(vf[b], lane_f32(s.up, lane_of(b, 1)), y, exact_v);
@@ -697,7 +733,7 @@ template <typename P, typename G, bool SPLIT>
 __global__ __launch_bounds__(kListThreads) void tensors_adamw8_kernel(const StepArgs a) {
   const Unit w = my_unit<SPLIT>(a.l);
   const G* g = a.grads.template at<const G>(w.t - a.l.t0);
-  if (g != nullptr) over_unit<SPLIT>(w, AdamW8<P, G>{a, w, g});
+  if (g != nullptr) over_unit<SPLIT>(w, AdamW8<P, G>{a.l, a.c, w, g});
 }
 
 struct Import8 {
@@ -812,18 +848,23 @@ struct Window {
 template <typename R, typename F, typename Go>
 int for_ranges(const zero_tensors_s* h, bool chunks, int most, R restart, F fits, Go go) {
   const int32_t n = int32_t(h->t.size());
-  const std::vector<int32_t>& counts = chunks ? h->chunk : h->first;
-  const int32_t* first = reinterpret_cast<const int32_t*>(static_cast<const char*>(h->table) +
-                                                          (chunks ? zero::table_chunks_at(n) : 0));
-  const zero_tensor* rec =
-      reinterpret_cast<const zero_tensor*>(static_cast<const char*>(h->table) + zero::table_records_at(n));
+  const zero::Table at(n);
+  const char* table = static_cast<const char*>(h->table);
+  const int kind = chunks ? 1 : 0;
+  const std::vector<int32_t>& counts = h->first[kind];
+  ListRange l;
+  l.first = reinterpret_cast<const int32_t*>(table + at.first[kind]);
+  l.slot = reinterpret_cast<const int32_t*>(table + at.slot[kind]);
+  l.rec = reinterpret_cast<const zero_tensor*>(table + at.records);
+  l.n_all = n;
+  l.shift = h->shift[kind];
   for (int32_t t0 = 0; t0 < n;) {
     restart();
     int32_t t1 = t0;
     while (t1 < n && t1 - t0 < most && (h->t[size_t(t1)].len == 0 || fits(t1))) ++t1;
     const int64_t end = counts[size_t(t1)];
     for (int64_t u = counts[size_t(t0)]; u < end; u += kListMaxUnits) {
-      const ListRange l{first, rec, t0, t1 - t0, int32_t(u), int32_t(std::min(end, u + kListMaxUnits))};
+      l.t0 = t0, l.n = t1 - t0, l.u0 = int32_t(u), l.u1 = int32_t(std::min(end, u + kListMaxUnits));
       if (int rc = go(l)) return rc;
     }
     t0 = t1;
@@ -831,7 +872,7 @@ int for_ranges(const zero_tensors_s* h, bool chunks, int most, R restart, F fits
   return zero::ok();
 }
 
-// for_ranges over the gradients' addresses, which go into args.grads.
+// for_ranges over the gradients' addresses, which go into args->grads.
 template <typename A, typename Go>
 int for_gradients(const zero_tensors_s* h, bool chunks, const void* const* grads, A* args, Go go) {
   const size_t size = h->grad_type == ZERO_BF16 ? 2 : 4;
@@ -849,18 +890,43 @@ int for_gradients(const zero_tensors_s* h, bool chunks, const void* const* grads
 constexpr int64_t kSplitUnits = 1024;
 bool split_units(const ListRange& l) { return l.u1 - l.u0 <= kSplitUnits; }
 
-// Launches kernel(args): one wave per unit, or with `split` four.
-#define ZERO_LIST_LAUNCH(kernel, split, args, stream) \
-  hipLaunchKernelGGL((kernel), dim3(unsigned((args).l.u1 - (args).l.u0) * ((split) ? 4u : 1u)), dim3(kListThreads), 0, stream, args)
+// Launches kernel(args): one wave per unit, or with `split` four. lds: bytes of
+// LDS a block asks for (and does not use), which limits the waves of a CU.
+#define ZERO_LIST_LAUNCH(kernel, split, lds, args, stream)                                                          \
+  hipLaunchKernelGGL((kernel), dim3(unsigned((args).l.u1 - (args).l.u0) * ((split) ? 4u : 1u)), dim3(kListThreads), \
+                     lds, stream, args)
+
+// LDS of the conversions' blocks, against too many waves in flight: with
+// 10 KiB, 16 to a CU, the import takes 195 us instead of 204 (119 M elements)
+// and the export the same 194; with fp32 arrays that do not start on 128-byte
+// lines, whose ends two waves write, the export takes 45.5 us with 16 KiB
+// against 50.4 (24.3 M; 215 us against 194 on lines).
+constexpr unsigned kConvertLds = 10 << 10, kConvertLdsOffLines = 16 << 10;
+
+// The same of the 32-bit step's: 20 waves to a CU instead of 32 (119 M elements,
+// bf16 gradients 527 us without and 520 us, fp32 569 and 560; 24.3 M, 111.5 and
+// 110.3).
+constexpr unsigned kStep32Lds = 8 << 10;
+
+// LDS of the 8-bit step's blocks in long launches, against too many waves in
+// flight. By the kernel's registers a CU holds 20; 12 (13 KiB) with bf16
+// gradients and 10 (16 KiB) with fp32 ones are faster from some 2^26 elements
+// on: 105 M, 284 us without and 277 us, 323 and 307; 119 M, 330 and 324, 377
+// and 359; but 47 M, 138.4 and 139.8, 154.1 and 156.1.
+constexpr int64_t kLongUnits = int64_t(1) << 16;
+template <typename G>
+unsigned step8_lds(const ListRange& l) {
+  return l.u1 - l.u0 <= kLongUnits ? 0u : sizeof(G) == 2 ? 13u << 10 : 16u << 10;
+}
 
 template <typename P, typename G>
 void launch_step(bool wide, const StepArgs& a, hipStream_t stream) {
   if (wide)
-    ZERO_LIST_LAUNCH((tensors_adamw_kernel<P, G>), true, a, stream);
+    ZERO_LIST_LAUNCH((tensors_adamw_kernel<P, G>), true, kStep32Lds, a, stream);
   else if (split_units(a.l))
-    ZERO_LIST_LAUNCH((tensors_adamw8_kernel<P, G, true>), true, a, stream);
+    ZERO_LIST_LAUNCH((tensors_adamw8_kernel<P, G, true>), true, 0, a, stream);
   else
-    ZERO_LIST_LAUNCH((tensors_adamw8_kernel<P, G, false>), false, a, stream);
+    ZERO_LIST_LAUNCH((tensors_adamw8_kernel<P, G, false>), false, step8_lds<G>(a.l), a, stream);
 }
 
 }  // namespace
@@ -875,15 +941,23 @@ int current_device(int* dev, const char* who) {
 
 int launch_upload(const zero_tensors_s* h, void* table, hipStream_t stream, const char* who) {
   const int32_t n = int32_t(h->t.size());
-  std::vector<uint32_t> words(table_bytes(n) / 4, 0u);
-  std::memcpy(words.data(), h->first.data(), h->first.size() * sizeof(int32_t));
-  std::memcpy(words.data() + table_chunks_at(n) / 4, h->chunk.data(), h->chunk.size() * sizeof(int32_t));
-  std::memcpy(words.data() + table_records_at(n) / 4, h->t.data(), h->t.size() * sizeof(zero_tensor));
-  for (size_t at = 0; at < words.size(); at += kUploadWords) {
+  const Table at(n);
+  std::vector<uint32_t> words(at.bytes / 4, 0u);
+  for (int k = 0; k < 2; ++k) {
+    const std::vector<int32_t>& first = h->first[k];
+    std::memcpy(words.data() + at.first[k] / 4, first.data(), first.size() * sizeof(int32_t));
+    int32_t t = 0;
+    for (int64_t s = 0; s < kSlots && (s << h->shift[k]) < first.back(); ++s) {
+      while (first[size_t(t) + 1] <= (s << h->shift[k])) ++t;
+      words[at.slot[k] / 4 + size_t(s)] = uint32_t(t);
+    }
+  }
+  std::memcpy(words.data() + at.records / 4, h->t.data(), h->t.size() * sizeof(zero_tensor));
+  for (size_t w = 0; w < words.size(); w += kUploadWords) {
     UploadArgs a;
-    a.dst = static_cast<uint32_t*>(table) + at;
-    a.n = int32_t(std::min<size_t>(kUploadWords, words.size() - at));
-    std::memcpy(a.w, words.data() + at, size_t(a.n) * 4);
+    a.dst = static_cast<uint32_t*>(table) + w;
+    a.n = int32_t(std::min<size_t>(kUploadWords, words.size() - w));
+    std::memcpy(a.w, words.data() + w, size_t(a.n) * 4);
     hipLaunchKernelGGL(tensors_upload_kernel, dim3(1), dim3(256), 0, stream, a);
     if (int rc = launched(who)) return rc;
   }
@@ -893,22 +967,22 @@ int launch_upload(const zero_tensors_s* h, void* table, hipStream_t stream, cons
 int launch_sqnorm(const zero_tensors_s* h, const void* const* grads, double* out, int32_t accumulate, double* ws,
                   hipStream_t stream, const char* who) {
   SqArgs a;
-  int64_t done = 0;   // partial sums written
+  int64_t n = 0;   // partial sums written
   const int rc = for_gradients(h, true, grads, &a, [&] {
     const int64_t chunks = a.l.u1 - a.l.u0, blocks = (chunks + kSqListWaves - 1) / kSqListWaves;
-    a.partial = ws + done;
-    done += blocks;
+    a.partial = ws + n;
+    n += blocks;
     if (h->grad_type == ZERO_BF16)
       hipLaunchKernelGGL(tensors_sqnorm_kernel<uint16_t>, dim3(unsigned(blocks)), dim3(kSqListThreads), 0, stream, a);
     else
       hipLaunchKernelGGL(tensors_sqnorm_kernel<float>, dim3(unsigned(blocks)), dim3(kSqListThreads), 0, stream, a);
     return launched(who);
   });
-  return rc ? rc : zero_sum_partials(ws, done, out, accumulate, stream);
+  return rc ? rc : zero_sum_partials(ws, n, out, accumulate, stream);
 }
 
 int launch_adamw(const zero_tensors_s* h, const void* const* grads, const StepConst& c, hipStream_t stream,
-                 const char* who) {
+                   const char* who) {
   StepArgs a;
   a.c = c;
   return for_gradients(h, false, grads, &a, [&] {
@@ -922,25 +996,30 @@ int launch_adamw(const zero_tensors_s* h, const void* const* grads, const StepCo
 }
 
 int launch_state8(const zero_tensors_s* h, bool import, const float* const* m, const float* const* v,
-                  hipStream_t stream, const char* who) {
+                    hipStream_t stream, const char* who) {
   State8Args a;
   Window wm, wv;
+  uintptr_t low = 0;
   const auto p = [](const float* const* x) { return reinterpret_cast<const void* const*>(x); };
   return for_ranges(
-      h, false, kStatePerLaunch, [&] { wm = wv = Window(); },
-      [&](int32_t t) { return wm.take(m[t], 4) && wv.take(v[t], 4); },
+      h, false, kStatePerLaunch, [&] { wm = wv = Window(), low = 0; },
+      [&](int32_t t) {
+        low |= uintptr_t(m[t]) | uintptr_t(v[t]);
+        return wm.take(m[t], 4) && wv.take(v[t], 4);
+      },
       [&](const ListRange& l) {
         a.l = l;
         wm.write(&a.m, p(m) + l.t0, l.n, 4);
         wv.write(&a.v, p(v) + l.t0, l.n, 4);
+        const unsigned lds = import || low % 128 == 0 ? kConvertLds : kConvertLdsOffLines;
         if (import && split_units(l))
-          ZERO_LIST_LAUNCH(tensors_import_kernel<true>, true, a, stream);
+          ZERO_LIST_LAUNCH(tensors_import_kernel<true>, true, 0, a, stream);
         else if (import)
-          ZERO_LIST_LAUNCH(tensors_import_kernel<false>, false, a, stream);
+          ZERO_LIST_LAUNCH(tensors_import_kernel<false>, false, lds, a, stream);
         else if (split_units(l))
-          ZERO_LIST_LAUNCH(tensors_export_kernel<true>, true, a, stream);
+          ZERO_LIST_LAUNCH(tensors_export_kernel<true>, true, 0, a, stream);
         else
-          ZERO_LIST_LAUNCH(tensors_export_kernel<false>, false, a, stream);
+          ZERO_LIST_LAUNCH(tensors_export_kernel<false>, false, lds, a, stream);
         return launched(who);
       });
 }

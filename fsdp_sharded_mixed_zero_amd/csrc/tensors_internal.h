@@ -17,21 +17,44 @@ namespace zero {
 constexpr int kUnitBlocks = 4;
 constexpr int kUnitElems = kUnitBlocks * ZERO_STATE8_BLOCK;
 
+// With a 32-bit state the units of a tensor begin up to 31 elements before it, so
+// that its fp32 masters fall into units (and waves) by whole 128-byte lines:
+// the elements between such a line's start and the first master.
+constexpr int kLineElems = 32;
+constexpr int line_phase(uintptr_t master) { return int((master >> 2) & (kLineElems - 1)); }
+
 // Elements that one wave of the norm takes.
 constexpr int kSqChunk = 4096;
 
+// Slots of a running count: runs of 2^shift units, as many as kSlots of them;
+// slot[s] is the tensor that holds unit s << shift, where a search begins.
+constexpr int kSlots = 2048;
+
 // The device table: first[n + 1], the running count of units (first[t] is the
-// first unit of tensor t, first[n] the total), padded to 16 bytes; the same of
-// the norm's chunks; then the n records, as the caller described them.
-inline size_t table_chunks_at(int32_t n) { return (size_t(n) + 1 + 3) / 4 * 16; }
-inline size_t table_records_at(int32_t n) { return 2 * table_chunks_at(n); }
-inline size_t table_bytes(int32_t n) { return table_records_at(n) + size_t(n) * sizeof(zero_tensor); }
+// first unit of tensor t, first[n] the total), and its slots; the same two of
+// the norm's chunks; then the n records, as the caller described them. Each
+// part starts at a multiple of 16 bytes.
+struct Table {
+  size_t first[2], slot[2], records, bytes;   // byte offsets; [0] units, [1] chunks
+  explicit Table(int32_t n) {
+    size_t at = 0;
+    for (int k = 0; k < 2; ++k) {
+      first[k] = at;
+      at += (size_t(n) + 1 + 3) / 4 * 16;
+      slot[k] = at;
+      at += size_t(kSlots) * sizeof(int32_t);
+    }
+    records = at;
+    bytes = at + size_t(n) * sizeof(zero_tensor);
+  }
+};
 
 }  // namespace zero
 
 struct zero_tensors_s {
   std::vector<zero_tensor> t;
-  std::vector<int32_t> first, chunk;   // running counts of units and of chunks
+  std::vector<int32_t> first[2];   // running counts of units and of chunks
+  int32_t shift[2] = {0, 0};       // of their slots
   std::vector<std::pair<uintptr_t, uintptr_t>> owned;   // byte ranges of the list's buffers, sorted, disjoint
   int32_t param_type = 0, grad_type = 0, state_bits = 0;
   int32_t top_group = 0;      // the largest group in use

@@ -31,7 +31,7 @@ class zero_tensor(ctypes.Structure):
 
 _VP = ctypes.c_void_p
 _I32 = ctypes.c_int32
-_PP = ctypes.POINTER(_VP)
+_PP = _VP     # host arrays of pointers (ctypes passes an array as its address)
 
 _SIGNATURES = {
     "zero_tensors": (ctypes.c_int, [ctypes.POINTER(zero_tensor), _I32, _I32, _I32, _I32, ctypes.POINTER(_VP)]),
@@ -40,7 +40,7 @@ _SIGNATURES = {
     "zero_tensors_upload": (ctypes.c_int, [_VP, _VP, ctypes.c_size_t, _VP]),
     "zero_tensors_sqnorm_workspace_bytes": (ctypes.c_size_t, [_VP]),
     "zero_tensors_sqnorm": (ctypes.c_int, [_VP, _PP, _VP, _I32, _VP, ctypes.c_size_t, _VP]),
-    "zero_tensors_adamw_step": (ctypes.c_int, [_VP, _PP, ctypes.POINTER(zero.zero_adamw_hparams), _I32, _VP, _I32,
+    "zero_tensors_adamw_step": (ctypes.c_int, [_VP, _PP, _VP, _I32, _VP, _I32,
                                                _VP]),
     "zero_tensors_state_import": (ctypes.c_int, [_VP, _PP, _PP, _VP]),
     "zero_tensors_state_export": (ctypes.c_int, [_VP, _PP, _PP, _VP]),
@@ -211,13 +211,18 @@ def _pointers(lst, tensors, dtype, what):
     return tensors
 
 
+def _done(name, rc):
+    if rc:
+        zero._check(name, rc)
+
+
 def zero_tensors_sqnorm(lst: TensorList, tensor_grads, out, accumulate: bool, workspace, ws_bytes: int | None = None,
                         stream=None):
     arr = _pointers(lst, tensor_grads, lst.grad_dtype, "gradient")
     zero._need(out, 8, "output")
     if ws_bytes is None:
         ws_bytes = workspace.numel() * workspace.element_size()
-    zero._check("zero_tensors_sqnorm", library().zero_tensors_sqnorm(
+    _done("zero_tensors_sqnorm", library().zero_tensors_sqnorm(
         lst.handle, arr, zero._ptr(out), 1 if accumulate else 0, zero._ptr(workspace), ws_bytes,
         _stream(stream)))
 
@@ -236,14 +241,15 @@ def zero_tensors_adamw_step(lst: TensorList, tensor_grads, hp, rank_sqnorms, n_r
     groups = group_array(hp)
     if n_ranks > 0:
         zero._need(rank_sqnorms, 8 * n_ranks, "rank sums of squares")
-    zero._check("zero_tensors_adamw_step", library().zero_tensors_adamw_step(
+    _done("zero_tensors_adamw_step", library().zero_tensors_adamw_step(
         lst.handle, arr, groups, len(groups), zero._ptr(rank_sqnorms), n_ranks, _stream(stream)))
 
 
 def _state8(name, lst, m, v, stream):
     import torch
+
     m, v = (_pointers(lst, x, torch.float32, what) for x, what in ((m, "m"), (v, "v")))
-    zero._check(name, getattr(library(), name)(lst.handle, m, v, _stream(stream)))
+    _done(name, getattr(library(), name)(lst.handle, m, v, _stream(stream)))
 
 
 def zero_tensors_state_import(lst: TensorList, m, v, stream=None):
