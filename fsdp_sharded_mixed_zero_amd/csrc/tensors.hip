@@ -117,10 +117,23 @@ struct Unit {
   int block;
 };
 
+// Blocks go round the 8 XCDs one by one; in this order an XCD gets runs of
+// kXcdRun consecutive units, whose neighbours' cache lines then meet in one L2
+// (8-bit step over tensors packed without gaps, fp32 gradients: 391 us in
+// dispatch order, 380 in runs of 32; the import 212 and 203; aligned tensors
+// gain up to 3 %). The blocks after the last whole round keep their order.
+constexpr int kXcds = 8, kXcdRun = 32;
+__device__ __forceinline__ int block_in_runs() {
+  const int b = int(blockIdx.x), whole = int(gridDim.x) / (kXcds * kXcdRun) * (kXcds * kXcdRun);
+  if (b >= whole) return b;
+  const int xcd = b % kXcds, i = b / kXcds;
+  return (i / kXcdRun * kXcds + xcd) * kXcdRun + i % kXcdRun;
+}
+
 // The wave's unit; with SPLIT four waves share one, a block each.
 template <bool SPLIT>
 __device__ __forceinline__ Unit my_unit(const ListRange& l) {
-  const int u = l.u0 + int(SPLIT ? blockIdx.x >> 2 : blockIdx.x);
+  const int u = l.u0 + (SPLIT ? int(blockIdx.x >> 2) : block_in_runs());
   Unit w;
   w.block = SPLIT ? int(blockIdx.x & 3) : 0;
   int start;
