@@ -11,7 +11,9 @@ using zero::fail;
 
 namespace {
 
-constexpr int64_t kMaxTotal = int64_t(1) << 40;   // elements of a list: its units fit 32 bits
+// Elements and tensors of a list: its units, at most 2^30 + 2^25, fit 32 bits.
+constexpr int64_t kMaxTotal = int64_t(1) << 40;
+constexpr int32_t kMaxTensors = 1 << 24;
 
 struct Range {
   uintptr_t lo, hi;
@@ -58,7 +60,7 @@ extern "C" int zero_tensors(const zero_tensor* tensors, int32_t n, int32_t param
                             int32_t state_bits, zero_tensors_t* out) {
   static const char* who = "zero_tensors";
   if (tensors == nullptr || out == nullptr) return fail(ZERO_EINVAL, "%s: NULL argument", who);
-  if (n < 1) return fail(ZERO_EINVAL, "%s: n must be >= 1 (got %d)", who, n);
+  if (n < 1 || n > kMaxTensors) return fail(ZERO_EINVAL, "%s: n must be >= 1 and <= 2^24 (got %d)", who, n);
   for (int32_t type : {param_type, grad_type})
     if (type != ZERO_BF16 && type != ZERO_F32) return fail(ZERO_EINVAL, "%s: unknown element type %d", who, type);
   if (state_bits != 32 && state_bits != 8) return fail(ZERO_EINVAL, "%s: state_bits must be 32 or 8", who);

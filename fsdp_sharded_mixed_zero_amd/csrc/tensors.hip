@@ -38,19 +38,20 @@ struct ListRange {
   int32_t n_all, shift;
 };
 
-// Addresses of a launch's N tensors: element-size steps from the lowest one,
-// so that twice as many fit the arguments as with pointers. A launch ends
-// before a tensor that lies 2^32 elements or more from another of its own.
+// Addresses of a launch's N tensors: steps of 2^shift bytes from the lowest one
+// (their common alignment), so that twice as many fit the arguments as with
+// pointers. A launch ends before a tensor that would need more than 32 bits.
 constexpr uint32_t kNoTensor = 0xFFFFFFFFu;
 template <int N>
 struct Addresses {
   uintptr_t base;
+  uint32_t shift;
   uint32_t step[N];
 
   template <typename T>
   __device__ __forceinline__ T* at(int i) const {
     const uint32_t s = step[i];
-    return s == kNoTensor ? nullptr : reinterpret_cast<T*>(base + uintptr_t(s) * sizeof(T));
+    return s == kNoTensor ? nullptr : reinterpret_cast<T*>(base + (uintptr_t(s) << shift));
   }
 };
 
@@ -834,24 +835,31 @@ int launched(const char* who) {
   return zero::ok();
 }
 
-// The lowest and the highest address of some tensors.
+// The lowest and the highest address of some tensors, and the bits in which
+// any of them differ.
 struct Window {
-  uintptr_t lo = ~uintptr_t(0), hi = 0;
+  uintptr_t lo = ~uintptr_t(0), hi = 0, differ = 0;
 
-  // Whether p joins without taking the window beyond 32-bit steps of `size`.
-  bool take(const void* p, size_t size) {
+  int shift() const { return differ == 0 ? 0 : __builtin_ctzll(differ); }
+
+  // Whether p joins without taking the window beyond 32-bit steps.
+  bool take(const void* p) {
     if (p == nullptr) return true;
-    const uintptr_t a = std::min(lo, uintptr_t(p)), b = std::max(hi, uintptr_t(p));
-    if ((b - a) / size >= kNoTensor) return false;
-    lo = a, hi = b;
+    Window w = *this;
+    if (hi != 0) w.differ |= uintptr_t(p) ^ lo;
+    w.lo = std::min(lo, uintptr_t(p));
+    w.hi = std::max(hi, uintptr_t(p));
+    if (((w.hi - w.lo) >> w.shift()) >= kNoTensor) return false;
+    *this = w;
     return true;
   }
 
   template <int N>
-  void write(Addresses<N>* out, const void* const* p, int n, size_t size) const {
+  void write(Addresses<N>* out, const void* const* p, int n) const {
     out->base = lo;
+    out->shift = uint32_t(shift());
     for (int i = 0; i < n; ++i)
-      out->step[i] = p[i] == nullptr ? kNoTensor : uint32_t((uintptr_t(p[i]) - lo) / size);
+      out->step[i] = p[i] == nullptr ? kNoTensor : uint32_t((uintptr_t(p[i]) - lo) >> out->shift);
   }
 };
 
@@ -888,13 +896,12 @@ int for_ranges(const zero_tensors_s* h, bool chunks, int most, R restart, F fits
 // for_ranges over the gradients' addresses, which go into args->grads.
 template <typename A, typename Go>
 int for_gradients(const zero_tensors_s* h, bool chunks, const void* const* grads, A* args, Go go) {
-  const size_t size = h->grad_type == ZERO_BF16 ? 2 : 4;
   Window w;
   return for_ranges(
-      h, chunks, ZERO_TENSORS_PER_LAUNCH, [&] { w = Window(); }, [&](int32_t t) { return w.take(grads[t], size); },
+      h, chunks, ZERO_TENSORS_PER_LAUNCH, [&] { w = Window(); }, [&](int32_t t) { return w.take(grads[t]); },
       [&](const ListRange& l) {
         args->l = l;
-        w.write(&args->grads, grads + l.t0, l.n, size);
+        w.write(&args->grads, grads + l.t0, l.n);
         return go();
       });
 }
@@ -1018,12 +1025,12 @@ int launch_state8(const zero_tensors_s* h, bool import, const float* const* m, c
       h, false, kStatePerLaunch, [&] { wm = wv = Window(), low = 0; },
       [&](int32_t t) {
         low |= uintptr_t(m[t]) | uintptr_t(v[t]);
-        return wm.take(m[t], 4) && wv.take(v[t], 4);
+        return wm.take(m[t]) && wv.take(v[t]);
       },
       [&](const ListRange& l) {
         a.l = l;
-        wm.write(&a.m, p(m) + l.t0, l.n, 4);
-        wv.write(&a.v, p(v) + l.t0, l.n, 4);
+        wm.write(&a.m, p(m) + l.t0, l.n);
+        wv.write(&a.v, p(v) + l.t0, l.n);
         const unsigned lds = import || low % 128 == 0 ? kConvertLds : kConvertLdsOffLines;
         if (import && split_units(l))
           ZERO_LIST_LAUNCH(tensors_import_kernel<true>, true, 0, a, stream);

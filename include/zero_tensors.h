@@ -46,7 +46,7 @@ extern "C" {
 
 /* Tensors whose gradients one launch carries in its arguments. A list of more
  * tensors takes several launches, one after another on the stream, and so does
- * one whose gradients lie 2^32 elements or more apart. */
+ * one whose gradients lie 2^32 times their common alignment or more apart. */
 #define ZERO_TENSORS_PER_LAUNCH 768
 
 /* One tensor of a list; device pointers.
@@ -86,8 +86,8 @@ typedef struct zero_tensors_s* zero_tensors_t;
  *   param_type, grad_type  ZERO_BF16 or ZERO_F32, of the whole list
  *   state_bits  32 or 8
  *   out         receives a handle to free with zero_tensors_free
- * Errors: ZERO_EINVAL for n < 1, a NULL argument, an unknown type or state, a
- * length below 0 or a total beyond 2^40 elements, a group out of range, a
+ * Errors: ZERO_EINVAL for n < 1 or above 2^24, a NULL argument, an unknown type
+ * or state, a length below 0 or a total beyond 2^40 elements, a group out of range, a
  * NULL or misaligned pointer that the types need, a master with fp32
  * parameters, scales with a 32-bit state, or two buffers of the list that
  * overlap (the same tensor listed twice among them); ZERO_ENOMEM if the host
@@ -155,8 +155,10 @@ int zero_tensors_sqnorm(zero_tensors_t h, const void* const* tensor_grads, doubl
  * correct rounding (nearest, ties to even) of the fp64 value: off by at most
  * 2^-4 relative, or 2^-10 of its scale below 2^-6. The root of a second moment
  * above zero is stored as at least 2^-9 scales: it never comes back as zero
- * under the division. A NaN or infinite moment is stored as the e4m3 NaN and
- * left out of the maxima, so it spoils its own element only.
+ * under the division. (Under this step's own division, a root below 2^-72 of
+ * its block's largest counts as zero, which matters with eps = 0 only.) A NaN
+ * or infinite moment is stored as the e4m3 NaN and left out of the maxima, so it
+ * spoils its own element only.
  *
  * Errors: ZERO_EINVAL for NULL arguments, n_groups outside [1,
  * ZERO_TENSOR_GROUPS] or not above a group the list uses, hyperparameters that

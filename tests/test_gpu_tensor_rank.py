@@ -16,7 +16,7 @@ from oracle import step as O
 from devbits import hp_of, u16
 from tensor_lists import Case
 from tolerance import ordered_f32
-from test_gpu_tensors import check_codes, check32, check8, run_step
+from test_gpu_tensors import check_codes, check32, check8, run_step, untouched
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -220,6 +220,50 @@ def test_lists_on_several_streams_and_threads(bits):
             check32(c, [O.AdamWHParams()], [5], coef, d_parts, 4)
         else:
             check8(c, [O.AdamWHParams()], [5], coef)
+
+
+def test_a_list_dropped_while_its_step_runs():
+    """The step waits on a side stream behind other work while its list is
+    dropped and new tensors are allocated: its table is not given out again
+    before the step has read it."""
+    case, twin = (Case([70_000, 300], 8, seed=33).to_device() for _ in range(2))
+    sums = torch.full((1,), 0.25, dtype=torch.float64, device=DEV)
+    side = torch.cuda.Stream()
+    busy = torch.randn(4096, 4096, device=DEV)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(20):
+            busy = busy @ busy * 1e-3
+        tensors.zero_tensors_adamw_step(case.list, case.grad_ptrs, zero.hparams(step=2), sums, 1)
+    size = case.list.table.numel()
+    case.list = None
+    filled = [torch.full((size,), -1, dtype=torch.int64, device=DEV) for _ in range(8)]
+    torch.cuda.synchronize()
+    tensors.zero_tensors_adamw_step(twin.list, twin.grad_ptrs, zero.hparams(step=2), sums, 1)
+    torch.cuda.synchronize()
+    for k in case.A:
+        assert np.array_equal(case.A[k].bits(), twin.A[k].bits()), k
+    assert all(int(f.min()) == -1 for f in filled)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_list_without_elements_or_gradients(bits):
+    case = Case([0, 0, 5, 0], bits, seed=34, missing=(2,)).to_device()
+    run_step(case)
+    case.check_guards()
+    untouched(case, 2)
+    case = Case([0, 0], bits, seed=35).to_device()
+    run_step(case)
+    case.check_guards()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("lens", [[3_000_000, 5, 2_000_001], [1 << 20] * 9])
+def test_long_lists(bits, lens):
+    """Units of their own for the waves and whole rounds of XCD runs."""
+    case = Case(lens, bits, seed=36).to_device()
+    got = run_step(case)
+    check32(case, *got, 4) if bits == 32 else check8(case, *got[:3])
 
 
 def test_gradients_beyond_32_bit_offsets():

@@ -80,6 +80,7 @@ def test_list_refusals():
     L = tensors.library()
     refused(make([record()], n=0)[0], "n must be")
     refused(make([record()], n=-3)[0], "n must be")
+    refused(make([record()], n=(1 << 24) + 1)[0], "n must be")
     refused(make([record()], bits=16)[0], "state_bits")
     refused(make([record()], param=2)[0], "type")
     refused(make([record()], grad=-1)[0], "type")
