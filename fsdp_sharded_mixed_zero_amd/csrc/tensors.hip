@@ -424,8 +424,8 @@ __device__ __forceinline__ uint32_t m_bytes(const float mf[4], float up, F exact
 }
 
 // sqrt(v), in units of the scale, to bytes; y[k]: that root in fp32, for the
-// update (roots below 2^-63 units, 2^-72 of the block's largest, count as zero
-// in y). vf: fp32 of v; exact(k): the fp64 v[k].
+// update, off by up to 2^-63 units where its square is subnormal. vf: fp32 of
+// v; exact(k): the fp64 v[k].
 template <typename F>
 __device__ __forceinline__ uint32_t v_bytes(const float vf[4], float up, float y[4], F exact) {
   const auto square = [&](int j) { return exact(j) * (double(up) * double(up)); };
@@ -653,6 +653,12 @@ __device__ __forceinline__ T reload(const T* p) {
   return *(const ZERO_GLOBAL T*)p;
 }
 
+// The 8-bit step's fp32 root is off by up to 2^-75 (a subnormal square of a
+// moment) and by up to 2^-63 units of the block's scale: a denominator below
+// 2^25 of either takes the update in fp64. With eps = 1e-8 that begins at
+// blocks whose largest root passes 10^5.
+constexpr float kLeastDenom = 0x1p-50f, kLeastUnits = 0x1p-38f;
+
 __device__ __forceinline__ float grad_value(uint16_t g) { return __uint_as_float(uint32_t(g) << 16); }
 __device__ __forceinline__ float grad_value(float g) { return g; }
 
@@ -729,11 +735,22 @@ struct AdamW8 {
       float y[4];
       const uint32_t vb = v_bytes(vf[b], lane_f32(s.up, lane_of(b, 1)), y, exact_v);
       const float v_scale = lane_f32(s.scale, lane_of(b, 1));
+      const float least = fmaxf(kLeastDenom, v_scale * kLeastUnits) * k.inv_sqrt_bc2;
+      uint32_t tiny = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float denom = fmaf(y[i] * v_scale, k.inv_sqrt_bc2, k.eps);
         const float q = mf[b][i] * __builtin_amdgcn_rcpf(denom);   // the reciprocal within one unit in the last place
+        if (denom < least) tiny |= 1u << i;
         p4[b][i] = fmaf(-k.step_size, q, fmaf(-k.lr_wd, p4[b][i], p4[b][i]));
+      }
+      for (tiny &= (1u << cnt) - 1u; tiny != 0; tiny &= tiny - 1) {
+        const int j = __ffs(int(tiny)) - 1;
+        const double denom = sqrt(exact_v(j)) / x.sqrt_bc2 + x.eps;
+        const float p = float(double(reload(master + b * kBlock + j)) * x.decay - x.step_size * (exact_m(j) / denom));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i == j) p4[b][i] = p;
       }
       store4(master + b * kBlock, cnt, p4[b]);
       if constexpr (sizeof(P) == 2) store4(param + b * kBlock, cnt, p4[b]);

@@ -155,10 +155,10 @@ int zero_tensors_sqnorm(zero_tensors_t h, const void* const* tensor_grads, doubl
  * correct rounding (nearest, ties to even) of the fp64 value: off by at most
  * 2^-4 relative, or 2^-10 of its scale below 2^-6. The root of a second moment
  * above zero is stored as at least 2^-9 scales: it never comes back as zero
- * under the division. (Under this step's own division, a root below 2^-72 of
- * its block's largest counts as zero, which matters with eps = 0 only.) A NaN
- * or infinite moment is stored as the e4m3 NaN and left out of the maxima, so it
- * spoils its own element only.
+ * under the division. Where a denominator is too small for fp32 to resolve its
+ * root (eps = 0 and small roots, or very different ones in a block), the update
+ * is evaluated in fp64. A moment that is NaN, or infinite in fp32, is stored as
+ * the e4m3 NaN and left out of the maxima, so it spoils its own element only.
  *
  * Errors: ZERO_EINVAL for NULL arguments, n_groups outside [1,
  * ZERO_TENSOR_GROUPS] or not above a group the list uses, hyperparameters that

@@ -103,10 +103,16 @@ def adamw8_step(grad, master, m_codes, m_scale, v_codes, v_scale, step: int, hp:
 
 def update_bound(master, m1, v1, step: int, hp: AdamWHParams):
     """|master - p'| allowed to an fp32 evaluation of the update from m1, v1,
-    in units of 2^-24: the decay (one rounded constant and two roundings of the
-    master), the step (constant, m1, the quotient), the denominator (the
-    scaled root: its square, square root, scale and the scale's reciprocal, two
-    products; the bias constant, the sum)."""
+    in units of 2^-24 (a rounding to nearest is 1, a hardware square root or
+    reciprocal within one unit in the last place is 2, and what is under a
+    square root counts half):
+
+    of the master: the decayed value 1, its constant under 1, the result 1;
+    of the step: its constant 1, m1 1, the reciprocal 2, the quotient 1, the
+    result 1; of the denominator under it: v1 1/2, the square of 448 / largest
+    root 1/2, their product 1/2, the square root 2, 448 / root and root / 448
+    one each, their product with the root 1, the bias constant or eps 1, the
+    sum 1. 6 + 8.5 = 14.5, and 1/2 for the products of these errors."""
     bias1, bias2 = 1.0 - hp.beta1 ** step, 1.0 - hp.beta2 ** step
     move = np.abs(hp.lr / bias1 * m1 / (np.sqrt(v1) / math.sqrt(bias2) + hp.eps))
-    return 2.0 ** -24 * (3 * np.abs(np.asarray(master, np.float64)) + 12 * move)
+    return 2.0 ** -24 * (3 * np.abs(np.asarray(master, np.float64)) + 15 * move)
