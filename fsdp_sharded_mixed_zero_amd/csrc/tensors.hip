@@ -8,10 +8,16 @@
 //   tensors_import_kernel, tensors_export_kernel
 //                           fp32 moments <-> the 8-bit state
 //
-// A unit of work is 1024 consecutive elements of one tensor, four 8-bit
-// blocks, and belongs to one wave. A launch carries the gradients' addresses
-// in its arguments, as 32-bit offsets of up to 768 tensors; everything that
-// does not change from step to step is in the list's device table.
+// Every element is read and written once and takes a few dozen instructions,
+// so the kernels are bound by HBM on long lists (5.7 to 6.4 TB/s, a plain copy
+// reaching 6.25) and by the launch on short ones (5 us). What a list adds to a
+// flat array is to find a wave's tensor, which costs memory latency: the work
+// is cut into units of 1024 consecutive elements of one tensor (four 8-bit
+// blocks; chunks of 4096 for the norm), and a running count of them is searched
+// from a slot near the answer. A launch carries the gradients' addresses in its
+// arguments, as 32-bit steps for up to 768 tensors; everything that does not
+// change from step to step is in the device table.
+// Times below are medians of one MI355X, the kernel alone unless a call is named.
 #include <cstring>
 
 #include "tensors_internal.h"
@@ -23,7 +29,9 @@ using zero::kSqChunk;
 using zero::kUnitElems;
 using zero::StepConst;
 
-constexpr int kListThreads = 64;                        // one wave, one unit
+// One wave a block: a wave's registers are free for the next unit as soon as it
+// ends (256 threads: the 8-bit step over 119 M elements 403 us against 382).
+constexpr int kListThreads = 64;
 constexpr int kSqListWaves = 4, kSqListThreads = 64 * kSqListWaves;
 constexpr int64_t kListMaxUnits = int64_t(1) << 23;     // units per launch: at most 2^31 work-items
 
@@ -463,11 +471,12 @@ __global__ __launch_bounds__(256) void tensors_upload_kernel(const UploadArgs a)
 }
 
 // Sums of squares. A wave takes a chunk of 4096 elements of one tensor, a lane
-// 16 bytes of it at a time: VE elements. (119 M bf16 gradients: 45 us with the
-// final sum, 5.3 TB/s; in chunks of 2048, 47 us; of 1024, where finding the
-// tensor takes most of a wave's life, 62 us. A short list in one block and one
-// launch instead of two is slower from some 16 thousand elements on: one CU
-// squares them in fp64, 92 thousand in 7.8 us against 5.5.)
+// 16 bytes of it at a time: VE elements. Bound by the reads: 119 M bf16
+// gradients in 37 us, 6.4 TB/s, and 4 us for the final sum over the partials;
+// 24.3 M fp32 20 us a call. (In chunks of 2048 and 1024, where finding the
+// tensor takes most of a wave's life, 47 and 62 us a call against 45. One block
+// and one launch instead of two gain 1 us up to some 60 thousand elements and
+// lose from 100 thousand on, where one CU squares them in fp64: left out.)
 template <typename G>
 struct SqChunk {
   static constexpr int VE = 16 / sizeof(G), NV = kSqChunk / (64 * VE);
@@ -598,11 +607,13 @@ __device__ __forceinline__ void over_unit(const Unit& w, const W& work) {
   }
 }
 
-// The 32-bit step, one wave to a block of 256 elements. P: uint16_t (bf16
-// parameters and an fp32 master) or float (its own master). The blocks lie by
-// the master's 128-byte lines (line_phase): with blocks by the tensor's first
+// The 32-bit step, one wave to a block of 256 elements (four blocks a wave:
+// 574 us against 563 when that was chosen). P: uint16_t (bf16 parameters and an
+// fp32 master) or float (its own master). Bound by HBM: 119 M elements in
+// 522 us, 6.4 TB/s, with no byte read or written twice. The blocks lie by the
+// master's 128-byte lines (line_phase): with blocks by the tensor's first
 // element, waves on different XCDs write parts of the same lines, and tensors
-// packed without gaps take 730 us instead of 555 for 119 M elements.
+// packed without gaps take 730 us instead of 555.
 template <typename P, typename G>
 __global__ __launch_bounds__(kListThreads) void tensors_adamw_kernel(const StepArgs a) {
   const Unit w = my_unit<true>(a.l);
@@ -664,7 +675,11 @@ __device__ __forceinline__ float grad_value(float g) { return g; }
 
 // The 8-bit step of NB blocks from b0 on in one wave: all loads first, then
 // the moments in fp64, the blocks' maxima together, then block by block the
-// bytes and the update.
+// bytes and the update. Four blocks share the eight reductions and keep 16
+// loads in flight a lane (one block a wave: 418 us for 119 M elements, two 372,
+// four 382, but 24.3 M in 99, 89 and 86 us). Bound by HBM: 119 M elements with
+// fp32 gradients in 354 us a call, 6.1 TB/s, 24.3 M packed without gaps in
+// 65 us, 6.0 TB/s; some 850 vector instructions per 1024 elements hide under it.
 template <typename P, typename G>
 struct AdamW8 {
   const ListRange& l;
@@ -722,7 +737,7 @@ struct AdamW8 {
     for (int b = 0; b < NB; ++b) {
       // An element's moments again in fp64, where a byte hangs on them: from
       // memory, so that the gradients and bytes need no registers until here
-      // (16 to 24 of 150, and with them the fourth wave of a SIMD).
+      // (137 to 149 without this, about 100 with it: four waves a SIMD, not three).
       const auto exact_m = [&](int j) {
         const int at = b * kBlock + j;
         return j < cnt ? first(b, e4m3_value(reload(st.m + at)), grad_value(reload(g + at))) : 0.0;
@@ -767,6 +782,10 @@ __global__ __launch_bounds__(kListThreads) void tensors_adamw8_kernel(const Step
   if (g != nullptr) over_unit<SPLIT>(w, AdamW8<P, G>{a.l, a.c, w, g});
 }
 
+// The conversions of NB blocks from b0 on, with the step's rounding and layout.
+// Bound by HBM: the import of 105 M elements takes 170 us, 6.2 TB/s; the export of
+// 24.3 M into arrays off 128-byte lines 42.5 us, 5.7 TB/s (4 % more bytes
+// written than asked for: both ends' waves write the lines they share).
 struct Import8 {
   const ListRange& l;
   const Unit& w;
@@ -923,7 +942,9 @@ int for_gradients(const zero_tensors_s* h, bool chunks, const void* const* grads
       });
 }
 
-// Whether four waves share a unit.
+// Whether four waves share a unit, a block each: with few units the waves are too
+// few to fill the chip (8-bit step over 90 units, 5.7 us against 9.9 with one
+// wave a unit; over 2048 units 9.8 against 8.6).
 constexpr int64_t kSplitUnits = 1024;
 bool split_units(const ListRange& l) { return l.u1 - l.u0 <= kSplitUnits; }
 
@@ -946,7 +967,7 @@ constexpr unsigned kConvertLds = 10 << 10, kConvertLdsOffLines = 16 << 10;
 constexpr unsigned kStep32Lds = 8 << 10;
 
 // LDS of the 8-bit step's blocks in long launches, against too many waves in
-// flight. By the kernel's registers a CU holds 20; 12 (13 KiB) with bf16
+// flight. By the kernel's registers a CU holds 16; 12 (13 KiB) with bf16
 // gradients and 10 (16 KiB) with fp32 ones are faster from some 2^26 elements
 // on: 105 M, 284 us without and 277 us, 323 and 307; 119 M, 330 and 324, 377
 // and 359; but 47 M, 138.4 and 139.8, 154.1 and 156.1.

@@ -174,8 +174,8 @@ int zero_tensors_adamw_step(zero_tensors_t h, const void* const* tensor_grads, c
  * 8-bit state of a list (state_bits 8) and back, for a checkpoint written with
  * fp32 moments, or one to be read by an optimizer that holds them so. The
  * import rounds as the step does, from m1 = m, v1 = v (a negative v is stored
- * as NaN); the export writes m = fp32(M * m_scale) and v = fp32((S *
- * v_scale)^2), each rounded once. Parameters and masters are not touched.
+ * as NaN); the export writes m = M * m_scale and v = (S * v_scale)^2, formed in
+ * fp64 and rounded to fp32. Parameters and masters are not touched.
  *   m, v   HOST arrays of the list's n device pointers to fp32 arrays of the
  *          tensors' lengths; a tensor with both entries NULL is left out
  * Errors: ZERO_EINVAL for NULL arguments, a list with a 32-bit state, one of a
