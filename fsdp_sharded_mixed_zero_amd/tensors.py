@@ -70,22 +70,29 @@ def state8_blocks(n: int) -> int:
 _torch_c = None
 
 
-def _stream(lst, stream):
+def _stream(stream):
     """The stream's handle, as zero._stream gives it; the current stream's by
     the short way (0.1 us against 2.6 us for the stream object, of a call that
-    takes 6). The list's table is marked as in use on the stream, so that its
-    memory, freed with the list, is not given out before the work is done."""
+    takes 6)."""
     global _torch_c
     if stream is not None:
-        handle = zero._stream(stream)
-    else:
-        if _torch_c is None:
-            from torch import _C
-            _torch_c = _C
-        handle = _torch_c._cuda_getCurrentRawStream(_torch_c._cuda_getDevice())
-    if handle not in lst._streams:
-        lst._use(handle)
-    return handle
+        return zero._stream(stream)
+    if _torch_c is None:
+        from torch import _C
+        _torch_c = _C
+    return _torch_c._cuda_getCurrentRawStream(_torch_c._cuda_getDevice())
+
+
+def _call(name, lst, stream, *args):
+    """One call of the library on the list. The list's table is marked as in
+    use on the stream, so that its memory, freed with the list, is not given
+    out before the work is done."""
+    stream = _stream(stream)
+    rc = getattr(_lib or library(), name)(lst.handle, *args, stream)
+    if rc:
+        zero._check(name, rc)
+    if stream not in lst._streams:
+        lst._use(stream)
 
 
 def _type_of(dtype, what):
@@ -134,6 +141,8 @@ class TensorList:
     def _use(self, handle):
         import torch
         self._streams.add(handle)
+        if isinstance(self.table, int):     # memory that the caller keeps
+            return
         self.table.record_stream(torch.cuda.ExternalStream(handle, device=self.device))
 
     def close(self):
@@ -167,7 +176,8 @@ def zero_tensors(param, m, v, master=None, m_scale=None, v_scale=None, group=Non
     p_type = _type_of(param[0].dtype, "param")
     grad_dtype = param[0].dtype if grad_dtype is None else grad_dtype
     g_type = _type_of(grad_dtype, "grad_dtype")
-    bits = 32 if m[0].dtype == torch.float32 else 8
+    first = next((t for t in m if t is not None), None)    # None: only tensors without elements
+    bits = 8 if first is not None and first.dtype != torch.float32 else 32
     state = (torch.float32,) if bits == 32 else (torch.float8_e4m3fn, torch.uint8, torch.int8)
     blocks = [state8_blocks(n) for n in lens]
     f32 = (torch.float32,)
@@ -192,8 +202,7 @@ def zero_tensors(param, m, v, master=None, m_scale=None, v_scale=None, group=Non
     with torch.cuda.device(device):
         nbytes = library().zero_tensors_table_bytes(h)
         lst.table = torch.empty((nbytes + 7) // 8, dtype=torch.int64, device=device)
-        zero._check("zero_tensors_upload", library().zero_tensors_upload(
-            h, lst.table.data_ptr(), nbytes, _stream(lst, stream)))
+        _call("zero_tensors_upload", lst, stream, lst.table.data_ptr(), nbytes)
         if not torch.cuda.is_current_stream_capturing():
             torch.cuda.synchronize(device)
     return lst
@@ -211,10 +220,11 @@ def zero_tensors_upload(lst: TensorList, table, table_bytes: int | None = None, 
     """Write the list's table into ``table`` and bind the list to it."""
     if table_bytes is None:
         table_bytes = table.numel() * table.element_size()
-    zero._check("zero_tensors_upload", library().zero_tensors_upload(
-        lst.handle, zero._ptr(table), table_bytes, _stream(lst, stream)))
-    lst.table = table
-    lst._streams = set()
+    zero._need(table, table_bytes, "table")
+    handle = _stream(stream)
+    zero._check("zero_tensors_upload", library().zero_tensors_upload(lst.handle, zero._ptr(table), table_bytes, handle))
+    lst.table, lst._streams = table, set()
+    lst._use(handle)
 
 
 def zero_tensors_sqnorm_workspace_bytes(lst: TensorList) -> int:
@@ -222,17 +232,15 @@ def zero_tensors_sqnorm_workspace_bytes(lst: TensorList) -> int:
 
 
 def _pointers(lst, tensors, dtype, what):
+    """``dtype`` None: float32."""
     if not isinstance(tensors, ctypes.Array):
+        if dtype is None:
+            from torch import float32 as dtype
         _check(tensors, lst.lens, (dtype,), lst.device, what)
         return zero._ptr_array([t if n else None for t, n in zip(tensors, lst.lens)])
     if len(tensors) < lst.n_tensors:
         raise ValueError(f"{what}: {len(tensors)} pointers for a list of {lst.n_tensors} tensors")
     return tensors
-
-
-def _done(name, rc):
-    if rc:
-        zero._check(name, rc)
 
 
 def zero_tensors_sqnorm(lst: TensorList, tensor_grads, out, accumulate: bool, workspace, ws_bytes: int | None = None,
@@ -241,9 +249,10 @@ def zero_tensors_sqnorm(lst: TensorList, tensor_grads, out, accumulate: bool, wo
     zero._need(out, 8, "output")
     if ws_bytes is None:
         ws_bytes = workspace.numel() * workspace.element_size()
-    _done("zero_tensors_sqnorm", library().zero_tensors_sqnorm(
-        lst.handle, arr, zero._ptr(out), 1 if accumulate else 0, zero._ptr(workspace), ws_bytes,
-        _stream(lst, stream)))
+    else:
+        zero._need(workspace, ws_bytes, "workspace")
+    _call("zero_tensors_sqnorm", lst, stream, arr, zero._ptr(out), 1 if accumulate else 0, zero._ptr(workspace),
+          ws_bytes)
 
 
 def group_array(hp):
@@ -260,15 +269,11 @@ def zero_tensors_adamw_step(lst: TensorList, tensor_grads, hp, rank_sqnorms, n_r
     groups = group_array(hp)
     if n_ranks > 0:
         zero._need(rank_sqnorms, 8 * n_ranks, "rank sums of squares")
-    _done("zero_tensors_adamw_step", library().zero_tensors_adamw_step(
-        lst.handle, arr, groups, len(groups), zero._ptr(rank_sqnorms), n_ranks, _stream(lst, stream)))
+    _call("zero_tensors_adamw_step", lst, stream, arr, groups, len(groups), zero._ptr(rank_sqnorms), n_ranks)
 
 
 def _state8(name, lst, m, v, stream):
-    import torch
-
-    m, v = (_pointers(lst, x, torch.float32, what) for x, what in ((m, "m"), (v, "v")))
-    _done(name, getattr(library(), name)(lst.handle, m, v, _stream(lst, stream)))
+    _call(name, lst, stream, _pointers(lst, m, None, "m"), _pointers(lst, v, None, "v"))
 
 
 def zero_tensors_state_import(lst: TensorList, m, v, stream=None):
