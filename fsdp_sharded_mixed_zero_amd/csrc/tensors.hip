@@ -476,7 +476,7 @@ __global__ __launch_bounds__(256) void tensors_upload_kernel(const UploadArgs a)
 // 24.3 M fp32 20 us a call. (In chunks of 2048 and 1024, where finding the
 // tensor takes most of a wave's life, 47 and 62 us a call against 45. One block
 // and one launch instead of two gain 1 us up to some 60 thousand elements and
-// lose from 100 thousand on, where one CU squares them in fp64: left out.)
+// lose from 90 thousand on, where one CU squares them in fp64: left out.)
 template <typename G>
 struct SqChunk {
   static constexpr int VE = 16 / sizeof(G), NV = kSqChunk / (64 * VE);
