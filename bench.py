@@ -100,7 +100,7 @@ def update_kernel(accum=1, separate_unpack=False, flat=False, state_arrays=False
     ``list_bits``: 32 or 8 for the step over a list of tensors."""
     if list_bits:
         return ("tensors_adamw_kernel<unsigned short, unsigned short>" if list_bits == 32 else
-                "tensors_adamw8_kernel<unsigned short, unsigned short, false>")
+                "tensors_adamw8_kernel<unsigned short, unsigned short, 1>")
     grad = "float" if accum > 1 else "unsigned short"
     if state_arrays:
         return f"adamw_arrays_vec_kernel<{grad}>"

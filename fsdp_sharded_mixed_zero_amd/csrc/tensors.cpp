@@ -103,6 +103,7 @@ extern "C" int zero_tensors(const zero_tensor* tensors, int32_t n, int32_t param
     h->state_bits = state_bits;
     h->t.assign(tensors, tensors + n);
     for (auto& f : h->first) f.resize(size_t(n) + 1);
+    h->partial.assign(size_t(n) + 1, 0);
     std::vector<Range> ranges;
     ranges.reserve(size_t(n) * 6);
     const bool wide = state_bits == 32, own_master = param_type == ZERO_F32;
@@ -123,6 +124,7 @@ extern "C" int zero_tensors(const zero_tensor* tensors, int32_t n, int32_t param
       }
       h->top_group = std::max(h->top_group, t.group);
       total += t.len;
+      h->partial[size_t(i) + 1] = h->partial[size_t(i)] + (t.len % zero::kUnitElems != 0);
       const int64_t lead = wide && t.len > 0 ? zero::line_phase(uintptr_t(own_master ? t.param : t.master)) : 0;
       units += (lead + t.len + zero::kUnitElems - 1) / zero::kUnitElems;
       chunks += (t.len + zero::kSqChunk - 1) / zero::kSqChunk;

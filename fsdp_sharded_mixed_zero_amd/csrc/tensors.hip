@@ -139,12 +139,13 @@ __device__ __forceinline__ int block_in_runs() {
   return (i / kXcdRun * kXcds + xcd) * kXcdRun + i % kXcdRun;
 }
 
-// The wave's unit; with SPLIT four waves share one, a block each.
-template <bool SPLIT>
+// The wave's unit, which WAVES waves share (1, 2 or 4), the same number of
+// blocks each.
+template <int WAVES>
 __device__ __forceinline__ Unit my_unit(const ListRange& l) {
-  const int u = l.u0 + (SPLIT ? int(blockIdx.x >> 2) : block_in_runs());
+  const int u = l.u0 + (WAVES > 1 ? int(blockIdx.x) / WAVES : block_in_runs());
   Unit w;
-  w.block = SPLIT ? int(blockIdx.x & 3) : 0;
+  w.block = int(blockIdx.x) % WAVES * (zero::kUnitBlocks / WAVES);
   int start;
   w.t = find_tensor(l, u, &start);
   w.base = int64_t(u - start) * kUnitElems;
@@ -592,18 +593,22 @@ __device__ __forceinline__ float old_scales(const State8& s) {
   return ((const ZERO_GLOBAL float*)(lane < 4 ? s.m_scale : s.v_scale))[block];
 }
 
-// Calls work.run<NB>(b): NB blocks from b on, all of them full where NB is more
-// than one. A wave with a unit of its own holds a full one's four blocks at
-// once and takes the blocks at a tensor's end in turn.
-template <bool SPLIT, typename W>
+// Calls work.run<NB, FULL>(b): NB blocks from b on, of which all are full, or some
+// reach beyond the tensor's end. A wave takes its blocks at once, except that the
+// four of a partial unit come in turn: a second copy of the code for four would
+// not fit the instruction cache beside the first (8-bit step of 24.3 M elements
+// 67 us instead of 63).
+template <int WAVES, typename W>
 __device__ __forceinline__ void over_unit(const Unit& w, const W& work) {
-  if constexpr (SPLIT) {
-    if (w.block * kBlock < w.rest) work.template run<1>(w.block);
-  } else if (w.rest >= kUnitElems) {
-    work.template run<kBlocks>(0);
+  constexpr int NB = kBlocks / WAVES;
+  const int64_t rest = w.rest - w.block * kBlock;
+  if (NB > 1 && rest >= NB * kBlock) {
+    work.template run<NB, true>(w.block);
+  } else if constexpr (NB < kBlocks) {
+    if (rest > 0) work.template run<NB, false>(w.block);
   } else {
 #pragma unroll 1
-    for (int b = 0; b * kBlock < w.rest; ++b) work.template run<1>(b);
+    for (int b = 0; b * kBlock < rest; ++b) work.template run<1, false>(b);
   }
 }
 
@@ -616,7 +621,7 @@ __device__ __forceinline__ void over_unit(const Unit& w, const W& work) {
 // packed without gaps take 730 us instead of 555.
 template <typename P, typename G>
 __global__ __launch_bounds__(kListThreads) void tensors_adamw_kernel(const StepArgs a) {
-  const Unit w = my_unit<true>(a.l);
+  const Unit w = my_unit<4>(a.l);
   const zero_tensor* r = a.l.rec + w.t;
   P* param = static_cast<P*>(uniform_load(&r->param));
   float* master = sizeof(P) == 4 ? reinterpret_cast<float*>(param) : uniform_load(&r->master);
@@ -687,7 +692,7 @@ struct AdamW8 {
   const Unit& w;
   const G* grad;
 
-  template <int NB>
+  template <int NB, bool FULL>
   __device__ __forceinline__ void run(int b0) const {
     const int lane = threadIdx.x & 63;
     const zero_tensor* r = l.rec + w.t;
@@ -696,16 +701,18 @@ struct AdamW8 {
     float* master = sizeof(P) == 4 ? reinterpret_cast<float*>(param) : uniform_load(&r->master) + e;
     const State8 st = state8_of(l, w, b0);
     const G* g = grad + e;
-    const int cnt = NB > 1 ? 4 : count4(w.rest - b0 * kBlock);
+    int cnt[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) cnt[b] = FULL ? 4 : count4(w.rest - (b0 + b) * kBlock);
     decltype(load4(g, 4)) g4[NB];
     f32x4 p4[NB];
     uint32_t m8[NB], s8[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      g4[b] = load4(g + b * kBlock, cnt);
-      p4[b] = load4(master + b * kBlock, cnt);
-      m8[b] = load4(st.m + b * kBlock, cnt);
-      s8[b] = load4(st.v + b * kBlock, cnt);
+      g4[b] = load4(g + b * kBlock, cnt[b]);
+      p4[b] = load4(master + b * kBlock, cnt[b]);
+      m8[b] = load4(st.m + b * kBlock, cnt[b]);
+      s8[b] = load4(st.v + b * kBlock, cnt[b]);
     }
     const float old = old_scales<NB>(st);
     const int group = uniform_load(&r->group);
@@ -740,11 +747,11 @@ struct AdamW8 {
       // (137 to 149 without this, about 100 with it: four waves a SIMD, not three).
       const auto exact_m = [&](int j) {
         const int at = b * kBlock + j;
-        return j < cnt ? first(b, e4m3_value(reload(st.m + at)), grad_value(reload(g + at))) : 0.0;
+        return j < cnt[b] ? first(b, e4m3_value(reload(st.m + at)), grad_value(reload(g + at))) : 0.0;
       };
       const auto exact_v = [&](int j) {
         const int at = b * kBlock + j;
-        return j < cnt ? second(b, e4m3_value(reload(st.v + at)), grad_value(reload(g + at))) : 0.0;
+        return j < cnt[b] ? second(b, e4m3_value(reload(st.v + at)), grad_value(reload(g + at))) : 0.0;
       };
       const uint32_t mb = m_bytes(mf[b], lane_f32(s.up, lane_of(b, 0)), exact_m);
       float y[4];
@@ -759,7 +766,7 @@ struct AdamW8 {
         if (denom < least) tiny |= 1u << i;
         p4[b][i] = fmaf(-k.step_size, q, fmaf(-k.lr_wd, p4[b][i], p4[b][i]));
       }
-      for (tiny &= (1u << cnt) - 1u; tiny != 0; tiny &= tiny - 1) {
+      for (tiny &= (1u << cnt[b]) - 1u; tiny != 0; tiny &= tiny - 1) {
         const int j = __ffs(int(tiny)) - 1;
         const double denom = sqrt(exact_v(j)) / x.sqrt_bc2 + x.eps;
         const float p = float(double(reload(master + b * kBlock + j)) * x.decay - x.step_size * (exact_m(j) / denom));
@@ -767,19 +774,19 @@ struct AdamW8 {
         for (int i = 0; i < 4; ++i)
           if (i == j) p4[b][i] = p;
       }
-      store4(master + b * kBlock, cnt, p4[b]);
-      if constexpr (sizeof(P) == 2) store4(param + b * kBlock, cnt, p4[b]);
-      store4(st.m + b * kBlock, cnt, mb);
-      store4(st.v + b * kBlock, cnt, vb);
+      store4(master + b * kBlock, cnt[b], p4[b]);
+      if constexpr (sizeof(P) == 2) store4(param + b * kBlock, cnt[b], p4[b]);
+      store4(st.m + b * kBlock, cnt[b], mb);
+      store4(st.v + b * kBlock, cnt[b], vb);
     }
   }
 };
 
-template <typename P, typename G, bool SPLIT>
+template <typename P, typename G, int WAVES>
 __global__ __launch_bounds__(kListThreads) void tensors_adamw8_kernel(const StepArgs a) {
-  const Unit w = my_unit<SPLIT>(a.l);
+  const Unit w = my_unit<WAVES>(a.l);
   const G* g = a.grads.template at<const G>(w.t - a.l.t0);
-  if (g != nullptr) over_unit<SPLIT>(w, AdamW8<P, G>{a.l, a.c, w, g});
+  if (g != nullptr) over_unit<WAVES>(w, AdamW8<P, G>{a.l, a.c, w, g});
 }
 
 // The conversions of NB blocks from b0 on, with the step's rounding and layout.
@@ -791,15 +798,17 @@ struct Import8 {
   const Unit& w;
   const float *m32, *v32;
 
-  template <int NB>
+  template <int NB, bool FULL>
   __device__ __forceinline__ void run(int b0) const {
     const int64_t e = w.base + b0 * kBlock + 4 * int(threadIdx.x & 63);
     const State8 st = state8_of(l, w, b0);
-    const int cnt = NB > 1 ? 4 : count4(w.rest - b0 * kBlock);
+    int cnt[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) cnt[b] = FULL ? 4 : count4(w.rest - (b0 + b) * kBlock);
     float m[NB][4], v[NB][4];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const f32x4 m4 = load4(m32 + e + b * kBlock, cnt), v4 = load4(v32 + e + b * kBlock, cnt);
+      const f32x4 m4 = load4(m32 + e + b * kBlock, cnt[b]), v4 = load4(v32 + e + b * kBlock, cnt[b]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) m[b][i] = m4[i], v[b][i] = v4[i];
     }
@@ -807,19 +816,19 @@ struct Import8 {
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       float y[4];
-      store4(st.m + b * kBlock, cnt,
+      store4(st.m + b * kBlock, cnt[b],
              m_bytes(m[b], lane_f32(s.up, lane_of(b, 0)), [&](int j) { return double(pick(m[b], j)); }));
-      store4(st.v + b * kBlock, cnt,
+      store4(st.v + b * kBlock, cnt[b],
              v_bytes(v[b], lane_f32(s.up, lane_of(b, 1)), y, [&](int j) { return double(pick(v[b], j)); }));
     }
   }
 };
 
-template <bool SPLIT>
+template <int WAVES>
 __global__ __launch_bounds__(kListThreads) void tensors_import_kernel(const State8Args a) {
-  const Unit w = my_unit<SPLIT>(a.l);
+  const Unit w = my_unit<WAVES>(a.l);
   const float *m32 = a.m.at<const float>(w.t - a.l.t0), *v32 = a.v.at<const float>(w.t - a.l.t0);
-  if (m32 != nullptr) over_unit<SPLIT>(w, Import8{a.l, w, m32, v32});
+  if (m32 != nullptr) over_unit<WAVES>(w, Import8{a.l, w, m32, v32});
 }
 
 struct Export8 {
@@ -827,16 +836,18 @@ struct Export8 {
   const Unit& w;
   float *m32, *v32;
 
-  template <int NB>
+  template <int NB, bool FULL>
   __device__ __forceinline__ void run(int b0) const {
     const int64_t e = w.base + b0 * kBlock + 4 * int(threadIdx.x & 63);
     const State8 st = state8_of(l, w, b0);
-    const int cnt = NB > 1 ? 4 : count4(w.rest - b0 * kBlock);
+    int cnt[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) cnt[b] = FULL ? 4 : count4(w.rest - (b0 + b) * kBlock);
     uint32_t m8[NB], s8[NB];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      m8[b] = load4(st.m + b * kBlock, cnt);
-      s8[b] = load4(st.v + b * kBlock, cnt);
+      m8[b] = load4(st.m + b * kBlock, cnt[b]);
+      s8[b] = load4(st.v + b * kBlock, cnt[b]);
     }
     const float old = old_scales<NB>(st);
 #pragma unroll
@@ -850,17 +861,17 @@ struct Export8 {
         m4[i] = m[i] * m_scale;
         v4[i] = float(double(root[i] * root[i]) * s2);   // an e4m3 value's square is exact
       }
-      store4(m32 + e + b * kBlock, cnt, m4);
-      store4(v32 + e + b * kBlock, cnt, v4);
+      store4(m32 + e + b * kBlock, cnt[b], m4);
+      store4(v32 + e + b * kBlock, cnt[b], v4);
     }
   }
 };
 
-template <bool SPLIT>
+template <int WAVES>
 __global__ __launch_bounds__(kListThreads) void tensors_export_kernel(const State8Args a) {
-  const Unit w = my_unit<SPLIT>(a.l);
+  const Unit w = my_unit<WAVES>(a.l);
   float *m32 = a.m.at<float>(w.t - a.l.t0), *v32 = a.v.at<float>(w.t - a.l.t0);
-  if (m32 != nullptr) over_unit<SPLIT>(w, Export8{a.l, w, m32, v32});
+  if (m32 != nullptr) over_unit<WAVES>(w, Export8{a.l, w, m32, v32});
 }
 
 // ----------------------------------------------------------------- launches
@@ -942,16 +953,25 @@ int for_gradients(const zero_tensors_s* h, bool chunks, const void* const* grads
       });
 }
 
-// Whether four waves share a unit, a block each: with few units the waves are too
-// few to fill the chip (8-bit step over 90 units, 5.7 us against 9.9 with one
-// wave a unit; over 2048 units 9.8 against 8.6).
-constexpr int64_t kSplitUnits = 1024;
-bool split_units(const ListRange& l) { return l.u1 - l.u0 <= kSplitUnits; }
+// Waves that share a unit: four up to kFourWaveUnits, where they are too few to
+// fill the chip (8-bit step over 90 units 5.4 us, with two waves 7.1, with one
+// 10); two up to kTwoWaveUnits (over 1536 units 7.3 us, with four 8.1, with one
+// 8.1), and where so many tensors end inside a unit that the partial units,
+// whose blocks one wave takes in turn, set the time (700 tensors of 8000
+// elements 21.3 us, with one wave 26.3; of 17243, 12.4 and 14.7; but of 30001,
+// 32.2 and 29.8); else one (2048 units 8.4 us, with two 8.7; 24 thousand 63 and 68).
+constexpr int64_t kFourWaveUnits = 1024, kTwoWaveUnits = 1792, kUnitsPerPartial = 20;
+int waves_of(const zero_tensors_s* h, const ListRange& l) {
+  const int64_t units = l.u1 - l.u0;
+  if (units <= kFourWaveUnits) return 4;
+  const int64_t partial = h->partial[size_t(l.t0) + size_t(l.n)] - h->partial[size_t(l.t0)];
+  return units <= kTwoWaveUnits || units <= kUnitsPerPartial * partial ? 2 : 1;
+}
 
-// Launches kernel(args): one wave per unit, or with `split` four. lds: bytes of
-// LDS a block asks for (and does not use), which limits the waves of a CU.
-#define ZERO_LIST_LAUNCH(kernel, split, lds, args, stream)                                                          \
-  hipLaunchKernelGGL((kernel), dim3(unsigned((args).l.u1 - (args).l.u0) * ((split) ? 4u : 1u)), dim3(kListThreads), \
+// Launches kernel(args), `waves` waves per unit. lds: bytes of LDS a block asks
+// for (and does not use), which limits the waves of a CU.
+#define ZERO_LIST_LAUNCH(kernel, waves, lds, args, stream)                                                \
+  hipLaunchKernelGGL((kernel), dim3(unsigned((args).l.u1 - (args).l.u0) * unsigned(waves)), dim3(kListThreads), \
                      lds, stream, args)
 
 // LDS of the conversions' blocks, against too many waves in flight: with
@@ -978,13 +998,16 @@ unsigned step8_lds(const ListRange& l) {
 }
 
 template <typename P, typename G>
-void launch_step(bool wide, const StepArgs& a, hipStream_t stream) {
-  if (wide)
-    ZERO_LIST_LAUNCH((tensors_adamw_kernel<P, G>), true, kStep32Lds, a, stream);
-  else if (split_units(a.l))
-    ZERO_LIST_LAUNCH((tensors_adamw8_kernel<P, G, true>), true, 0, a, stream);
+void launch_step(const zero_tensors_s* h, const StepArgs& a, hipStream_t stream) {
+  const int waves = h->state_bits == 32 ? 0 : waves_of(h, a.l);
+  if (waves == 0)
+    ZERO_LIST_LAUNCH((tensors_adamw_kernel<P, G>), 4, kStep32Lds, a, stream);
+  else if (waves == 4)
+    ZERO_LIST_LAUNCH((tensors_adamw8_kernel<P, G, 4>), 4, 0, a, stream);
+  else if (waves == 2)
+    ZERO_LIST_LAUNCH((tensors_adamw8_kernel<P, G, 2>), 2, 0, a, stream);
   else
-    ZERO_LIST_LAUNCH((tensors_adamw8_kernel<P, G, false>), false, step8_lds<G>(a.l), a, stream);
+    ZERO_LIST_LAUNCH((tensors_adamw8_kernel<P, G, 1>), 1, step8_lds<G>(a.l), a, stream);
 }
 
 }  // namespace
@@ -1044,11 +1067,11 @@ int launch_adamw(const zero_tensors_s* h, const void* const* grads, const StepCo
   StepArgs a;
   a.c = c;
   return for_gradients(h, false, grads, &a, [&] {
-    const bool wide = h->state_bits == 32, bf16 = h->grad_type == ZERO_BF16;
+    const bool bf16 = h->grad_type == ZERO_BF16;
     if (h->param_type == ZERO_BF16)
-      bf16 ? launch_step<uint16_t, uint16_t>(wide, a, stream) : launch_step<uint16_t, float>(wide, a, stream);
+      bf16 ? launch_step<uint16_t, uint16_t>(h, a, stream) : launch_step<uint16_t, float>(h, a, stream);
     else
-      bf16 ? launch_step<float, uint16_t>(wide, a, stream) : launch_step<float, float>(wide, a, stream);
+      bf16 ? launch_step<float, uint16_t>(h, a, stream) : launch_step<float, float>(h, a, stream);
     return launched(who);
   });
 }
@@ -1070,14 +1093,19 @@ int launch_state8(const zero_tensors_s* h, bool import, const float* const* m, c
         wm.write(&a.m, p(m) + l.t0, l.n);
         wv.write(&a.v, p(v) + l.t0, l.n);
         const unsigned lds = import || low % 128 == 0 ? kConvertLds : kConvertLdsOffLines;
-        if (import && split_units(l))
-          ZERO_LIST_LAUNCH(tensors_import_kernel<true>, true, 0, a, stream);
+        const int waves = waves_of(h, l);
+        if (import && waves == 4)
+          ZERO_LIST_LAUNCH(tensors_import_kernel<4>, 4, 0, a, stream);
+        else if (import && waves == 2)
+          ZERO_LIST_LAUNCH(tensors_import_kernel<2>, 2, 0, a, stream);
         else if (import)
-          ZERO_LIST_LAUNCH(tensors_import_kernel<false>, false, lds, a, stream);
-        else if (split_units(l))
-          ZERO_LIST_LAUNCH(tensors_export_kernel<true>, true, 0, a, stream);
+          ZERO_LIST_LAUNCH(tensors_import_kernel<1>, 1, lds, a, stream);
+        else if (waves == 4)
+          ZERO_LIST_LAUNCH(tensors_export_kernel<4>, 4, 0, a, stream);
+        else if (waves == 2)
+          ZERO_LIST_LAUNCH(tensors_export_kernel<2>, 2, 0, a, stream);
         else
-          ZERO_LIST_LAUNCH(tensors_export_kernel<false>, false, lds, a, stream);
+          ZERO_LIST_LAUNCH(tensors_export_kernel<1>, 1, lds, a, stream);
         return launched(who);
       });
 }

@@ -55,6 +55,7 @@ struct zero_tensors_s {
   std::vector<zero_tensor> t;
   std::vector<int32_t> first[2];   // running counts of units and of chunks
   int32_t shift[2] = {0, 0};       // of their slots
+  std::vector<int32_t> partial;    // running count of tensors that end inside a unit
   std::vector<std::pair<uintptr_t, uintptr_t>> owned;   // byte ranges of the list's buffers, sorted, disjoint
   int32_t param_type = 0, grad_type = 0, state_bits = 0;
   int32_t top_group = 0;      // the largest group in use

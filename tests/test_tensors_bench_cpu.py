@@ -26,7 +26,7 @@ def test_algorithmic_bytes_of_a_list(name):
     # both moments a byte, and a scale of 4 bytes per 256 elements of a tensor, read and written
     blocks = sum((n + 255) // 256 for n in lens)
     _, _, b8 = bench.algorithmic_bytes(wl, list_bits=8)
-    assert b8["tensors_adamw8_kernel<unsigned short, unsigned short, false>"] == (2 + 2 + 8 + 4) * real + 16 * blocks
+    assert b8["tensors_adamw8_kernel<unsigned short, unsigned short, 1>"] == (2 + 2 + 8 + 4) * real + 16 * blocks
 
 
 @pytest.mark.parametrize("flags", [["--per-tensor", "--flat"], ["--per-tensor", "--accum", "2"],
