@@ -2,7 +2,7 @@
 // of device.hip, after kernels.hip.
 //
 //   tensors_upload_kernel   the list's table, out of the kernel arguments
-//   tensors_sqnorm_kernel   one partial sum of squares per unit
+//   tensors_sqnorm_kernel   one partial sum of squares per four chunks
 //   tensors_adamw_kernel    clip + AdamW + parameter cast, 32-bit state
 //   tensors_adamw8_kernel   the same with the moments in 8 bits
 //   tensors_import_kernel, tensors_export_kernel
@@ -63,8 +63,11 @@ struct Addresses {
   }
 };
 
+// base: the first chunk of the first block, at most l.u0; the chunks from there
+// to l.u0 are another launch's, which left their sum in partial[0].
 struct SqArgs {
   ListRange l;
+  int32_t base;
   double* partial;
   Addresses<ZERO_TENSORS_PER_LAUNCH> grads;
 };
@@ -509,12 +512,17 @@ struct SqChunk {
   }
 };
 
-// One wave per chunk, one partial per block.
+// One wave per chunk, one partial per block, summed wave by wave. Where a launch
+// begins inside a block's chunks, the first wave, which has none, takes the sum
+// of the ones before: the block then adds the same values in the same order as
+// if one launch held them all.
 template <typename G>
 __global__ __launch_bounds__(kSqListThreads) void tensors_sqnorm_kernel(const SqArgs a) {
-  const int64_t u = a.l.u0 + int64_t(blockIdx.x) * kSqListWaves + (threadIdx.x >> 6);
+  const int64_t u = a.base + int64_t(blockIdx.x) * kSqListWaves + (threadIdx.x >> 6);
   double acc = 0.0;
-  if (u < a.l.u1) {
+  if (u < a.l.u0) {
+    if (threadIdx.x == 0) acc = a.partial[0];
+  } else if (u < a.l.u1) {
     int start;
     const int t = find_tensor(a.l, __builtin_amdgcn_readfirstlane(int(u)), &start);
     const int64_t base = (u - start) * kSqChunk;
@@ -910,9 +918,10 @@ struct Window {
   }
 };
 
-// Calls go(range) for ranges that cover the list's units (chunks): at most `most`
-// tensors, as far as fits(t) lets tensor t join the ones before it, and
-// kListMaxUnits units each. restart() begins a new set of tensors.
+// Calls go(range) for ranges that cover the list's units (chunks): tensors of one
+// run of `most`, as far as fits(t) lets tensor t join the ones before it, and
+// kListMaxUnits units each. restart() begins a new set of tensors. The runs
+// begin at multiples of `most`, wherever the ranges between them end.
 template <typename R, typename F, typename Go>
 int for_ranges(const zero_tensors_s* h, bool chunks, int most, R restart, F fits, Go go) {
   const int32_t n = int32_t(h->t.size());
@@ -929,7 +938,7 @@ int for_ranges(const zero_tensors_s* h, bool chunks, int most, R restart, F fits
   for (int32_t t0 = 0; t0 < n;) {
     restart();
     int32_t t1 = t0;
-    while (t1 < n && t1 - t0 < most && (h->t[size_t(t1)].len == 0 || fits(t1))) ++t1;
+    while (t1 < n && (t1 == t0 || t1 % most != 0) && (h->t[size_t(t1)].len == 0 || fits(t1))) ++t1;
     const int64_t end = counts[size_t(t1)];
     for (int64_t u = counts[size_t(t0)]; u < end; u += kListMaxUnits) {
       l.t0 = t0, l.n = t1 - t0, l.u0 = int32_t(u), l.u1 = int32_t(std::min(end, u + kListMaxUnits));
@@ -1048,11 +1057,23 @@ int launch_upload(const zero_tensors_s* h, void* table, hipStream_t stream, cons
 int launch_sqnorm(const zero_tensors_s* h, const void* const* grads, double* out, int32_t accumulate, double* ws,
                   hipStream_t stream, const char* who) {
   SqArgs a;
-  int64_t n = 0;   // partial sums written
+  // The blocks hold four chunks each, counted from the first one of the launch's
+  // run of tensors: the lengths alone say which chunks share a block, also where
+  // the addresses end a launch between them.
+  const std::vector<int32_t>& counts = h->first[1];
+  int32_t run = -1;
+  int64_t first = 0, n = 0;   // partial sums before the run, and all so far
   const int rc = for_gradients(h, true, grads, &a, [&] {
-    const int64_t chunks = a.l.u1 - a.l.u0, blocks = (chunks + kSqListWaves - 1) / kSqListWaves;
-    a.partial = ws + n;
-    n += blocks;
+    if (a.l.t0 / ZERO_TENSORS_PER_LAUNCH != run) {
+      run = a.l.t0 / ZERO_TENSORS_PER_LAUNCH;
+      first = n;
+    }
+    const int64_t begin = counts[size_t(run) * ZERO_TENSORS_PER_LAUNCH];
+    const int64_t group = (a.l.u0 - begin) / kSqListWaves;
+    a.base = int32_t(begin + group * kSqListWaves);
+    const int64_t blocks = (a.l.u1 - a.base + kSqListWaves - 1) / kSqListWaves;
+    a.partial = ws + first + group;
+    n = first + group + blocks;
     if (h->grad_type == ZERO_BF16)
       hipLaunchKernelGGL(tensors_sqnorm_kernel<uint16_t>, dim3(unsigned(blocks)), dim3(kSqListThreads), 0, stream, a);
     else
