@@ -164,8 +164,9 @@ def zero_tensors(param, m, v, master=None, m_scale=None, v_scale=None, group=Non
     tensors, or one byte per element (float8_e4m3fn, uint8 or int8) with
     float32 scales, ``state8_blocks`` of them per tensor. ``group``: one index
     per tensor (default 0). ``grad_dtype``: the gradients' type (default: the
-    parameters'). The call waits until the table is written, unless the stream
-    is being captured."""
+    parameters'). The call waits until the table is written, unless a stream
+    is being captured: then the graph's replays write it, and a call outside
+    the graph reads it only after one of them."""
     import torch
 
     param = list(param)
@@ -201,9 +202,14 @@ def zero_tensors(param, m, v, master=None, m_scale=None, v_scale=None, group=Non
                      [list(c) for _, c, _, _ in columns if c is not None])
     with torch.cuda.device(device):
         nbytes = library().zero_tensors_table_bytes(h)
-        lst.table = torch.empty((nbytes + 7) // 8, dtype=torch.int64, device=device)
-        _call("zero_tensors_upload", lst, stream, lst.table.data_ptr(), nbytes)
-        if not torch.cuda.is_current_stream_capturing():
+        capturing = torch.cuda.is_current_stream_capturing()
+        # the table's memory belongs to the stream that writes it: memory that another stream
+        # has freed may still be written by that stream's pending work
+        with torch.cuda.stream(torch.cuda.ExternalStream(_stream(stream), device=device)):
+            lst.table = torch.empty((nbytes + 7) // 8, dtype=torch.int64, device=device)
+            _call("zero_tensors_upload", lst, stream, lst.table.data_ptr(), nbytes)
+            capturing = capturing or torch.cuda.is_current_stream_capturing()
+        if not capturing:
             torch.cuda.synchronize(device)
     return lst
 

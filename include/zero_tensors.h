@@ -104,7 +104,8 @@ void zero_tensors_free(zero_tensors_t h);
  * at least zero_tensors_table_bytes(h) bytes, 16-byte aligned) and bind the
  * handle to it and to the current device. The table travels in kernel
  * arguments, so the call can be captured and reads no host memory after it
- * returns. The steps read the table: order their streams after this one. The
+ * returns. The steps read the table: order their streams after this one (after
+ * a captured upload, a call outside the graph after one of its replays). The
  * table must stay as written, at that address, as long as the handle is used;
  * a second upload binds the handle to a new table.
  * Errors: ZERO_EINVAL for NULL or misaligned arguments or too few bytes;
