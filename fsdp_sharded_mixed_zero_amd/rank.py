@@ -459,28 +459,20 @@ class TensorRank(RankShard):
                                         device=dev).view(torch.bfloat16)
         self.rank_sq = torch.zeros(wl.n_d, dtype=torch.float64, device=dev)
         self.master = torch.empty(S, dtype=torch.float32, device=dev)
-        lens = [n for _, _, _, n in self.segments]
-
-        def parts(flat):
-            return [flat[d:d + n] for _, _, d, n in self.segments]
-
-        self.m, self.v = (torch.zeros(S, dtype=torch.float32, device=dev) for _ in range(2))
-        m32, v32 = self.m, self.v
-        scales = {}
+        # (tensor, its first element, the shard's, length, first scale) of each segment
+        self.parts, self.blocks = [], 0
+        for i, s, d, n in self.segments:
+            self.parts.append((i, s, d, n, self.blocks))
+            self.blocks += tensors.state8_blocks(n)
         if state_bits == 8:
-            blocks = [tensors.state8_blocks(n) for n in lens]
+            self.m = self.v = None
             self.m8, self.v8 = (torch.zeros(S, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)
                                 for _ in range(2))
-            self.m_scale, self.v_scale = (torch.zeros(sum(blocks), dtype=torch.float32, device=dev)
-                                          for _ in range(2))
-            scales = {"m_scale": list(self.m_scale.split(blocks)), "v_scale": list(self.v_scale.split(blocks))}
-        self.blocks = sum(tensors.state8_blocks(n) for n in lens)
-        self.groups = groups
-        self.list = tensors.zero_tensors(
-            [self.params[i][s:s + n] for i, s, _, n in self.segments],
-            parts(self.m8 if state_bits == 8 else self.m), parts(self.v8 if state_bits == 8 else self.v),
-            master=parts(self.master), group=None if group_of is None else [group_of(s[0]) for s in self.segments],
-            **scales)
+            self.m_scale, self.v_scale = (torch.zeros(self.blocks, dtype=torch.float32, device=dev) for _ in range(2))
+        else:
+            self.m, self.v = (torch.zeros(S, dtype=torch.float32, device=dev) for _ in range(2))
+        self.groups, self.group_of = groups, group_of
+        self.list = self._list(self.parts)
         self.grad_ptrs = zero.pointer_array([self.grads[i][s:s + n] for i, s, _, n in self.segments])
         self.workspace = torch.empty(tensors.zero_tensors_sqnorm_workspace_bytes(self.list) // 8,
                                      dtype=torch.float64, device=dev)
@@ -488,11 +480,59 @@ class TensorRank(RankShard):
             self.fill_state()
             self.fill_grads(wl.step)
             self.fill_other_ranks()
-        if state_bits == 8:      # the fp32 moments were only there to be drawn and imported
-            if fill:
-                tensors.zero_tensors_state_import(self.list, parts(m32), parts(v32))
-                torch.cuda.synchronize(dev)
-            self.m = self.v = None
+
+    def _list(self, parts):
+        """The list of these parts of the slice."""
+        def cut(flat):
+            return [flat[d:d + n] for _, _, d, n, _ in parts]
+
+        def scales(flat):
+            return [flat[b:b + tensors.state8_blocks(n)] for _, _, _, n, b in parts]
+
+        state = ({"m": cut(self.m), "v": cut(self.v)} if self.state_bits == 32 else
+                 {"m": cut(self.m8), "v": cut(self.v8), "m_scale": scales(self.m_scale),
+                  "v_scale": scales(self.v_scale)})
+        return tensors.zero_tensors([self.params[i][s:s + n] for i, s, _, n, _ in parts], master=cut(self.master),
+                                    group=None if self.group_of is None else [self.group_of(p[0]) for p in parts],
+                                    **state)
+
+    def fill_state(self, on_chunk=None):
+        """As RankShard.fill_state. Moments in 8 bits are drawn in fp32 chunk by
+        chunk and imported from there, so the whole shard's are never in
+        memory; what a chunk begins of a block goes in front of the next one."""
+        if self.state_bits == 32:
+            return super().fill_state(on_chunk)
+        wl, S, B = self.wl, self.shard, tensors.ZERO_STATE8_BLOCK
+        moments = [torch.empty(B + min(self.STATE_CHUNK, S), dtype=torch.float32, device=self.device)
+                   for _ in range(2)]
+        kept = 0         # elements in front of the chunk
+        for k, lo in enumerate(range(0, S, self.STATE_CHUNK)):
+            hi = min(S, lo + self.STATE_CHUNK)
+            bufs = [self.master[lo:hi]] + [x[kept:kept + hi - lo] for x in moments]
+            r = max(0, min(hi, self.real) - lo)
+            for x, buf_id, std, absval in zip(bufs, (synth.MASTER, synth.EXP_AVG, synth.EXP_AVG_SQ),
+                                              (wl.master_std, wl.m_std, wl.v_std), (False, False, True)):
+                x.zero_()
+                if std > 0 and r > 0:
+                    synth.device_normal_(x[:r], std, wl.seed, buf_id, abs_value=absval, salt=(self.rank << 12) + k)
+            if on_chunk is not None:
+                on_chunk(lo, hi, *bufs)
+            first, kept, ready = lo - kept, 0, []
+            for i, s, d, n, b in self.parts:
+                a, end = max(d, first), min(d + n, hi)
+                if a >= end:
+                    continue
+                if end < d + n:      # goes on in the next chunk: whole blocks now
+                    whole = d + (end - d) // B * B
+                    kept, end = end - whole, whole
+                if a < end:
+                    ready.append((i, s + a - d, a, end - a, b + (a - d) // B))
+            if ready:
+                tensors.zero_tensors_state_import(self._list(ready), *[
+                    [x[a - first:a - first + n] for _, _, a, n, _ in ready] for x in moments])
+            for x in moments:
+                x[:kept] = x[hi - first - kept:hi - first].clone()
+        torch.cuda.synchronize(self.device)
 
     def step(self, step, stream=None, timing=None, events=None, before_micro=None, phases=None):
         """One local step: the list's sum of squares, then the update. Arguments
