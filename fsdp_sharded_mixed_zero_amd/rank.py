@@ -428,11 +428,15 @@ class TensorRank(RankShard):
     zero_tensors_adamw_step over fp32 masters and moments (``state_bits=32``)
     or moments in 8 bits (``state_bits=8``: 6.06 instead of 12 bytes of state
     per parameter; "第 5 课：ZeRO 与 FSDP" section 2 counts K = 12). Master and
-    moments are slices of shard-long arrays; padding is not part of the list.
+    moments are slices of shard-long arrays (``master`` with ``m`` and ``v``,
+    or with ``m8``, ``v8``, ``m_scale`` and ``v_scale``), which may be rebound
+    between steps; padding is not part of the list.
 
     ``groups``: hyperparameter sets (zero.hparams without the step's number) by
     group index, and ``group_of(tensor)``: a tensor's group. By default one
     group with the workload's hyperparameters."""
+
+    STATE = {32: ("master", "m", "v"), 8: ("master", "m8", "v8", "m_scale", "v_scale")}
 
     def __init__(self, wl: synth.Workload, rank: int | None = None, device="cuda", fill: bool = True,
                  state_bits: int = 32, groups=None, group_of=None):
@@ -472,7 +476,8 @@ class TensorRank(RankShard):
         else:
             self.m, self.v = (torch.zeros(S, dtype=torch.float32, device=dev) for _ in range(2))
         self.groups, self.group_of = groups, group_of
-        self.list = self._list(self.parts)
+        self.list, self._bound_at = None, None
+        self._bind()
         self.grad_ptrs = zero.pointer_array([self.grads[i][s:s + n] for i, s, _, n in self.segments])
         self.workspace = torch.empty(tensors.zero_tensors_sqnorm_workspace_bytes(self.list) // 8,
                                      dtype=torch.float64, device=dev)
@@ -480,6 +485,20 @@ class TensorRank(RankShard):
             self.fill_state()
             self.fill_grads(wl.step)
             self.fill_other_ranks()
+
+    def _bind(self):
+        """Make the list again if a state array was rebound (a restored checkpoint)."""
+        arrays = {k: getattr(self, k) for k in self.STATE[self.state_bits]}
+        at = [a.data_ptr() for a in arrays.values()]
+        if at == self._bound_at:
+            return
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("a state array was rebound: run a step before capturing one")
+        for k, a in arrays.items():
+            n = self.blocks if "scale" in k else self.shard
+            if a.shape != (n,):
+                raise ValueError(f"{k} has shape {tuple(a.shape)}, the rank's has ({n},)")
+        self.list, self._bound_at = self._list(self.parts), at
 
     def _list(self, parts):
         """The list of these parts of the slice."""
@@ -538,6 +557,7 @@ class TensorRank(RankShard):
         """One local step: the list's sum of squares, then the update. Arguments
         as RankShard.step (phases "sqnorm" and "adamw")."""
         wl = self.wl
+        self._bind()
         if stream is None:
             stream = torch.cuda.current_stream()
         on = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
