@@ -450,8 +450,6 @@ class TensorRank(RankShard):
         self.segments = self.layout.segments
         self.shard = S = self.info["shard"]
         self.real = S - (self.info["pad_end"] - self.info["pad_begin"])
-        if not self.segments:
-            raise ValueError("the rank's shard holds padding only: there is no tensor to update")
         self.bucket, self.bucketed, self.n_streams, self.streams = 0, False, 1, []
         self.flat, self.fused_norm, self.fused_unpack, self.accum_steps = False, False, False, 1
         self.state, self.state_arrays, self.state_bits = None, True, state_bits
@@ -478,7 +476,7 @@ class TensorRank(RankShard):
         self.groups, self.group_of = groups, group_of
         self.list, self._bound_at = None, None
         self._bind()
-        self.grad_ptrs = zero.pointer_array([self.grads[i][s:s + n] for i, s, _, n in self.segments])
+        self.grad_ptrs = zero.pointer_array([self.grads[i][s:s + n] for i, s, _, n in self.segments] or [None])
         self.workspace = torch.empty(tensors.zero_tensors_sqnorm_workspace_bytes(self.list) // 8,
                                      dtype=torch.float64, device=dev)
         if fill:
@@ -501,7 +499,11 @@ class TensorRank(RankShard):
         self.list, self._bound_at = self._list(self.parts), at
 
     def _list(self, parts):
-        """The list of these parts of the slice."""
+        """The list of these parts of the slice; of a shard of padding only, one tensor without elements."""
+        if not parts:
+            none = torch.empty(0, dtype=torch.float32 if self.state_bits == 32 else torch.uint8, device=self.device)
+            return tensors.zero_tensors([none.to(torch.bfloat16)], [none], [none])
+
         def cut(flat):
             return [flat[d:d + n] for _, _, d, n, _ in parts]
 
