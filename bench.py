@@ -27,7 +27,9 @@ BREAKDOWN_MIN_STEPS = 100     # steps with events around every phase, before the
 BREAKDOWN_MIN_SECONDS = 1.0   # ... and at least this much wall time
 ROOT = os.path.dirname(os.path.abspath(__file__))
 sys.path.insert(0, ROOT)
-KERNEL_SOURCE = os.path.join(ROOT, "fsdp_sharded_mixed_zero_amd", "csrc", "kernels.hip")
+CSRC = os.path.join(ROOT, "fsdp_sharded_mixed_zero_amd", "csrc")
+KERNEL_SOURCE = os.path.join(CSRC, "kernels.hip")
+LIST_SOURCES = ("kernels.hip", "tensors.hip", "tensors_internal.h")   # of the kernels over a list of tensors
 PROFILES = os.path.join(ROOT, "profiles")
 
 
@@ -205,12 +207,21 @@ def code_text(text):
     return " ".join("".join(out).split())
 
 
-def source_hash():
+def source_hash(lists=False):
     """sha256 of the kernels' code (comments and blank space aside): the
-    counters of a profile stay valid across comment edits, not code edits."""
+    counters of a profile stay valid across comment edits, not code edits.
+    ``lists``: of every source of the kernels over a list of tensors."""
     import hashlib
-    with open(KERNEL_SOURCE, encoding="utf-8") as f:
-        return hashlib.sha256(code_text(f.read()).encode()).hexdigest()
+    h = hashlib.sha256()
+    for path in [os.path.join(CSRC, name) for name in LIST_SOURCES] if lists else [KERNEL_SOURCE]:
+        with open(path, encoding="utf-8") as f:
+            h.update(code_text(f.read()).encode())
+    return h.hexdigest()
+
+
+def hash_line(lists=False):
+    names = ", ".join(LIST_SOURCES) if lists else os.path.basename(KERNEL_SOURCE)
+    return f"{names} code sha256 (comments and blank space aside): `{source_hash(lists)}`"
 
 
 def traffic_file(workload):
@@ -354,7 +365,7 @@ def stats_summary(stats_dir, wl, steps, warmup, accum=1, separate_norm=False, fl
              f"--no-cpu-baseline --no-copy-ceiling",
              f"    cd $R && python bench.py --workload {wl.name} --steps {steps} --warmup {warmup}{mode} "
              f"--stats-summary {stats_dir}", "",
-             f"kernels.hip code sha256 (comments and blank space aside): `{source_hash()}`", "",
+             hash_line(bool(list_bits)), "",
              f"{steps_run:.0f} steps traced; bytes per launch = the step's algorithmic bytes for that "
              f"kernel divided by its launches per step. The {n_setup} launches of each sum-of-squares "
              f"kernel that set up the other ranks' partial sums come first and are left out.", "",
@@ -430,7 +441,7 @@ def update_sweep(wl, reps=20):
     lines = [f"# The fused update against its size: {wl.name}, rank {wl.rank} of N_d={wl.n_d}", "",
              "Command (one MI355X; R is the repository root):", "",
              f"    cd $R && python3 bench.py --workload {wl.name} --update-sweep", "",
-             f"kernels.hip code sha256 (comments and blank space aside): `{source_hash()}`", "",
+             hash_line(), "",
              f"zero_adamw_step_unpack over shard elements [0, n), {reps} launches each, HIP events around each "
              f"launch, median. Fit: time = {fixed:.1f} us + bytes / {1e-3 / slope:.1f} GB/s "
              f"({100 * 1e-3 / slope / HBM_PEAK_GBPS:.1f} % of 8 TB/s).", "",
