@@ -328,6 +328,16 @@ def stats_summary(stats_dir, wl, steps, warmup, accum=1, separate_norm=False, fl
         for r in csv.DictReader(open(tpath)):
             spans.setdefault(kernel_name(r["Kernel_Name"]), []).append(
                 (int(r["Start_Timestamp"]), int(r["End_Timestamp"])))
+    if list_bits == 8:
+        # the last template argument is how many waves share a unit: by the list's length, and a
+        # list of several launches may take several
+        pinned = update_kernel(list_bits=8)
+        stem = pinned.rsplit(",", 1)[0]
+        waves = sorted(k for k in spans if k.startswith(stem))
+        if waves:
+            key = f"{stem}, {' or '.join(k[len(stem) + 2:-1] for k in waves)}>"
+            spans[key] = [iv for k in waves for iv in spans.pop(k)]
+            algo[key] = algo.pop(pinned)
     n_setup = setup_sqnorm_launches(wl)
     for k in spans:
         spans[k].sort()

@@ -1,5 +1,5 @@
 """The summaries of a profile of the step over a list of tensors: which code
-they are of."""
+they are of, and the 8-bit update's bytes however many waves share a unit."""
 
 import os
 import shutil
@@ -48,3 +48,17 @@ def test_a_list_profile_names_the_code_of_its_kernels(tmp_path, monkeypatch, cha
     path.write_text(text + "\nint one_more;\n", encoding="utf-8")
     assert line[0] not in summary(tmp_path, [update], wl, 32)
     assert (bench.source_hash() == flat) == (changed != "kernels.hip")
+
+
+@pytest.mark.parametrize("waves", [(1,), (2,), (4,), (1, 4)])
+def test_the_8_bit_update_has_its_bytes(tmp_path, waves):
+    wl = synth.WORKLOADS["tiny"]
+    md = summary(tmp_path, [f"tensors_adamw8_kernel<unsigned short, unsigned short, {w}>({NS}StepArgs)" for w in waves],
+                 wl, 8)
+    _, _, algo = bench.algorithmic_bytes(wl, list_bits=8)
+    want = algo["tensors_adamw8_kernel<unsigned short, unsigned short, 1>"]
+    rows = [[c.strip() for c in line.split("|")[1:-1]] for line in md.splitlines() if line.startswith("| tensors_adamw8")]
+    assert len(rows) == 1 and all(f" {w}" in rows[0][0] for w in waves)
+    assert int(rows[0][1]) == 3 * len(waves) and float(rows[0][2]) == len(waves)
+    assert int(rows[0][6]) == int(want / len(waves))
+    assert float(rows[0][9]) == pytest.approx(2.0 * len(waves))
