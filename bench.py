@@ -61,7 +61,8 @@ def parse():
                     help="the rank's slice as a list of tensors (zero_tensors_sqnorm, zero_tensors_adamw_step): "
                          "gradients read and parameters written in place, no pack, no unpack")
     ap.add_argument("--state-bits", type=int, choices=(32, 8), default=32,
-                    help="with --per-tensor: moments in fp32, or in 8 bits (e4m3, one scale per 256 elements)")
+                    help="with --per-tensor: moments in fp32, or in 8 bits (e4m3, one scale per 256 elements; the "
+                         "second moment follows AdamW's over many steps up to beta2 = 0.95)")
     ap.add_argument("--offload", action="store_true",
                     help="ZeRO-Offload: fp32 state in host memory, AdamW on the host cores")
     ap.add_argument("--offload-bucket", type=int, default=1 << 24, metavar="N",

@@ -40,6 +40,8 @@ unpack): sum of squares -> clip + AdamW + bf16 cast.
 
 from __future__ import annotations
 
+import warnings
+
 import torch
 
 from . import synth, tensors, zero
@@ -432,8 +434,11 @@ class TensorRank(RankShard):
     or with ``m8``, ``v8``, ``m_scale`` and ``v_scale``), which may be rebound
     between steps; padding is not part of the list.
 
-    ``groups``: hyperparameter sets (zero.hparams without the step's number) by
-    group index, and ``group_of(tensor)``: a tensor's group. By default one
+    The 8-bit second moment follows AdamW's up to beta2 = 0.95 or so, not at
+    0.999 (include/zero_tensors.h): a rank made with more than 0.95 warns.
+
+    ``groups``: hyperparameter sets by group index, each a dict of
+    zero.hparams' arguments without the step's number, and ``group_of(tensor)``: a tensor's group. By default one
     group with the workload's hyperparameters."""
 
     STATE = {32: ("master", "m", "v"), 8: ("master", "m8", "v8", "m_scale", "v_scale")}
@@ -442,6 +447,10 @@ class TensorRank(RankShard):
                  state_bits: int = 32, groups=None, group_of=None):
         if state_bits not in (32, 8):
             raise ValueError("state_bits is 32 or 8")
+        betas = [wl.beta2] if groups is None else [zero.hparams(**g).beta2 for g in groups]
+        if state_bits == 8 and max(betas) > 0.95:
+            warnings.warn(f"beta2 = {max(betas):g} with moments in 8 bits: the second moment stops following the "
+                          "gradients over many steps; use at most 0.95, or fp32 moments", stacklevel=2)
         self.wl = wl
         self.rank = wl.rank if rank is None else rank
         self.device = dev = torch.device(device)

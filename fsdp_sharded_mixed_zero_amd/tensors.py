@@ -162,7 +162,9 @@ def zero_tensors(param, m, v, master=None, m_scale=None, v_scale=None, group=Non
     """Describe a list and write its table. ``param``: bfloat16 tensors, with
     float32 ``master`` tensors, or float32 ones without. ``m``, ``v``: float32
     tensors, or one byte per element (float8_e4m3fn, uint8 or int8) with
-    float32 scales, ``state8_blocks`` of them per tensor. ``group``: one index
+    float32 scales, ``state8_blocks`` of them per tensor (for a beta2 of up to
+    0.95: beyond, the 8-bit second moment does not follow its gradients over
+    many steps). ``group``: one index
     per tensor (default 0). ``grad_dtype``: the gradients' type (default: the
     parameters'). The call waits until the table is written, unless a stream
     is being captured: then the graph's replays write it, and a call outside
@@ -270,7 +272,8 @@ def group_array(hp):
 
 
 def zero_tensors_adamw_step(lst: TensorList, tensor_grads, hp, rank_sqnorms, n_ranks: int, stream=None):
-    """``hp``: one zero.hparams, or a list of them, one per group."""
+    """``hp``: one zero.hparams, or a list of them, one per group. With an 8-bit
+    state, beta2 up to 0.95 (include/zero_tensors.h, "Over many steps")."""
     arr = _pointers(lst, tensor_grads, lst.grad_dtype, "gradient")
     groups = group_array(hp)
     if n_ranks > 0:

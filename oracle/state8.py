@@ -5,7 +5,9 @@ The pages keep the optimizer state at K = 12 bytes per parameter in fp32
 ("第 5 课：ZeRO 与 FSDP", section 2) and give no 8-bit form, so the definition is
 this library's own: m and sqrt(v) as OCP e4m3 values with one fp32 scale per
 256 consecutive elements of a tensor (include/zero_tensors.h). The rest is
-AdamW as in ``oracle.step``.
+AdamW as in ``oracle.step``. Rounding to nearest keeps a root that moves by
+less than half a step of its byte: one update is AdamW's on the state it finds,
+a chain of them only up to beta2 = 0.95 or so.
 """
 
 from __future__ import annotations
