@@ -196,8 +196,10 @@ def zero_tensors(param, m, v, master=None, m_scale=None, v_scale=None, group=Non
     if group is not None and len(group) != len(lens):
         raise ValueError(f"group: {len(group)} entries for a list of {len(lens)} tensors")
     for i, (rec, n) in enumerate(zip(arr, lens)):
-        rec.len = n
-        rec.group = int(group[i]) if group is not None else 0
+        k = int(group[i]) if group is not None else 0
+        if not -(1 << 31) <= k < 1 << 31:       # the record would hold another one
+            raise ValueError(f"group {k} of tensor {i} outside [0, {ZERO_TENSOR_GROUPS})")
+        rec.len, rec.group = n, k
     h = _VP()
     zero._check("zero_tensors", library().zero_tensors(arr, len(lens), p_type, g_type, bits, ctypes.byref(h)))
     lst = TensorList(h.value, lens, grad_dtype, bits, device, None,
