@@ -159,7 +159,8 @@ int zero_tensors_sqnorm(zero_tensors_t h, const void* const* tensor_grads, doubl
  * under the division. Where a denominator is too small for fp32 to resolve its
  * root (eps = 0 and small roots, or very different ones in a block), the update
  * is evaluated in fp64. A moment that is NaN, or infinite in fp32, is stored as
- * the e4m3 NaN and left out of the maxima, so it spoils its own element only.
+ * the e4m3 NaN and left out of the maxima, so it spoils its own element only;
+ * the step of an element whose second moment is infinite in fp32 is zero.
  *
  * Over many steps: rounding to nearest returns a root to its byte unless a step
  * changes it by half a step of e4m3, 1/30 to 1/16 of itself. It changes by
