@@ -995,15 +995,16 @@ constexpr unsigned kConvertLds = 10 << 10, kConvertLdsOffLines = 16 << 10;
 // 110.3).
 constexpr unsigned kStep32Lds = 8 << 10;
 
-// LDS of the 8-bit step's blocks in long launches, against too many waves in
-// flight. By the kernel's registers a CU holds 16; 12 (13 KiB) with bf16
-// gradients and 10 (16 KiB) with fp32 ones are faster from some 2^26 elements
-// on: 105 M, 284 us without and 277 us, 323 and 307; 119 M, 330 and 324, 377
-// and 359; but 47 M, 138.4 and 139.8, 154.1 and 156.1.
+// LDS of the 8-bit step's blocks in long launches with fp32 gradients, against
+// too many waves in flight: by the kernel's registers a CU holds 16; with 16 KiB,
+// 10. By the elements of 100 equal tensors, with and without it: 2^25.9, 174 us
+// and 168; 2^26.1, 204 and 205; 2^26.5, 278 and 285; 2^27, 387 and 404. Lists of
+// several shapes at 84 to 119 M elements gain 1 % in the mean (-3 to 4 %). With
+// bf16 gradients, 12 waves gained nothing over the same lists (within 3 %).
 constexpr int64_t kLongUnits = int64_t(1) << 16;
 template <typename G>
 unsigned step8_lds(const ListRange& l) {
-  return l.u1 - l.u0 <= kLongUnits ? 0u : sizeof(G) == 2 ? 13u << 10 : 16u << 10;
+  return sizeof(G) == 2 || l.u1 - l.u0 <= kLongUnits ? 0u : 16u << 10;
 }
 
 template <typename P, typename G>
