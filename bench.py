@@ -368,7 +368,7 @@ def stats_summary(stats_dir, wl, steps, warmup, accum=1, separate_norm=False, fl
             (" --state-arrays" if state_arrays else "") +
             (f" --per-tensor --state-bits {list_bits}" if list_bits else ""))
     lines = [f"# Kernel durations: {wl.name}, rank {wl.rank} of N_d={wl.n_d} "
-             f"(shard {S} elements{f', buckets of {wl.bucket}' if wl.bucket else ''})", "",
+             f"(shard {S} elements{f', buckets of {wl.bucket}' if wl.bucket and not list_bits else ''})", "",
              "Commands (one MI355X; R is the repository root):", "",
              "    cd /tmp && export TMPDIR=/tmp",
              f"    timeout -k 10 600 rocprofv3 --kernel-trace --stats --output-format csv -d $R/{stats_dir} -o bench -- "

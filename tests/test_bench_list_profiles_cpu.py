@@ -62,3 +62,11 @@ def test_the_8_bit_update_has_its_bytes(tmp_path, waves):
     assert int(rows[0][1]) == 3 * len(waves) and float(rows[0][2]) == len(waves)
     assert int(rows[0][6]) == int(want / len(waves))
     assert float(rows[0][9]) == pytest.approx(2.0 * len(waves))
+
+
+def test_a_list_has_no_buckets(tmp_path):
+    """The step over a list is not cut into the workload's buckets."""
+    wl = synth.WORKLOADS["llama-70b"]
+    assert wl.bucket > 0
+    md = summary(tmp_path, [f"tensors_adamw_kernel<unsigned short, unsigned short>({NS}StepArgs)"], wl, 32)
+    assert "buckets" not in md and "3 steps traced" in md
