@@ -107,7 +107,8 @@ __device__ __forceinline__ T uniform_load(const T* p) {
 // its first unit. The 64 lanes compare 64 consecutive entries, from the slot's
 // tensor on, as often as all of them are at or below u (the counts ascend).
 // (64 entries spaced over a launch's tensors, then the rest between two of them,
-// touch a cache line a lane: the 32-bit step over 868 tensors 544 us against 535.)
+// touch a cache line a lane: the 32-bit step over 868 tensors 544 us against 535
+// when the slots were chosen; with what came after them it takes 522.)
 __device__ __forceinline__ int find_tensor(const ListRange& l, int u, int* start) {
   int lo = l.n_all <= 64 ? 0 : uniform_load(l.slot + (u >> l.shift));
   const int lane = threadIdx.x & 63;
@@ -326,7 +327,8 @@ __device__ __forceinline__ uint32_t decide(uint32_t down, uint32_t up, F exact) 
 
 // The fp32 values that are rounded to bytes are off by at most 2^-22 of
 // themselves: the bytes of x * (1 - 2^-21) and x * (1 + 2^-21) agree unless a
-// border is that near (one element in 10^5).
+// border is that near (one element in 10^5). Roots of zero are not rare where
+// rows get no gradients, and v_bytes looks at each of them again.
 constexpr float kBelow = 1.f - 0x1p-21f, kAbove = 1.f + 0x1p-21f;
 
 template <int CTRL>
@@ -437,7 +439,10 @@ __device__ __forceinline__ uint32_t m_bytes(const float mf[4], float up, F exact
 
 // sqrt(v), in units of the scale, to bytes; y[k]: that root in fp32, for the
 // update, off by up to 2^-63 units where its square is subnormal. vf: fp32 of
-// v; exact(k): the fp64 v[k].
+// v; exact(k): the fp64 v[k], which every zero byte asks for, and every element
+// of a block of tiny roots or of zeros only. In the step it comes from memory
+// again: 24.3 M elements take 72 us, 98 with half of the blocks zero and 131
+// with all of them (119 M, fp32 gradients: 361, 563, 787).
 template <typename F>
 __device__ __forceinline__ uint32_t v_bytes(const float vf[4], float up, float y[4], F exact) {
   const auto square = [&](int j) { return exact(j) * (double(up) * double(up)); };
