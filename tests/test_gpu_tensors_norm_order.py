@@ -101,3 +101,27 @@ def test_missing_gradients_far_apart(arena):
     want = norm(lst, gone(place(arena, torch.bfloat16, grads, [False] * len(LENS))))
     for _, far in patterns(len(LENS)):
         assert norm(lst, gone(place(arena, torch.bfloat16, grads, far))) == want
+
+
+def test_far_apart_from_a_graph(arena):
+    """Replays, whatever the workspace holds before each, between eager norms of the same gradients near each other."""
+    far = [i % 2 == 1 for i in range(len(LENS))]
+    grads, lst = make(LENS, "bf16", 7)
+    ws = torch.empty(tensors.zero_tensors_sqnorm_workspace_bytes(lst) // 8, dtype=torch.float64, device=DEV)
+    out = torch.zeros(1, dtype=torch.float64, device=DEV)
+    views = place(arena, torch.bfloat16, grads, far)
+    ptrs = zero.pointer_array([g if g.numel() else None for g in views])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        tensors.zero_tensors_sqnorm(lst, ptrs, out, False, ws)
+    for k in range(4):
+        for x, g in zip(views, grads):
+            g.mul_(-0.5 - k)
+            x.copy_(g)
+        ws.fill_(float("nan") if k % 2 else 1e30)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.item()
+        near = [g.clone() for g in grads]
+        assert norm(lst, near) == got
