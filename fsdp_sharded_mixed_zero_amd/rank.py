@@ -432,14 +432,16 @@ class TensorRank(RankShard):
     per parameter; "第 5 课：ZeRO 与 FSDP" section 2 counts K = 12). Master and
     moments are slices of shard-long arrays (``master`` with ``m`` and ``v``,
     or with ``m8``, ``v8``, ``m_scale`` and ``v_scale``), which may be rebound
-    between steps; padding is not part of the list.
+    between steps (a graph captured before goes on with the arrays of then);
+    padding is not part of the list.
 
     The 8-bit second moment follows AdamW's up to beta2 = 0.95 or so, not at
     0.999 (include/zero_tensors.h): a rank made with more than 0.95 warns.
 
     ``groups``: hyperparameter sets by group index, each a dict of
-    zero.hparams' arguments without the step's number, and ``group_of(tensor)``: a tensor's group. By default one
-    group with the workload's hyperparameters."""
+    zero.hparams' arguments without the step's number, and
+    ``group_of(tensor)``: a tensor's group. By default one group with the
+    workload's hyperparameters."""
 
     STATE = {32: ("master", "m", "v"), 8: ("master", "m8", "v8", "m_scale", "v_scale")}
 
@@ -483,7 +485,7 @@ class TensorRank(RankShard):
         else:
             self.m, self.v = (torch.zeros(S, dtype=torch.float32, device=dev) for _ in range(2))
         self.groups, self.group_of = groups, group_of
-        self.list, self._bound_at = None, None
+        self.list, self._bound_at, self._tables = None, None, []
         self._bind()
         self.grad_ptrs = zero.pointer_array([self.grads[i][s:s + n] for i, s, _, n in self.segments] or [None])
         self.workspace = torch.empty(tensors.zero_tensors_sqnorm_workspace_bytes(self.list) // 8,
@@ -506,6 +508,7 @@ class TensorRank(RankShard):
             if a.shape != (n,):
                 raise ValueError(f"{k} has shape {tuple(a.shape)}, the rank's has ({n},)")
         self.list, self._bound_at = self._list(self.parts), at
+        self._tables.append(self.list.table)      # for good: a graph captured with an earlier list reads its table
 
     def _list(self, parts):
         """The list of these parts of the slice; of a shard of padding only, one tensor without elements."""

@@ -164,9 +164,8 @@ def zero_tensors(param, m, v, master=None, m_scale=None, v_scale=None, group=Non
     tensors, or one byte per element (float8_e4m3fn, uint8 or int8) with
     float32 scales, ``state8_blocks`` of them per tensor (for a beta2 of up to
     0.95: beyond, the 8-bit second moment does not follow its gradients over
-    many steps). ``group``: one index
-    per tensor (default 0). ``grad_dtype``: the gradients' type (default: the
-    parameters'). The call waits until the table is written, unless a stream
+    many steps). ``group``: one index per tensor (default 0). ``grad_dtype``:
+    the gradients' type (default: the parameters'). The call waits until the table is written, unless a stream
     is being captured: then the graph's replays write it, and a call outside
     the graph reads it only after one of them."""
     import torch

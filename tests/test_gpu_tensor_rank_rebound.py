@@ -59,3 +59,28 @@ def test_rebound_arrays_are_refused_while_capturing():
     torch.cuda.synchronize()
     b.step(ODD.step)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_graph_captured_before_goes_on_with_its_arrays(bits):
+    """Its list's table is still there after the rank's list was made again and memory given out."""
+    a, b = TensorRank(ODD, state_bits=bits), TensorRank(ODD, state_bits=bits)
+    a.step(ODD.step)
+    b.step(ODD.step)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.step(ODD.step)
+    old = {k: getattr(b, k) for k in NAMES[bits]}
+    size = b.list.table.numel()
+    for k in NAMES[bits]:
+        setattr(b, k, old[k].clone())
+    b.step(ODD.step)
+    filled = [torch.full((size,), -1, dtype=torch.int64, device="cuda") for _ in range(8)]
+    for _ in range(3):
+        a.step(ODD.step)
+        graph.replay()
+        torch.cuda.synchronize()
+        for k in NAMES[bits]:
+            assert torch.equal(getattr(a, k).view(torch.uint8), old[k].view(torch.uint8)), k
+    assert all(int(f.min()) == -1 for f in filled)
