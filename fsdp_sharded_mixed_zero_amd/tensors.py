@@ -226,7 +226,9 @@ def zero_tensors_table_bytes(lst: TensorList) -> int:
 
 
 def zero_tensors_upload(lst: TensorList, table, table_bytes: int | None = None, stream=None) -> None:
-    """Write the list's table into ``table`` and bind the list to it."""
+    """Write the list's table into ``table`` and bind the list to it. The table
+    before (``lst.table``) has to be kept as long as a graph captured with it
+    may be replayed."""
     if table_bytes is None:
         table_bytes = table.numel() * table.element_size()
     zero._need(table, table_bytes, "table")
