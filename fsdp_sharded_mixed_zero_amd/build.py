@@ -23,7 +23,7 @@ LIB_NAME = "libzero_mi355x.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 ARCH = "gfx950"
 
-SOURCES = ["layout.cpp", "offload.cpp", "tensors.cpp", "device.hip"]
+SOURCES = ["layout.cpp", "offload.cpp", "tensors.cpp", "layers.cpp", "device.hip"]
 
 
 def hipcc() -> str:

@@ -2,3 +2,4 @@
 // use the conversions, sums, clip coefficient and update of the flat ones.
 #include "kernels.hip"
 #include "tensors.hip"
+#include "layers.hip"
