@@ -130,7 +130,7 @@ extern "C" int zero_embedding(const void* tokens, int32_t token_type, int64_t n,
 
 extern "C" size_t zero_token_order_bytes(int64_t n, int64_t rows) {
   if (n < 0 || n > ZERO_LAYER_ROWS || rows < 1 || rows > ZERO_LAYER_ROWS) return 0;
-  return size_t(zero::Order(n, rows).words) * sizeof(int32_t);
+  return size_t(zero::Order(n).words) * sizeof(int32_t);
 }
 
 extern "C" int zero_token_order(const void* tokens, int32_t token_type, int64_t n, int64_t rows, void* order,
@@ -151,8 +151,7 @@ extern "C" int zero_token_order(const void* tokens, int32_t token_type, int64_t 
 
 extern "C" size_t zero_embedding_grad_workspace_bytes(int64_t n, int64_t dim) {
   if (!sizes_fit(n, dim)) return 0;
-  const int64_t pieces = std::max<int64_t>(1, (n + zero::kPiece - 1) / zero::kPiece);
-  return size_t(pieces) * 2 * size_t((dim + 3) / 4 * 4) * sizeof(float);
+  return size_t(std::max<int64_t>(1, zero::embedding_pieces(n))) * 2 * size_t((dim + 3) / 4 * 4) * sizeof(float);
 }
 
 extern "C" int zero_embedding_grad(const void* order, int64_t n, int64_t rows, int64_t dim, const void* d_out,

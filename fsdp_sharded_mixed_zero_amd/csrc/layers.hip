@@ -12,11 +12,12 @@
 //                            the norm of rows in registers, and of longer ones
 //   norm_grad_kernel, norm_grad_long_kernel, norm_grad_columns_kernel,
 //   norm_grad_join_kernel    its gradient
+#include <type_traits>
+
 #include "layers_internal.h"
 
 namespace {
 
-using zero::kPiece;
 using zero::kSortBits;
 using zero::kSortBlock;
 using zero::kSortDigits;
@@ -27,10 +28,24 @@ using zero::Order;
 
 // ------------------------------------------------------- E elements of a row
 //
-// A lane owns E consecutive elements, of which `cnt` exist (fewer than E at a
-// row's end only, none beyond). Rows start at any element, so the accesses are
-// declared with their element's alignment: the hardware takes them at any
-// address.
+// A row is cut into vectors of E elements, one a lane. Its last lane takes the
+// row's last E elements, of which the first `lo` are the neighbour's: so every
+// lane's load is one instruction that no branch guards (a guarded one has to wait
+// for those before it), also of a lane with nothing to do, whose lo is E. Rows
+// start at any element, so the accesses are declared with their element's
+// alignment: the hardware takes them at any address. A row shorter than a vector
+// goes element by element.
+
+struct Span {
+  int col, lo, hi;     // elements [col + lo, col + hi) of the row are the lane's
+};
+template <int E>
+__device__ __forceinline__ Span span_of(int vector, int dim) {
+  const int col = vector * E;
+  if (dim < E) return {0, 0, vector == 0 ? dim : 0};
+  const int over = max(0, col + E - dim);
+  return {col - over, min(over, E), E};
+}
 
 template <int E, typename T> struct Words;
 template <> struct Words<8, uint16_t> { u32x4 w; };
@@ -41,25 +56,43 @@ template <> struct Words<8, float> { f32x4 w, w2; };
 template <typename V>
 __device__ __forceinline__ V plain_load(const void* p) { return *(const ZERO_GLOBAL V*)p; }
 
-template <int E, bool STREAM = true, typename T>
-__device__ __forceinline__ Words<E, T> load_row(const T* p, int cnt) {
+template <int E, bool STREAM, typename T>
+__device__ __forceinline__ Words<E, T> load_vector(const T* p) {
   Words<E, T> r;
-  if (cnt >= E) {
-    if constexpr (sizeof(T) == 2 && E == 8) r.w = STREAM ? stream_load<words4_any>(p) : plain_load<words4_any>(p);
-    else if constexpr (sizeof(T) == 2) r.w = STREAM ? stream_load<bf16x4_any>(p) : plain_load<bf16x4_any>(p);
-    else r.w = STREAM ? stream_load<f32x4_any>(p) : plain_load<f32x4_any>(p);
-    if constexpr (sizeof(T) == 4 && E == 8) r.w2 = STREAM ? stream_load<f32x4_any>(p + 4) : plain_load<f32x4_any>(p + 4);
-    return r;
-  }
-  r = Words<E, T>{};
+  if constexpr (sizeof(T) == 2 && E == 8) r.w = STREAM ? stream_load<words4_any>(p) : plain_load<words4_any>(p);
+  else if constexpr (sizeof(T) == 2) r.w = STREAM ? stream_load<bf16x4_any>(p) : plain_load<bf16x4_any>(p);
+  else r.w = STREAM ? stream_load<f32x4_any>(p) : plain_load<f32x4_any>(p);
+  if constexpr (sizeof(T) == 4 && E == 8) r.w2 = STREAM ? stream_load<f32x4_any>(p + 4) : plain_load<f32x4_any>(p + 4);
+  return r;
+}
+
+// The elements [lo, hi) of the E at p, zeros beside them.
+template <int E, typename T>
+__device__ __forceinline__ Words<E, T> load_some(const T* p, int lo, int hi) {
+  Words<E, T> r{};
 #pragma unroll
-  for (int k = 0; k < E - 1; ++k) {
-    if (k >= cnt) continue;
+  for (int k = 0; k < E; ++k) {
+    if (k < lo || k >= hi) continue;
     if constexpr (sizeof(T) == 2) r.w[k >> 1] |= uint32_t(p[k]) << (16 * (k & 1));
     else if constexpr (E == 8) { if (k < 4) r.w[k & 3] = p[k]; else r.w2[k & 3] = p[k]; }
     else r.w[k] = p[k];
   }
   return r;
+}
+
+// The lane's vector of the row at p, the neighbour's elements included.
+template <int E, bool STREAM = true, typename T>
+__device__ __forceinline__ Words<E, T> load_row(const T* p, const Span& s, int dim) {
+  if (dim >= E) return load_vector<E, STREAM>(p + s.col);
+  return load_some<E, T>(p, 0, s.hi);
+}
+
+// The neighbour's elements zeroed.
+template <int E>
+__device__ __forceinline__ void only_own(const Span& s, float (&x)[E]) {
+  if (s.lo > 0)
+#pragma unroll
+    for (int k = 0; k < E; ++k) x[k] = k < s.lo ? 0.f : x[k];
 }
 
 template <int E, typename T>
@@ -85,6 +118,13 @@ __device__ __forceinline__ Words<E, T> narrow(const float (&x)[E]) {
   return r;
 }
 
+// The words as if just read: what was computed from them before is not kept.
+template <int E, typename T>
+__device__ __forceinline__ void opaque(Words<E, T>& r) {
+  asm volatile("" : "+v"(r.w));
+  if constexpr (sizeof(T) == 4 && E == 8) asm volatile("" : "+v"(r.w2));
+}
+
 // The elements [lo, cnt) of the lane's E.
 template <int E, typename T>
 __device__ __forceinline__ void store_some(T* p, int lo, int cnt, const Words<E, T>& r) {
@@ -97,12 +137,8 @@ __device__ __forceinline__ void store_some(T* p, int lo, int cnt, const Words<E,
   }
 }
 
-template <int E, bool STREAM = true, typename T>
-__device__ __forceinline__ void store_row(T* p, int cnt, const Words<E, T>& r) {
-  if (cnt < E) {
-    store_some<E, T>(p, 0, cnt, r);
-    return;
-  }
+template <int E, bool STREAM, typename T>
+__device__ __forceinline__ void store_vector(T* p, const Words<E, T>& r) {
   if constexpr (STREAM) {
     if constexpr (sizeof(T) == 2 && E == 8) stream_store<words4_any>(p, r.w);
     else if constexpr (sizeof(T) == 2) stream_store<bf16x4_any>(p, r.w);
@@ -114,6 +150,12 @@ __device__ __forceinline__ void store_row(T* p, int cnt, const Words<E, T>& r) {
     else *(ZERO_GLOBAL f32x4_any*)p = r.w;
     if constexpr (sizeof(T) == 4 && E == 8) *(ZERO_GLOBAL f32x4_any*)(p + 4) = r.w2;
   }
+}
+
+template <int E, bool STREAM = true, typename T>
+__device__ __forceinline__ void store_row(T* p, const Span& s, const Words<E, T>& r) {
+  if (s.lo == 0 && s.hi == E) store_vector<E, STREAM>(p + s.col, r);
+  else store_some<E, T>(p + s.col, s.lo, s.hi, r);
 }
 
 // ------------------------------------------------------------------- lookup
@@ -135,92 +177,82 @@ template <typename T, typename O, int E>
 __global__ __launch_bounds__(256) void embedding_kernel(const void* __restrict__ tokens, int wide, int n,
                                                         const T* __restrict__ table, int rows, int dim, int tiles,
                                                         float scale, O* __restrict__ out, int64_t stride) {
-  const int64_t w = int64_t(blockIdx.x) * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t t0 = w / tiles * kLookupRows;
+  const uint32_t w = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t0 = int64_t(w / uint32_t(tiles)) * kLookupRows;
   if (t0 >= n) return;
-  const int col = int(w % tiles) * 64 * E + int(threadIdx.x & 63) * E;
-  const int cnt = dim - col;
+  const Span s = span_of<E>(int(w % uint32_t(tiles)) * 64 + int(threadIdx.x & 63), dim);
+  int row[kLookupRows];
   Words<E, T> x[kLookupRows];
 #pragma unroll
-  for (int k = 0; k < kLookupRows; ++k) {
-    const int row = t0 + k < n ? uniform_row(tokens, wide, t0 + k, rows) : rows;
-    x[k] = load_row<E, false>(table + int64_t(row) * dim + col, row < rows ? cnt : 0);
-  }
+  for (int k = 0; k < kLookupRows; ++k) row[k] = t0 + k < n ? uniform_row(tokens, wide, t0 + k, rows) : rows;
+#pragma unroll
+  for (int k = 0; k < kLookupRows; ++k)
+    x[k] = load_row<E, false>(table + int64_t(row[k] < rows ? row[k] : 0) * dim, s, dim);
 #pragma unroll
   for (int k = 0; k < kLookupRows; ++k) {
     if (t0 + k >= n) break;
     float v[E];
     widen<E, T>(x[k], v);
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] *= scale;
-    store_row<E>(out + (t0 + k) * stride + col, cnt, narrow<E, O>(v));
+    for (int e = 0; e < E; ++e) v[e] = row[k] < rows ? v[e] * scale : 0.f;
+    store_row<E>(out + (t0 + k) * stride, s, narrow<E, O>(v));
   }
 }
 
 // --------------------------------------------------------------------- sort
 
 // Few tokens: a token's place is the number of tokens before it, those of lower
-// rows and those of its own row at lower positions. The 64 tokens of a block are
-// compared with all of them, its 16 waves taking a part each. The blocks after
-// those set the bits of the rows that have a token, 2^18 rows a block.
-constexpr int kRankThreads = 1024, kRankWaves = kRankThreads / 64;
-constexpr int kBitWords = 8192;
+// rows and those of its own row at lower positions: n^2 comparisons, two
+// instructions for each 64 of them. A block takes 32 tokens, each in both halves
+// of a wave, and its 32 half waves take a part of the tokens to compare with
+// each, from LDS.
+constexpr int kRankThreads = 1024, kRankParts = kRankThreads / 32;
 
 __global__ __launch_bounds__(kRankThreads) void order_rank_kernel(const void* __restrict__ tokens, int wide, int n,
-                                                                  int rows, int rank_blocks, int32_t* __restrict__ head,
-                                                                  int32_t* __restrict__ row, int32_t* __restrict__ pos,
-                                                                  uint32_t* __restrict__ bits) {
-  __shared__ int32_t key[zero::kRankTokens + 256];
-  __shared__ int32_t part[kRankWaves][64];
-  __shared__ uint32_t word[kBitWords];
+                                                                  int rows, int32_t* __restrict__ head,
+                                                                  int32_t* __restrict__ row, int32_t* __restrict__ pos) {
+  __shared__ alignas(16) int32_t key[zero::kRankTokens + 4 * kRankParts];
+  __shared__ int32_t part[kRankParts][32];
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  if (int(blockIdx.x) >= rank_blocks) {
-    const int w0 = (int(blockIdx.x) - rank_blocks) * kBitWords;
-    const int words = min(kBitWords, (rows + 31) / 32 - w0);
-    for (int k = t; k < words; k += kRankThreads) word[k] = 0;
-    __syncthreads();
-    for (int k = t; k < n; k += kRankThreads) {
-      const int r = table_row(tokens, wide, k, rows);
-      const int at = (r >> 5) - w0;
-      if (r < rows && at >= 0 && at < words) atomicOr(&word[at], 1u << (r & 31));
+  // a half wave's part: whole fours of tokens
+  const int each = ((n + kRankParts - 1) / kRankParts + 3) / 4 * 4;
+  for (int k = t; k < each * kRankParts; k += kRankThreads) key[k] = k < n ? table_row(tokens, wide, k, rows) : 0x7FFFFFFF;
+  __syncthreads();
+  const int i0 = int(blockIdx.x) * 32, i = i0 + (lane & 31), half = t >> 5;
+  const int mine = i < n ? key[i] : 0;
+  const int j0 = half * each, j1 = j0 + each;
+  // before the block's tokens an equal row counts, behind them it does not
+  const int before = min(max(i0, j0), j1), behind = max(min(i0 + 32, j1), before);
+  int place = 0;
+  const auto count = [&](int from, int to, int limit) {
+#pragma unroll 4
+    for (int j = from; j < to; j += 4) {
+      const int4 k = *reinterpret_cast<const int4*>(&key[j]);
+      place += (k.x < limit) + (k.y < limit) + (k.z < limit) + (k.w < limit);
     }
-    __syncthreads();
-    for (int k = t; k < words; k += kRankThreads) bits[w0 + k] = word[k];
-    return;
-  }
-  // a wave's part: whole fours of tokens
-  const int each = ((n + kRankWaves - 1) / kRankWaves + 3) / 4 * 4;
-  const int padded = each * kRankWaves;         // at most kRankTokens + 60
-  for (int k = t; k < padded; k += kRankThreads) key[k] = k < n ? table_row(tokens, wide, k, rows) : 0x7FFFFFFF;
+  };
+  count(j0, before, mine + 1);
+  for (int j = before; j < behind; ++j) place += (key[j] < mine || (key[j] == mine && j < i)) ? 1 : 0;
+  count(behind, j1, mine);
+  part[half][lane & 31] = place;
   __syncthreads();
-  const int i = int(blockIdx.x) * 64 + lane;
-  const int mine = i < n ? key[i] : 0x7FFFFFFF;
-  int before = 0;
-  for (int j = wave * each; j < (wave + 1) * each; j += 4) {
-    const int4 k4 = *reinterpret_cast<const int4*>(&key[j]);
-    const int k[4] = {k4.x, k4.y, k4.z, k4.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) before += (k[e] < mine || (k[e] == mine && j + e < i)) ? 1 : 0;
-  }
-  part[wave][lane] = before;
-  __syncthreads();
-  if (wave == 0 && i < n) {
+  if (t < 32 && i < n) {
     int at = 0;
 #pragma unroll
-    for (int k = 0; k < kRankWaves; ++k) at += part[k][lane];
+    for (int k = 0; k < kRankParts; ++k) at += part[k][t];
     row[at] = mine;
     pos[at] = i;
   }
   if (blockIdx.x == 0) {       // how many lie in the table
     int live = 0;
     for (int k = t; k < n; k += kRankThreads) live += key[k] < rows ? 1 : 0;
-    __syncthreads();
     for (int off = 32; off >= 1; off >>= 1) live += __shfl_xor(live, off, 64);
-    if (lane == 0) part[wave][0] = live;
+    __syncthreads();
+    if (lane == 0) part[0][wave] = live;
     __syncthreads();
     if (t == 0) {
       int sum = 0;
-      for (int k = 0; k < kRankWaves; ++k) sum += part[k][0];
+      for (int k = 0; k < kRankThreads / 64; ++k) sum += part[0][k];
       *head = sum;
     }
   }
@@ -236,7 +268,6 @@ struct SortArgs {
   const int32_t *row_in, *pos_in;
   int32_t *row_out, *pos_out;
   int32_t *digits, *live, *head;
-  uint32_t* present;
 };
 
 template <bool FIRST>
@@ -254,8 +285,6 @@ __global__ __launch_bounds__(kSortThreads) void order_count_kernel(SortArgs a) {
     atomicAdd(&count[(r >> a.shift) & ((1 << a.bits) - 1)], 1);
     live += r < a.rows ? 1 : 0;
   }
-  if (FIRST)        // the bits, cleared for the scatter that follows
-    for (int k = int(blockIdx.x) * kSortThreads + t; k < (a.rows + 31) / 32; k += a.blocks * kSortThreads) a.present[k] = 0;
   __syncthreads();
   for (int k = t; k < (1 << a.bits); k += kSortThreads) a.digits[int64_t(blockIdx.x) * kSortDigits + k] = count[k];
   if (FIRST) {
@@ -275,9 +304,19 @@ __global__ __launch_bounds__(kSortThreads) void order_scatter_kernel(SortArgs a)
   __shared__ int32_t wave_sum[kWaves];
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
   const int n_digits = 1 << a.bits;
+  // a wave's tokens are consecutive: 64 at a time, each one's rank among those of its digit
+  const int first = int(blockIdx.x) * kSortBlock + wave * 64 * kSortItems;
+  int row[kSortItems], pos[kSortItems], rank[kSortItems];
+#pragma unroll
+  for (int k = 0; k < kSortItems; ++k) {
+    const int i = first + k * 64 + lane;
+    row[k] = i >= a.n ? -1 : FIRST ? table_row(a.tokens, a.wide, i, a.rows) : a.row_in[i];
+    pos[k] = i >= a.n ? 0 : FIRST ? i : a.pos_in[i];
+  }
   for (int k = t; k < kWaves * kSortDigits; k += kSortThreads) (&seen[0][0])[k] = 0;
   // two digits a thread: all blocks' tokens of lower digits, and the earlier blocks' of its own
   int total[2] = {0, 0}, before[2] = {0, 0};
+#pragma unroll 8
   for (int b = 0; b < a.blocks; ++b) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -299,15 +338,6 @@ __global__ __launch_bounds__(kSortThreads) void order_scatter_kernel(SortArgs a)
   for (int w = 0; w < wave; ++w) lower += wave_sum[w];
   base[2 * t] = lower + before[0];
   base[2 * t + 1] = lower + total[0] + before[1];
-  // a wave's tokens are consecutive: 64 at a time, each one's rank among those of its digit
-  const int first = int(blockIdx.x) * kSortBlock + wave * 64 * kSortItems;
-  int row[kSortItems], pos[kSortItems], rank[kSortItems];
-#pragma unroll
-  for (int k = 0; k < kSortItems; ++k) {
-    const int i = first + k * 64 + lane;
-    row[k] = i >= a.n ? -1 : FIRST ? table_row(a.tokens, a.wide, i, a.rows) : a.row_in[i];
-    pos[k] = i >= a.n ? 0 : FIRST ? i : a.pos_in[i];
-  }
 #pragma unroll
   for (int k = 0; k < kSortItems; ++k) {
     const bool there = row[k] >= 0;
@@ -343,7 +373,6 @@ __global__ __launch_bounds__(kSortThreads) void order_scatter_kernel(SortArgs a)
     const int at = seen[wave][d] + rank[k];
     a.row_out[at] = row[k];
     a.pos_out[at] = pos[k];
-    if (FIRST && row[k] < a.rows) atomicOr(&a.present[row[k] >> 5], 1u << (row[k] & 31));
   }
   if (LAST && blockIdx.x == 0 && wave == 0) {
     int live = 0;
@@ -357,35 +386,45 @@ __global__ __launch_bounds__(kSortThreads) void order_scatter_kernel(SortArgs a)
 
 struct EmbeddingGradArgs {
   const int32_t *head, *row, *pos;
-  const uint32_t* present;
   const void* d_out;
   void* grad;
   float* ws;                 // [pieces][2][dim4]: sums of a run's middle or end, and of its beginning
   int64_t stride, first, count;
   float scale;
-  int32_t dim, dim4, tiles, pieces;
+  int32_t dim, dim4, tiles, pieces, piece;
   int32_t row_lo, row_hi;    // rows that the part touches
-  int32_t sum_blocks, accumulate;
+  int32_t sum_blocks, fill_rows, accumulate;
 };
 
-// The part's elements of row r at column col, E of them from there: grad's
-// element index, and which of the E lie in the part.
-struct Place {
-  int64_t at;
-  int lo, hi;
-};
-template <int E>
-__device__ __forceinline__ Place place_of(const EmbeddingGradArgs& a, int r, int col) {
-  Place p;
-  p.at = int64_t(r) * a.dim + col - a.first;
-  const int64_t end = a.count - p.at;
-  p.lo = p.at >= 0 ? 0 : p.at <= -E ? E : int(-p.at);
-  p.hi = min(end >= E ? E : end <= 0 ? 0 : int(end), a.dim - col);
-  return p;
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef i32x8 i32x8_any __attribute__((aligned(4)));
+
+// The elements of row r that are the lane's and in the part: those of `s`, cut
+// where the part begins or ends inside the row.
+__device__ __forceinline__ Span in_part(const EmbeddingGradArgs& a, int64_t base, Span s) {
+  if (base < 0) s.lo = max(s.lo, int(min(-base - s.col, int64_t(64))));
+  if (base + a.dim > a.count) s.hi = min(s.hi, int(max(a.count - base - s.col, int64_t(0))));
+  return s;
+}
+
+// grad's elements of row r at the lane's span, before the sum is added.
+template <int E, typename G>
+__device__ __forceinline__ Words<E, G> read_grad(const EmbeddingGradArgs& a, int r, const Span& s) {
+  const int64_t base = int64_t(r) * a.dim - a.first;      // grad's index of the row's first element
+  const G* g = static_cast<const G*>(a.grad) + base;
+  if (base >= 0 && base + a.dim <= a.count) return load_row<E>(g, s, a.dim);
+  const Span p = in_part(a, base, s);
+  return load_some<E, G>(g + p.col, p.lo, p.hi);
 }
 
 template <int E, typename G>
-__device__ __forceinline__ void write_row(const EmbeddingGradArgs& a, const Place& p, const Words<E, G>& old,
+__device__ __forceinline__ void write_grad(const EmbeddingGradArgs& a, int r, const Span& s, const Words<E, G>& w) {
+  const int64_t base = int64_t(r) * a.dim - a.first;
+  store_row<E>(static_cast<G*>(a.grad) + base, in_part(a, base, s), w);
+}
+
+template <int E, typename G>
+__device__ __forceinline__ void write_sum(const EmbeddingGradArgs& a, int r, const Span& s, const Words<E, G>& old,
                                           const float (&sum)[E]) {
   float v[E];
   if (a.accumulate) {
@@ -396,24 +435,23 @@ __device__ __forceinline__ void write_row(const EmbeddingGradArgs& a, const Plac
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] = sum[e] * a.scale;
   }
-  G* g = static_cast<G*>(a.grad) + p.at;
-  const Words<E, G> w = narrow<E, G>(v);
-  if (p.lo == 0 && p.hi >= E) store_row<E>(g, E, w);
-  else store_some<E, G>(g, p.lo, p.hi, w);
+  write_grad<E, G>(a, r, s, narrow<E, G>(v));
 }
 
-template <int E, typename G>
-__device__ __forceinline__ Words<E, G> read_row(const EmbeddingGradArgs& a, const Place& p) {
-  const G* g = static_cast<const G*>(a.grad) + p.at;
-  if (p.lo == 0 && p.hi >= E) return load_row<E>(g, E);
-  Words<E, G> r{};
-#pragma unroll
-  for (int k = 0; k < E; ++k) {
-    if (k < p.lo || k >= p.hi) continue;
-    if constexpr (sizeof(G) == 2) r.w[k >> 1] |= uint32_t(g[k]) << (16 * (k & 1));
-    else r.w[k] = g[k];
+// The first of the sorted rows [from, live) that is at or above r, 64 compared at
+// a time: their spacing goes down by 64 each round.
+__device__ __forceinline__ int first_at(const int32_t* row, int from, int live, int r) {
+  const int lane = threadIdx.x & 63;
+  int lo = from, n = live - from;      // the answer is in [lo, lo + n]
+  while (n > 0) {
+    const int step = (n + 63) >> 6, i = lo + min((lane + 1) * step, n) - 1;
+    const int below = __popcll(__ballot(row[i] < r));       // of the lanes' last rows: so many steps lie below
+    if (below == 64) return lo + n;
+    lo = __builtin_amdgcn_readfirstlane(lo + below * step);
+    if (step == 1) return lo;
+    n = __builtin_amdgcn_readfirstlane(min(step, live - lo));
   }
-  return r;
+  return lo;
 }
 
 constexpr int kBatch = 8;      // rows that a wave loads before it adds them
@@ -421,46 +459,58 @@ constexpr int kBatch = 8;      // rows that a wave loads before it adds them
 template <typename T, typename G, int E>
 __global__ __launch_bounds__(256) void embedding_grad_kernel(const EmbeddingGradArgs a) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (int(blockIdx.x) >= a.sum_blocks) {      // zeros, a wave a row
-    const int r = a.row_lo + (int(blockIdx.x) - a.sum_blocks) * 4 + wave;
-    if (r >= a.row_hi || (uniform_load(a.present + (r >> 5)) >> (r & 31) & 1)) return;
-    const Words<E, G> zero{};
-    for (int col = lane * E; col < a.dim; col += 64 * E) {
-      const Place p = place_of<E>(a, r, col);
-      G* g = static_cast<G*>(a.grad) + p.at;
-      if (p.lo == 0 && p.hi >= E) store_row<E>(g, E, zero);
-      else store_some<E, G>(g, p.lo, p.hi, zero);
+  const int live = uniform_load(a.head);
+  if (int(blockIdx.x) >= a.sum_blocks) {      // zeros, for the rows without a token
+    const int r0 = a.row_lo + ((int(blockIdx.x) - a.sum_blocks) * 4 + wave) * a.fill_rows;
+    const int r1 = min(r0 + a.fill_rows, a.row_hi);
+    if (r0 >= r1) return;
+    const int from = first_at(a.row, 0, live, r0), to = first_at(a.row, from, live, r1);
+    // a lane a row: is it among the sorted ones between
+    int lo = from, hi = to;
+    const int mine = r0 + lane;
+    while (__ballot(lo < hi)) {
+      const int mid = (lo + hi) >> 1;
+      if (lo < hi) {
+        if (a.row[mid] < mine) lo = mid + 1;
+        else hi = mid;
+      }
     }
+    const bool absent = lo >= to || a.row[lo < to ? lo : 0] != mine;
+    const uint64_t rows = __ballot(absent && mine < r1);
+    for (int k = 0; k < r1 - r0; ++k)
+      if (rows >> k & 1)
+        for (int c = 0; c < a.tiles; ++c) write_grad<E, G>(a, r0 + k, span_of<E>(c * 64 + lane, a.dim), Words<E, G>{});
     return;
   }
-  const int64_t w = int64_t(blockIdx.x) * 4 + wave;
-  const int piece = int(w / a.tiles);
+  const uint32_t w = blockIdx.x * 4 + wave;
+  const int piece = int(w / uint32_t(a.tiles));
   if (piece >= a.pieces) return;
-  const int col = int(w % a.tiles) * 64 * E + lane * E;
-  const int cnt = a.dim - col;
-  const int live = uniform_load(a.head);
-  const int i0 = piece * kPiece, i1 = min(i0 + kPiece, live);
+  const Span s = span_of<E>(int(w % uint32_t(a.tiles)) * 64 + lane, a.dim);
+  const int i0 = piece * a.piece, i1 = min(i0 + a.piece, live);
   if (i0 >= i1) return;
   const int r_first = uniform_load(a.row + i0), r_last = uniform_load(a.row + i1 - 1);
   if (r_last < a.row_lo || r_first >= a.row_hi) return;
-  bool head = i0 > 0 && uniform_load(a.row + i0 - 1) == r_first;     // the run at hand began in an earlier piece
-  const int next = i1 < live ? uniform_load(a.row + i1) : -1;
+  bool head = i0 > 0 && uniform_load(a.row + max(i0 - 1, 0)) == r_first;     // the run at hand began in an earlier piece
   float sum[E] = {};
   for (int i = i0; i < i1; i += kBatch) {
+    // rows and positions by eights: the arrays go on that far behind their last entry
+    const i32x8 r8 = *(const __attribute__((address_space(4))) i32x8_any*)(a.row + i);
+    const i32x8 p8 = *(const __attribute__((address_space(4))) i32x8_any*)(a.pos + i);
+    const int r9 = uniform_load(a.row + i + kBatch);
     int r[kBatch + 1];
     Words<E, T> x[kBatch];
     Words<E, G> old[kBatch];
-    Place p[kBatch];
 #pragma unroll
-    for (int k = 0; k <= kBatch; ++k) r[k] = i + k < i1 ? uniform_load(a.row + i + k) : i + k == i1 ? next : -1;
+    for (int k = 0; k <= kBatch; ++k) r[k] = i + k >= live ? -1 : k < kBatch ? r8[k % kBatch] : r9;
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const bool mine = i + k < i1 && r[k] >= a.row_lo && r[k] < a.row_hi;
-      const int64_t at = mine ? int64_t(uniform_load(a.pos + i + k)) * a.stride + col : 0;
-      x[k] = load_row<E>(static_cast<const T*>(a.d_out) + at, mine ? cnt : 0);
-      p[k] = place_of<E>(a, r[k], col);
-      old[k] = Words<E, G>{};
-      if (a.accumulate && mine && r[k] != r[k + 1]) old[k] = read_row<E, G>(a, p[k]);
+      x[k] = load_row<E>(static_cast<const T*>(a.d_out) + (mine ? int64_t(p8[k]) * a.stride : 0), s, a.dim);
+    }
+    if (a.accumulate) {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (i + k < i1 && r[k] != r[k + 1] && r[k] >= a.row_lo && r[k] < a.row_hi) old[k] = read_grad<E, G>(a, r[k], s);
     }
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
@@ -472,14 +522,10 @@ __global__ __launch_bounds__(256) void embedding_grad_kernel(const EmbeddingGrad
       const bool end = r[k] != r[k + 1];
       if (!end && i + k + 1 < i1) continue;
       if (r[k] >= a.row_lo && r[k] < a.row_hi) {
-        if (head || !end) {
-          if (cnt > 0) {
-            float* s = a.ws + (int64_t(piece) * 2 + (head ? 0 : 1)) * a.dim4 + col;
-            store_row<E, false>(s, cnt, narrow<E, float>(sum));
-          }
-        } else {
-          write_row<E, G>(a, p[k], old[k], sum);
-        }
+        if (head || !end)
+          store_row<E, false>(a.ws + (int64_t(piece) * 2 + (head ? 0 : 1)) * a.dim4, s, narrow<E, float>(sum));
+        else
+          write_sum<E, G>(a, r[k], s, old[k], sum);
       }
       head = false;
 #pragma unroll
@@ -491,88 +537,118 @@ __global__ __launch_bounds__(256) void embedding_grad_kernel(const EmbeddingGrad
 template <typename G, int E>
 __global__ __launch_bounds__(256) void embedding_join_kernel(const EmbeddingGradArgs a) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t w = int64_t(blockIdx.x) * 4 + wave;
-  const int piece = int(w / a.tiles);
+  const uint32_t w = blockIdx.x * 4 + wave;
+  const int piece = int(w / uint32_t(a.tiles));
   if (piece >= a.pieces) return;
-  const int col = int(w % a.tiles) * 64 * E + lane * E;
-  const int cnt = a.dim - col;
+  const Span s = span_of<E>(int(w % uint32_t(a.tiles)) * 64 + lane, a.dim);
   const int live = uniform_load(a.head);
-  const int i0 = piece * kPiece, i1 = i0 + kPiece;
+  const int i0 = piece * a.piece, i1 = i0 + a.piece;
   if (i1 >= live) return;
   const int r = uniform_load(a.row + i1);
   if (uniform_load(a.row + i1 - 1) != r || r < a.row_lo || r >= a.row_hi) return;
-  if (i0 > 0 && uniform_load(a.row + i0) == r && uniform_load(a.row + i0 - 1) == r) return;    // began earlier
-  const float* s = a.ws + int64_t(piece) * 2 * a.dim4 + col;
+  if (i0 > 0 && uniform_load(a.row + i0) == r && uniform_load(a.row + max(i0 - 1, 0)) == r) return;    // began earlier
+  // the pieces whose first token goes on with the run: 64 compared at a time
+  int last = piece;
+  for (;;) {
+    const int64_t i = int64_t(last + 1 + lane) * a.piece;
+    const uint64_t on = __ballot(i < live && a.row[i < live ? i : 0] == r);
+    const int more = on == ~uint64_t(0) ? 64 : __builtin_ctzll(~on);
+    last += more;
+    if (more < 64) break;
+  }
+  const float* p = a.ws + int64_t(piece) * 2 * a.dim4;
   float sum[E];
-  widen<E, float>(load_row<E, false>(s + a.dim4, cnt), sum);
-  for (int j = piece + 1; j * kPiece < live && uniform_load(a.row + j * kPiece) == r; ++j) {
-    s += 2 * a.dim4;
+  widen<E, float>(load_row<E, false>(p + a.dim4, s, a.dim), sum);
+#pragma unroll 8
+  for (int j = piece + 1; j <= last; ++j) {
     float v[E];
-    widen<E, float>(load_row<E, false>(s, cnt), v);
+    widen<E, float>(load_row<E, false>(p + int64_t(j - piece) * 2 * a.dim4, s, a.dim), v);
 #pragma unroll
     for (int e = 0; e < E; ++e) sum[e] += v[e];
   }
-  const Place p = place_of<E>(a, r, col);
   Words<E, G> old{};
-  if (a.accumulate) old = read_row<E, G>(a, p);
-  write_row<E, G>(a, p, old, sum);
+  if (a.accumulate) old = read_grad<E, G>(a, r, s);
+  write_sum<E, G>(a, r, s, old, sum);
 }
 
 // --------------------------------------------------------------------- norm
 
-// E elements of a vector of either type, as fp32; ones or zeros where there is none.
-template <int E>
-__device__ __forceinline__ void load_weight(const void* w, bool bf16, int col, int cnt, float none, float (&x)[E]) {
-  if (w == nullptr) {
+// E elements of a vector; ones or zeros where there is none.
+template <int E, typename W>
+__device__ __forceinline__ Words<E, W> load_weight(const void* w, const Span& s, int dim, float none) {
+  if (w != nullptr) return load_row<E, false>(static_cast<const W*>(w), s, dim);
+  float x[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = none;
-  } else if (bf16) {
-    widen<E, uint16_t>(load_row<E, false>(static_cast<const uint16_t*>(w) + col, cnt), x);
-  } else {
-    widen<E, float>(load_row<E, false>(static_cast<const float*>(w) + col, cnt), x);
-  }
+  for (int e = 0; e < E; ++e) x[e] = none;
+  return narrow<E, W>(x);
 }
 
-// The sum of K values over the TPR threads that share a row, in every one of
-// them. lds: of a block's waves, for TPR above 64; a block that calls it again
-// takes the other half (`turn`), so one barrier a call suffices.
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float x) {
+  return x + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xF, 0xF, true));
+}
+
+// The sum over aligned groups of LANES lanes, in every lane and in the same
+// order for all: pairs, fours, eights, sixteens by moves within a row of 16
+// lanes, then the rows and the halves of the wave by swaps.
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float x) {
+  static_assert(LANES == 16 || LANES == 64, "a row of lanes or the wave");
+  x = dpp_add<0xB1>(x);       // quad_perm [1, 0, 3, 2]
+  x = dpp_add<0x4E>(x);       // quad_perm [2, 3, 0, 1]
+  x = dpp_add<0x141>(x);      // row_half_mirror
+  x = dpp_add<0x140>(x);      // row_mirror
+  if constexpr (LANES == 64) {
+    auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+    p = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  }
+  return x;
+}
+
+// The sums of K values over the TPR threads that share a row, in every one of
+// them. With TPR above 64 every thread of the block has to call it, and lds holds
+// 2 * K * (waves of the block) values, half of which a call takes (`turn`, 0 and 1
+// in turn), so one barrier a call suffices.
 template <int TPR, int K>
 __device__ __forceinline__ void row_sum(float (&x)[K], float* lds, int turn) {
 #pragma unroll
-  for (int off = (TPR < 64 ? TPR : 64) / 2; off >= 1; off >>= 1)
-#pragma unroll
-    for (int k = 0; k < K; ++k) x[k] += __shfl_xor(x[k], off, 64);
+  for (int k = 0; k < K; ++k) x[k] = lanes_sum<(TPR < 64 ? TPR : 64)>(x[k]);
   if constexpr (TPR > 64) {
     constexpr int kWaves = TPR / 64;
-    float* s = lds + turn * K * kWaves;
+    float* s = lds + turn * K * int(blockDim.x / 64);
+    const int wave = threadIdx.x / 64, first = wave / kWaves * kWaves;
     if ((threadIdx.x & 63) == 0)
 #pragma unroll
-      for (int k = 0; k < K; ++k) s[k * kWaves + (threadIdx.x >> 6)] = x[k];
+      for (int k = 0; k < K; ++k) s[wave * K + k] = x[k];
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       x[k] = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) x[k] += s[k * kWaves + w];
+      for (int w = 0; w < kWaves; ++w) x[k] += s[(first + w) * K + k];
     }
   }
 }
 
-template <typename T, int TPR, int V>
+template <typename T, typename W, int TPR, int V>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(const zero_norm_args a) {
   constexpr int E = 16 / int(sizeof(T));
   constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
-  __shared__ float lds[2 * (TPR / 64 + 1)];
+  __shared__ float lds[2 * (TPR < 256 ? 4 : TPR / 64)];
   const int64_t row = int64_t(blockIdx.x) * kRows + threadIdx.x / TPR;
   const int t = threadIdx.x % TPR;
   if (row >= a.n) return;          // whole rows: with TPR above 64 a block has one
   const int dim = int(a.dim);
   const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+  Span s[V];
   Words<E, T> raw[V];
+  Words<E, W> w[V], b[V];
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    const int col = (t + k * TPR) * E;
-    raw[k] = load_row<E>(x + col, dim - col);
+    s[k] = span_of<E>(t + k * TPR, dim);
+    raw[k] = load_row<E>(x, s[k], dim);
   }
   float v[V][E];
   if (a.residual != nullptr) {
@@ -580,61 +656,70 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(const zero_
     T* total = static_cast<T*>(a.total) + row * a.total_stride;
     Words<E, T> more[V];
 #pragma unroll
+    for (int k = 0; k < V; ++k) more[k] = load_row<E>(res, s[k], dim);
+#pragma unroll
     for (int k = 0; k < V; ++k) {
-      const int col = (t + k * TPR) * E;
-      more[k] = load_row<E>(res + col, dim - col);
+      w[k] = load_weight<E, W>(a.weight, s[k], dim, 1.f);
+      b[k] = load_weight<E, W>(a.bias, s[k], dim, 0.f);
     }
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      const int col = (t + k * TPR) * E;
       float r[E];
       widen<E, T>(raw[k], v[k]);
       widen<E, T>(more[k], r);
 #pragma unroll
       for (int e = 0; e < E; ++e) v[k][e] += r[e];
       raw[k] = narrow<E, T>(v[k]);
-      store_row<E>(total + col, dim - col, raw[k]);
+      store_row<E>(total, s[k], raw[k]);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      w[k] = load_weight<E, W>(a.weight, s[k], dim, 1.f);
+      b[k] = load_weight<E, W>(a.bias, s[k], dim, 0.f);
     }
   }
-  float s[1] = {0.f};
+  float sum[1] = {0.f};
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     widen<E, T>(raw[k], v[k]);
+    only_own<E>(s[k], v[k]);
 #pragma unroll
-    for (int e = 0; e < E; ++e) s[0] += v[k][e];
+    for (int e = 0; e < E; ++e) sum[0] += v[k][e];
   }
   float mean = 0.f;
   if (!a.rms) {
-    row_sum<TPR, 1>(s, lds, 0);
-    mean = s[0] / float(dim);
+    row_sum<TPR, 1>(sum, lds, 0);
+    mean = sum[0] / float(dim);
   }
-  s[0] = 0.f;
+  sum[0] = 0.f;
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    const int rest = dim - (t + k * TPR) * E;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float d = e < rest ? v[k][e] - mean : 0.f;
-      s[0] = fmaf(d, d, s[0]);
+    for (int e = 0; e < E; ++e) v[k][e] -= mean;
+    only_own<E>(s[k], v[k]);
+    if (dim < E) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[k][e] = e < s[k].hi ? v[k][e] : 0.f;
     }
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum[0] = fmaf(v[k][e], v[k][e], sum[0]);
   }
-  row_sum<TPR, 1>(s, lds, 1);
-  const float rstd = 1.f / sqrtf(s[0] / float(dim) + float(a.eps));
+  row_sum<TPR, 1>(sum, lds, 1);
+  const float rstd = 1.f / sqrtf(sum[0] / float(dim) + float(a.eps));
   if (t == 0) {
     if (a.mean != nullptr) a.mean[row] = mean;
     if (a.rstd != nullptr) a.rstd[row] = rstd;
   }
   T* y = static_cast<T*>(a.y) + row * a.y_stride;
-  const bool bf16 = a.weight_type == ZERO_BF16;
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    const int col = (t + k * TPR) * E;
-    float w[E], b[E];
-    load_weight<E>(a.weight, bf16, col, dim - col, 1.f, w);
-    load_weight<E>(a.bias, bf16, col, dim - col, 0.f, b);
+    float wf[E], bf[E];
+    widen<E, W>(w[k], wf);
+    widen<E, W>(b[k], bf);
 #pragma unroll
-    for (int e = 0; e < E; ++e) w[e] = fmaf((v[k][e] - mean) * rstd, w[e], b[e]);
-    store_row<E>(y + col, dim - col, narrow<E, T>(w));
+    for (int e = 0; e < E; ++e) v[k][e] = fmaf(v[k][e] * rstd, wf[e], bf[e]);
+    store_row<E>(y, s[k], narrow<E, T>(v[k]));
   }
 }
 
@@ -642,145 +727,181 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(const zero_
 // ones from the caches. Element by element, so that y and total may be x.
 constexpr int kLongThreads = 1024;
 
-template <typename T>
+template <typename T, typename W>
 __global__ __launch_bounds__(kLongThreads) void norm_long_kernel(const zero_norm_args a) {
   constexpr int E = 16 / int(sizeof(T));
   __shared__ float lds[2 * (kLongThreads / 64)];
   const int64_t row = blockIdx.x;
-  const int dim = int(a.dim);
+  const int dim = int(a.dim), vectors = (dim + E - 1) / E;
   const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
   const T* res = a.residual != nullptr ? static_cast<const T*>(a.residual) + row * a.residual_stride : nullptr;
   T* total = res != nullptr ? static_cast<T*>(a.total) + row * a.total_stride : nullptr;
-  float s[1] = {0.f};
-  for (int col = threadIdx.x * E; col < dim; col += kLongThreads * E) {
+  float sum[1] = {0.f};
+  for (int k = threadIdx.x; k < vectors; k += kLongThreads) {
+    const Span s = span_of<E>(k, dim);
     float v[E];
-    Words<E, T> raw = load_row<E, false>(x + col, dim - col);
+    Words<E, T> raw = load_row<E, false>(x, s, dim);
     widen<E, T>(raw, v);
     if (res != nullptr) {
       float r[E];
-      widen<E, T>(load_row<E, false>(res + col, dim - col), r);
+      widen<E, T>(load_row<E, false>(res, s, dim), r);
 #pragma unroll
       for (int e = 0; e < E; ++e) v[e] += r[e];
       raw = narrow<E, T>(v);
-      store_row<E, false>(total + col, dim - col, raw);
+      store_row<E, false>(total, s, raw);
       widen<E, T>(raw, v);
     }
+    only_own<E>(s, v);
 #pragma unroll
-    for (int e = 0; e < E; ++e) s[0] += v[e];
+    for (int e = 0; e < E; ++e) sum[0] += v[e];
   }
   if (res != nullptr) x = total;       // every thread reads back what it wrote
   float mean = 0.f;
   if (!a.rms) {
-    row_sum<kLongThreads, 1>(s, lds, 0);
-    mean = s[0] / float(dim);
+    row_sum<kLongThreads, 1>(sum, lds, 0);
+    mean = sum[0] / float(dim);
   }
-  s[0] = 0.f;
-  for (int col = threadIdx.x * E; col < dim; col += kLongThreads * E) {
+  sum[0] = 0.f;
+  for (int k = threadIdx.x; k < vectors; k += kLongThreads) {
+    const Span s = span_of<E>(k, dim);
     float v[E];
-    widen<E, T>(load_row<E, false>(x + col, dim - col), v);
+    widen<E, T>(load_row<E, false>(x, s, dim), v);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float d = col + e < dim ? v[e] - mean : 0.f;
-      s[0] = fmaf(d, d, s[0]);
-    }
+    for (int e = 0; e < E; ++e) v[e] -= mean;
+    only_own<E>(s, v);
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum[0] = fmaf(v[e], v[e], sum[0]);
   }
-  row_sum<kLongThreads, 1>(s, lds, 1);
-  const float rstd = 1.f / sqrtf(s[0] / float(dim) + float(a.eps));
+  row_sum<kLongThreads, 1>(sum, lds, 1);
+  const float rstd = 1.f / sqrtf(sum[0] / float(dim) + float(a.eps));
   if (threadIdx.x == 0) {
     if (a.mean != nullptr) a.mean[row] = mean;
     if (a.rstd != nullptr) a.rstd[row] = rstd;
   }
   T* y = static_cast<T*>(a.y) + row * a.y_stride;
-  const bool bf16 = a.weight_type == ZERO_BF16;
-  for (int col = threadIdx.x * E; col < dim; col += kLongThreads * E) {
+  for (int k = threadIdx.x; k < vectors; k += kLongThreads) {
+    const Span s = span_of<E>(k, dim);
     float v[E], w[E], b[E];
-    widen<E, T>(load_row<E, false>(x + col, dim - col), v);
-    load_weight<E>(a.weight, bf16, col, dim - col, 1.f, w);
-    load_weight<E>(a.bias, bf16, col, dim - col, 0.f, b);
+    widen<E, T>(load_row<E, false>(x, s, dim), v);
+    widen<E, W>(load_weight<E, W>(a.weight, s, dim, 1.f), w);
+    widen<E, W>(load_weight<E, W>(a.bias, s, dim, 0.f), b);
 #pragma unroll
-    for (int e = 0; e < E; ++e) w[e] = fmaf((v[e] - mean) * rstd, w[e], b[e]);
-    store_row<E, false>(y + col, dim - col, narrow<E, T>(w));
+    for (int e = 0; e < E; ++e) v[e] = fmaf((v[e] - mean) * rstd, w[e], b[e]);
+    store_row<E, false>(y, s, narrow<E, T>(v));
   }
 }
 
 // ---------------------------------------------------------- norm's gradient
 
-// A block takes every gridDim.x-th row (or group of rows) and keeps the sums of
-// d_weight and d_bias over them in registers; its waves' sums meet in LDS and go
-// to the workspace, which norm_grad_join_kernel adds up.
-template <typename T, int TPR, int V>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_grad_kernel(const zero_norm_grad_args a, float* ws, int dim4) {
+// A block takes every gridDim.x-th group of rows, TPR threads a row, and keeps the
+// sums of d_weight and d_bias over its rows in registers; the groups' sums meet in
+// LDS and go to the workspace, which norm_grad_join_kernel adds up.
+constexpr int kGradThreads = 1024;
+
+template <typename T, typename W, int TPR, int V>
+__global__ __launch_bounds__(kGradThreads) void norm_grad_kernel(const zero_norm_grad_args a, float* ws, int dim4) {
   constexpr int E = 16 / int(sizeof(T));
-  constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
-  __shared__ float lds[4 * (TPR / 64 + 1)];
+  constexpr int kRows = kGradThreads / TPR;
+  __shared__ float lds[kGradThreads * V * E];      // row sums, then the groups' column sums
   const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
   const int dim = int(a.dim);
-  float w[V][E], sum_w[V][E], sum_b[V][E];
+  const bool skip = a.d_total != nullptr;
+  Span s[V];
+  Words<E, W> w_raw[V];
+  float sum_w[V][E], sum_b[V][E];
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    const int col = (t + k * TPR) * E;
-    load_weight<E>(a.weight, a.weight_type == ZERO_BF16, col, dim - col, 1.f, w[k]);
+    s[k] = span_of<E>(t + k * TPR, dim);
+    w_raw[k] = load_weight<E, W>(a.weight, s[k], dim, 1.f);
 #pragma unroll
     for (int e = 0; e < E; ++e) sum_w[k][e] = sum_b[k][e] = 0.f;
   }
-  int turn = 0;
-  for (int64_t row = int64_t(blockIdx.x) * kRows + group; row < a.n; row += int64_t(gridDim.x) * kRows) {
+  // the next rows are read before this one's sums
+  struct Row {
+    Words<E, T> dy[V], x[V], total[V];
+    float mean, rstd;
+  };
+  const auto read = [&](int64_t row0) {
+    const int64_t row = row0 + group < a.n ? row0 + group : row0;
     const T* dy = static_cast<const T*>(a.d_y) + row * a.d_y_stride;
     const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
-    Words<E, T> dy_raw[V], x_raw[V], more[V];
+    Row r;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      const int col = (t + k * TPR) * E;
-      dy_raw[k] = load_row<E>(dy + col, dim - col);
-      x_raw[k] = load_row<E>(x + col, dim - col);
+      r.dy[k] = load_row<E>(dy, s[k], dim);
+      r.x[k] = load_row<E>(x, s[k], dim);
     }
-    const bool with_total = a.d_total != nullptr;
-    if (with_total) {
-      const T* d_total = static_cast<const T*>(a.d_total) + row * a.d_total_stride;
+    if (skip) {
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        r.total[k] = load_row<E>(static_cast<const T*>(a.d_total) + row * a.d_total_stride, s[k], dim);
+    }
+    r.mean = a.rms ? 0.f : a.mean[row];
+    r.rstd = a.rstd[row];
+    return r;
+  };
+  int turn = 0;
+  const int64_t step = int64_t(gridDim.x) * kRows;
+  Row now, next;
+  if (int64_t(blockIdx.x) * kRows < a.n) next = read(int64_t(blockIdx.x) * kRows);
+  for (int64_t row0 = int64_t(blockIdx.x) * kRows; row0 < a.n; row0 += step) {
+    const bool there = row0 + group < a.n;
+    const int64_t row = row0 + group;
+    now = next;
+    if (row0 + step < a.n) next = read(row0 + step);
+    const float mean = now.mean, rstd = now.rstd;
+    float c[2] = {0.f, 0.f};
+    if (there) {
 #pragma unroll
       for (int k = 0; k < V; ++k) {
-        const int col = (t + k * TPR) * E;
-        more[k] = load_row<E>(d_total + col, dim - col);
-      }
-    }
-    const float mean = a.rms ? 0.f : a.mean[row], rstd = a.rstd[row];
-    float s[2] = {0.f, 0.f};
+        float g[E], xh[E], w[E];
+        widen<E, T>(now.dy[k], g);
+        widen<E, T>(now.x[k], xh);
+        widen<E, W>(w_raw[k], w);
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const int rest = dim - (t + k * TPR) * E;
-      float g[E], xh[E];
-      widen<E, T>(dy_raw[k], g);
-      widen<E, T>(x_raw[k], xh);
+        for (int e = 0; e < E; ++e) {
+          xh[e] = (xh[e] - mean) * rstd;
+          sum_w[k][e] = fmaf(g[e], xh[e], sum_w[k][e]);
+          sum_b[k][e] += g[e];
+          g[e] *= w[e];
+        }
+        only_own<E>(s[k], g);
+        only_own<E>(s[k], xh);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        xh[e] = e < rest ? (xh[e] - mean) * rstd : 0.f;
-        sum_w[k][e] = fmaf(g[e], xh[e], sum_w[k][e]);
-        sum_b[k][e] += g[e];
-        const float gw = g[e] * w[k][e];
-        s[0] += gw;
-        s[1] = fmaf(gw, xh[e], s[1]);
+        for (int e = 0; e < E; ++e) {
+          c[0] += g[e];
+          c[1] = fmaf(g[e], xh[e], c[1]);
+        }
       }
     }
     if (a.d_x == nullptr) continue;
-    row_sum<TPR, 2>(s, lds, turn);
+    row_sum<TPR, 2>(c, lds, turn);
     turn ^= 1;
-    const float c0 = a.rms ? 0.f : s[0] / float(dim), c1 = s[1] / float(dim);
+    if (!there) continue;
+    // widened again: kept over the sum as fp32, the three rows do not fit the registers
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      opaque(now.dy[k]);
+      opaque(now.x[k]);
+      opaque(w_raw[k]);
+    }
+    const float c0 = a.rms ? 0.f : c[0] / float(dim), c1 = c[1] / float(dim);
     T* dx = static_cast<T*>(a.d_x) + row * a.d_x_stride;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      const int col = (t + k * TPR) * E;
-      float g[E], xh[E], m[E];
-      widen<E, T>(dy_raw[k], g);
-      widen<E, T>(x_raw[k], xh);
+      float g[E], xh[E], w[E], m[E];
+      widen<E, T>(now.dy[k], g);
+      widen<E, T>(now.x[k], xh);
+      widen<E, W>(w_raw[k], w);
 #pragma unroll
       for (int e = 0; e < E; ++e) m[e] = 0.f;
-      if (with_total) widen<E, T>(more[k], m);
+      if (skip) widen<E, T>(now.total[k], m);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         xh[e] = (xh[e] - mean) * rstd;
-        g[e] = fmaf(fmaf(-xh[e], c1, g[e] * w[k][e] - c0), rstd, m[e]);
+        g[e] = fmaf(fmaf(-xh[e], c1, g[e] * w[e] - c0), rstd, m[e]);
       }
-      store_row<E>(dx + col, dim - col, narrow<E, T>(g));
+      store_row<E>(dx, s[k], narrow<E, T>(g));
     }
   }
   if (a.d_weight == nullptr && a.d_bias == nullptr) return;
@@ -788,12 +909,11 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_grad_kernel(const 
   if constexpr (kRows == 1) {
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      const int col = (t + k * TPR) * E;
-      store_row<E, false>(out + col, dim - col, narrow<E, float>(sum_w[k]));
-      store_row<E, false>(out + dim4 + col, dim - col, narrow<E, float>(sum_b[k]));
+      store_row<E, false>(out, s[k], narrow<E, float>(sum_w[k]));
+      store_row<E, false>(out + dim4, s[k], narrow<E, float>(sum_b[k]));
     }
   } else {
-    __shared__ float part[256 * V * E];       // [group][V * E][TPR]: lanes next to each other
+    // [group][V][E][TPR], lanes side by side; a vector's neighbour's elements are left out
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
       __syncthreads();
@@ -801,86 +921,94 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_grad_kernel(const 
       for (int k = 0; k < V; ++k)
 #pragma unroll
         for (int e = 0; e < E; ++e)
-          part[(group * V * E + k * E + e) * TPR + t] = which ? sum_b[k][e] : sum_w[k][e];
+          lds[(group * V * E + k * E + e) * TPR + t] = which ? sum_b[k][e] : sum_w[k][e];
       __syncthreads();
-      for (int j = threadIdx.x; j < V * E * TPR; j += 256) {
-        float s = 0.f;
+      for (int j = threadIdx.x; j < V * E * TPR; j += kGradThreads) {
+        float x = 0.f;
 #pragma unroll
-        for (int g = 0; g < kRows; ++g) s += part[g * V * E * TPR + j];
-        const int ke = j / TPR, col = (j % TPR + ke / E * TPR) * E + ke % E;
-        if (col < dim) out[which * dim4 + col] = s;
+        for (int g = 0; g < kRows; ++g) x += lds[g * V * E * TPR + j];
+        const int ke = j / TPR, e = ke % E;
+        const Span at = span_of<E>(j % TPR + ke / E * TPR, dim);
+        if (e >= at.lo && e < at.hi) out[which * dim4 + at.col + e] = x;
       }
     }
   }
 }
 
 // Rows longer than the registers: the rows' gradient in two passes over each.
-template <typename T>
+template <typename T, typename W>
 __global__ __launch_bounds__(kLongThreads) void norm_grad_long_kernel(const zero_norm_grad_args a) {
   constexpr int E = 16 / int(sizeof(T));
-  __shared__ float lds[2 * (kLongThreads / 64)];
+  __shared__ float lds[2 * 2 * (kLongThreads / 64)];
   const int64_t row = blockIdx.x;
-  const int dim = int(a.dim);
+  const int dim = int(a.dim), vectors = (dim + E - 1) / E;
   const T* dy = static_cast<const T*>(a.d_y) + row * a.d_y_stride;
   const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
   const T* d_total = a.d_total != nullptr ? static_cast<const T*>(a.d_total) + row * a.d_total_stride : nullptr;
   T* dx = static_cast<T*>(a.d_x) + row * a.d_x_stride;
-  const bool bf16 = a.weight_type == ZERO_BF16;
   const float mean = a.rms ? 0.f : a.mean[row], rstd = a.rstd[row];
-  float s[2] = {0.f, 0.f};
-  for (int col = threadIdx.x * E; col < dim; col += kLongThreads * E) {
+  float c[2] = {0.f, 0.f};
+  for (int k = threadIdx.x; k < vectors; k += kLongThreads) {
+    const Span s = span_of<E>(k, dim);
     float g[E], xh[E], w[E];
-    widen<E, T>(load_row<E, false>(dy + col, dim - col), g);
-    widen<E, T>(load_row<E, false>(x + col, dim - col), xh);
-    load_weight<E>(a.weight, bf16, col, dim - col, 1.f, w);
+    widen<E, T>(load_row<E, false>(dy, s, dim), g);
+    widen<E, T>(load_row<E, false>(x, s, dim), xh);
+    widen<E, W>(load_weight<E, W>(a.weight, s, dim, 1.f), w);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const float gw = col + e < dim ? g[e] * w[e] : 0.f;
-      s[0] += gw;
-      s[1] = fmaf(gw, (xh[e] - mean) * rstd, s[1]);
+      g[e] *= w[e];
+      xh[e] = (xh[e] - mean) * rstd;
+    }
+    only_own<E>(s, g);
+    only_own<E>(s, xh);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      c[0] += g[e];
+      c[1] = fmaf(g[e], xh[e], c[1]);
     }
   }
-  row_sum<kLongThreads, 2>(s, lds, 0);
-  const float c0 = a.rms ? 0.f : s[0] / float(dim), c1 = s[1] / float(dim);
-  for (int col = threadIdx.x * E; col < dim; col += kLongThreads * E) {
+  row_sum<kLongThreads, 2>(c, lds, 0);
+  const float c0 = a.rms ? 0.f : c[0] / float(dim), c1 = c[1] / float(dim);
+  for (int k = threadIdx.x; k < vectors; k += kLongThreads) {
+    const Span s = span_of<E>(k, dim);
     float g[E], xh[E], w[E], m[E];
-    widen<E, T>(load_row<E, false>(dy + col, dim - col), g);
-    widen<E, T>(load_row<E, false>(x + col, dim - col), xh);
-    load_weight<E>(a.weight, bf16, col, dim - col, 1.f, w);
+    widen<E, T>(load_row<E, false>(dy, s, dim), g);
+    widen<E, T>(load_row<E, false>(x, s, dim), xh);
+    widen<E, W>(load_weight<E, W>(a.weight, s, dim, 1.f), w);
 #pragma unroll
     for (int e = 0; e < E; ++e) m[e] = 0.f;
-    if (d_total != nullptr) widen<E, T>(load_row<E, false>(d_total + col, dim - col), m);
+    if (d_total != nullptr) widen<E, T>(load_row<E, false>(d_total, s, dim), m);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       xh[e] = (xh[e] - mean) * rstd;
       g[e] = fmaf(fmaf(-xh[e], c1, g[e] * w[e] - c0), rstd, m[e]);
     }
-    store_row<E, false>(dx + col, dim - col, narrow<E, T>(g));
+    store_row<E, false>(dx, s, narrow<E, T>(g));
   }
 }
 
-// Their column sums: a thread takes E columns of every gridDim.y-th row. Before
+// Their column sums: a thread takes a vector of every gridDim.y-th row. Before
 // the rows' gradient, which may overwrite d_y or x.
 template <typename T>
 __global__ __launch_bounds__(256) void norm_grad_columns_kernel(const zero_norm_grad_args a, float* ws, int dim4) {
   constexpr int E = 16 / int(sizeof(T));
-  const int col = (int(blockIdx.x) * 256 + int(threadIdx.x)) * E, dim = int(a.dim);
-  if (col >= dim) return;
+  const int dim = int(a.dim);
+  const Span s = span_of<E>(int(blockIdx.x) * 256 + int(threadIdx.x), dim);
   float sum_w[E] = {}, sum_b[E] = {};
   for (int64_t row = blockIdx.y; row < a.n; row += gridDim.y) {
     const float mean = a.rms ? 0.f : uniform_load(a.mean + row), rstd = uniform_load(a.rstd + row);
     float g[E], xh[E];
-    widen<E, T>(load_row<E, false>(static_cast<const T*>(a.d_y) + row * a.d_y_stride + col, dim - col), g);
-    widen<E, T>(load_row<E, false>(static_cast<const T*>(a.x) + row * a.x_stride + col, dim - col), xh);
+    widen<E, T>(load_row<E, false>(static_cast<const T*>(a.d_y) + row * a.d_y_stride, s, dim), g);
+    widen<E, T>(load_row<E, false>(static_cast<const T*>(a.x) + row * a.x_stride, s, dim), xh);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       sum_w[e] = fmaf(g[e], (xh[e] - mean) * rstd, sum_w[e]);
       sum_b[e] += g[e];
     }
   }
-  float* out = ws + int64_t(blockIdx.y) * 2 * dim4 + col;
-  store_row<E, false>(out, dim - col, narrow<E, float>(sum_w));
-  store_row<E, false>(out + dim4, dim - col, narrow<E, float>(sum_b));
+  float* out = ws + int64_t(blockIdx.y) * 2 * dim4;
+  store_row<E, false>(out, s, narrow<E, float>(sum_w));
+  store_row<E, false>(out + dim4, s, narrow<E, float>(sum_b));
 }
 
 // The blocks' sums, added up: 64 columns a block, its 16 waves taking every
@@ -913,20 +1041,33 @@ __global__ __launch_bounds__(64 * kJoinWaves) void norm_grad_join_kernel(const f
   }
 }
 
-// The threads and vectors of a row of `dim` elements, `per` of them a vector.
-NormShape norm_shape(int64_t dim, int per, int top) {
-  const int64_t vectors = (dim + per - 1) / per;
-  static const NormShape shapes[] = {{16, 1}, {64, 1}, {64, 2}, {64, 4}, {256, 2}, {256, 4}, {1024, 2}, {1024, 4}};
+template <int N>
+using Int = std::integral_constant<int, N>;
+
+// A call's launch for its two element types.
+template <typename F>
+void by_types(int32_t first, int32_t second, const F& go) {
+  if (first == ZERO_BF16) second == ZERO_BF16 ? go(uint16_t(), uint16_t()) : go(uint16_t(), float());
+  else second == ZERO_BF16 ? go(float(), uint16_t()) : go(float(), float());
+}
+
+// How a row of `vectors` 16-byte vectors is spread over threads: few vectors a
+// thread, so that many waves share the latency.
+NormShape norm_shape(int64_t vectors) {
+  static const NormShape shapes[] = {{16, 1}, {64, 1}, {64, 2}, {256, 1}, {256, 2}, {256, 4}, {1024, 2}, {1024, 4}};
   for (const NormShape& s : shapes)
-    if (int64_t(s.threads) * s.vectors >= vectors && s.threads * s.vectors <= top) return s;
+    if (int64_t(s.threads) * s.vectors >= vectors) return s;
   return {0, 0};
 }
 
-// The longest row of the gradient kernel: its sums take 16 registers twice with 1024 threads.
-constexpr int kNormGradDim = 16384;
-
+// The same for the gradient, whose two sums a column limit a thread to 8 elements, 16 for the longest rows.
 NormShape norm_grad_shape(int64_t dim, int per) {
-  return dim > kNormGradDim ? NormShape{0, 0} : norm_shape(dim, per, 1 << 20);
+  const int64_t vectors = (dim + per - 1) / per;
+  static const int threads[] = {64, 128, 256, 512, 1024};
+  if (vectors <= 16) return {16, 1};
+  for (int t : threads)
+    if (int64_t(t) * (8 / per) >= vectors) return {t, 8 / per};
+  return vectors <= 2 * 1024 * (8 / per) ? NormShape{1024, 16 / per} : NormShape{0, 0};
 }
 
 }  // namespace
@@ -935,7 +1076,7 @@ namespace zero {
 
 int64_t norm_grad_blocks(int64_t n, int64_t dim) {
   const NormShape s = norm_grad_shape(dim, 8);
-  const int64_t rows = s.threads == 0 ? 16 : s.threads < 256 ? 256 / s.threads : 1;
+  const int64_t rows = s.threads == 0 ? 16 : kGradThreads / s.threads;
   return std::max<int64_t>(1, std::min<int64_t>((n + rows - 1) / rows, 512));
 }
 
@@ -952,20 +1093,16 @@ int launch_embedding(const void* tokens, bool wide, int64_t n, const void* table
         tokens, wide, int(n), static_cast<const T*>(table), int(rows), int(dim), int(tiles), scale,
         static_cast<O*>(out), out_stride);
   };
-  if (table_type == ZERO_BF16) out_type == ZERO_BF16 ? go(uint16_t(), uint16_t()) : go(uint16_t(), float());
-  else out_type == ZERO_BF16 ? go(float(), uint16_t()) : go(float(), float());
+  by_types(table_type, out_type, go);
   return launched(who);
 }
 
 int launch_token_order(const void* tokens, bool wide, int64_t n, int64_t rows, int32_t* order, hipStream_t stream,
                        const char* who) {
-  const Order o(n, rows);
+  const Order o(n);
   if (n <= kRankTokens) {
-    const int rank_blocks = std::max<int>(1, int(n + 63) / 64);
-    const int bit_blocks = int((rows + 32 * kBitWords - 1) / (32 * kBitWords));
-    order_rank_kernel<<<dim3(uint32_t(rank_blocks + bit_blocks)), kRankThreads, 0, stream>>>(
-        tokens, wide, int(n), int(rows), rank_blocks, order, order + o.row, order + o.pos,
-        reinterpret_cast<uint32_t*>(order + o.bits));
+    order_rank_kernel<<<dim3(uint32_t(std::max<int64_t>(1, (n + 31) / 32))), kRankThreads, 0, stream>>>(
+        tokens, wide, int(n), int(rows), order, order + o.row, order + o.pos);
     return launched(who);
   }
   const int bits = row_bits(rows), passes = (bits + kSortBits - 1) / kSortBits, each = (bits + passes - 1) / passes;
@@ -978,7 +1115,6 @@ int launch_token_order(const void* tokens, bool wide, int64_t n, int64_t rows, i
   a.digits = order + o.digits;
   a.live = order + o.live;
   a.head = order;
-  a.present = reinterpret_cast<uint32_t*>(order + o.bits);
   int32_t *row[2] = {order + o.row, order + o.row2}, *pos[2] = {order + o.pos, order + o.pos2};
   for (int p = 0; p < passes; ++p) {
     const int to = (passes - 1 - p) & 1;       // the last pass ends in the order's own arrays
@@ -1004,12 +1140,11 @@ int launch_embedding_grad(const int32_t* order, int64_t n, int64_t rows, int64_t
                           int32_t out_type, int64_t out_stride, float scale, void* grad, int32_t grad_type,
                           int64_t first, int64_t count, bool accumulate, float* ws, hipStream_t stream,
                           const char* who) {
-  const Order o(n, rows);
+  const Order o(n);
   EmbeddingGradArgs a{};
   a.head = order;
   a.row = order + o.row;
   a.pos = order + o.pos;
-  a.present = reinterpret_cast<const uint32_t*>(order + o.bits);
   a.d_out = d_out;
   a.grad = grad;
   a.ws = ws;
@@ -1019,7 +1154,8 @@ int launch_embedding_grad(const int32_t* order, int64_t n, int64_t rows, int64_t
   a.scale = scale;
   a.dim = int32_t(dim);
   a.dim4 = int32_t((dim + 3) / 4 * 4);
-  a.pieces = int32_t((n + kPiece - 1) / kPiece);
+  a.piece = embedding_piece(n);
+  a.pieces = int32_t(embedding_pieces(n));
   a.row_lo = int32_t(first / dim);
   a.row_hi = int32_t((first + count + dim - 1) / dim);
   a.accumulate = accumulate;
@@ -1028,40 +1164,43 @@ int launch_embedding_grad(const int32_t* order, int64_t n, int64_t rows, int64_t
     using G = decltype(gv);
     constexpr int E = sizeof(T) == 2 && sizeof(G) == 2 ? 8 : 4;
     a.tiles = int32_t((dim + 64 * E - 1) / (64 * E));
-    const int64_t sums = (int64_t(a.pieces) * a.tiles + 3) / 4, fills = accumulate ? 0 : (a.row_hi - a.row_lo + 3) / 4;
+    const int64_t sums = (int64_t(a.pieces) * a.tiles + 3) / 4;
+    const int touched = a.row_hi - a.row_lo;
+    a.fill_rows = std::min(std::max(touched / 2048, 1), 16);
+    const int64_t fills = accumulate ? 0 : (touched + 4 * a.fill_rows - 1) / (4 * a.fill_rows);
     a.sum_blocks = int32_t(sums);
     if (sums + fills > 0)
       embedding_grad_kernel<T, G, E><<<dim3(uint32_t(sums + fills)), 256, 0, stream>>>(a);
     if (a.pieces > 1) embedding_join_kernel<G, E><<<dim3(uint32_t(sums)), 256, 0, stream>>>(a);
   };
-  if (out_type == ZERO_BF16) grad_type == ZERO_BF16 ? go(uint16_t(), uint16_t()) : go(uint16_t(), float());
-  else grad_type == ZERO_BF16 ? go(float(), uint16_t()) : go(float(), float());
+  by_types(out_type, grad_type, go);
   return launched(who);
 }
 
 int launch_norm(const zero_norm_args& a, hipStream_t stream, const char* who) {
-  const auto go = [&](auto tv) {
+  const auto go = [&](auto tv, auto wv) {
     using T = decltype(tv);
-    const NormShape s = norm_shape(a.dim, 16 / int(sizeof(T)), 1 << 20);
+    using W = decltype(wv);
+    constexpr int E = 16 / int(sizeof(T));
+    const NormShape s = norm_shape((a.dim + E - 1) / E);
     const uint32_t rows = s.threads == 0 || s.threads >= 256 ? 1u : 256u / uint32_t(s.threads);
     const dim3 grid{uint32_t((a.n + rows - 1) / rows)};
-#define ZERO_NORM(TPR, V) \
-  if (s.threads == TPR && s.vectors == V) { \
-    norm_kernel<T, TPR, V><<<grid, TPR < 256 ? 256 : TPR, 0, stream>>>(a); \
-    return; \
-  }
-    ZERO_NORM(16, 1)
-    ZERO_NORM(64, 1)
-    ZERO_NORM(64, 2)
-    ZERO_NORM(64, 4)
-    ZERO_NORM(256, 2)
-    ZERO_NORM(256, 4)
-    ZERO_NORM(1024, 2)
-    ZERO_NORM(1024, 4)
-#undef ZERO_NORM
-    norm_long_kernel<T><<<grid, kLongThreads, 0, stream>>>(a);
+    const auto spread = [&](auto threads, auto vectors) {
+      constexpr int TPR = decltype(threads)::value, V = decltype(vectors)::value;
+      if (s.threads != TPR || s.vectors != V) return;
+      norm_kernel<T, W, TPR, V><<<grid, TPR < 256 ? 256 : TPR, 0, stream>>>(a);
+    };
+    spread(Int<16>(), Int<1>());
+    spread(Int<64>(), Int<1>());
+    spread(Int<64>(), Int<2>());
+    spread(Int<256>(), Int<1>());
+    spread(Int<256>(), Int<2>());
+    spread(Int<256>(), Int<4>());
+    spread(Int<1024>(), Int<2>());
+    spread(Int<1024>(), Int<4>());
+    if (s.threads == 0) norm_long_kernel<T, W><<<grid, kLongThreads, 0, stream>>>(a);
   };
-  a.type == ZERO_BF16 ? go(uint16_t()) : go(float());
+  by_types(a.type, a.weight_type, go);
   return launched(who);
 }
 
@@ -1069,31 +1208,31 @@ int launch_norm_grad(const zero_norm_grad_args& a, float* ws, hipStream_t stream
   const int64_t blocks = norm_grad_blocks(a.n, a.dim);
   const int dim = int(a.dim), dim4 = (dim + 3) / 4 * 4;
   const bool sums = a.d_weight != nullptr || a.d_bias != nullptr;
-  const auto go = [&](auto tv) {
+  const auto go = [&](auto tv, auto wv) {
     using T = decltype(tv);
+    using W = decltype(wv);
     constexpr int E = 16 / int(sizeof(T));
     const NormShape s = norm_grad_shape(a.dim, E);
-    const dim3 grid{uint32_t(blocks)};
-#define ZERO_NORM(TPR, V) \
-  if (s.threads == TPR && s.vectors == V) { \
-    norm_grad_kernel<T, TPR, V><<<grid, TPR < 256 ? 256 : TPR, 0, stream>>>(a, ws, dim4); \
-    return; \
-  }
-    ZERO_NORM(16, 1)
-    ZERO_NORM(64, 1)
-    ZERO_NORM(64, 2)
-    ZERO_NORM(64, 4)
-    ZERO_NORM(256, 2)
-    ZERO_NORM(256, 4)
-    ZERO_NORM(1024, 2)
-    if constexpr (sizeof(T) == 4) ZERO_NORM(1024, 4)
-#undef ZERO_NORM
+    const auto spread = [&](auto threads, auto vectors) {
+      constexpr int TPR = decltype(threads)::value, V = decltype(vectors)::value;
+      if (s.threads != TPR || s.vectors != V) return;
+      norm_grad_kernel<T, W, TPR, V><<<dim3(uint32_t(blocks)), kGradThreads, 0, stream>>>(a, ws, dim4);
+    };
+    spread(Int<16>(), Int<1>());
+    spread(Int<64>(), Int<8 / E>());
+    spread(Int<128>(), Int<8 / E>());
+    spread(Int<256>(), Int<8 / E>());
+    spread(Int<512>(), Int<8 / E>());
+    spread(Int<1024>(), Int<8 / E>());
+    spread(Int<1024>(), Int<16 / E>());
+    if (s.threads != 0) return;
     if (sums)
       norm_grad_columns_kernel<T><<<dim3(uint32_t((dim + 256 * E - 1) / (256 * E)), uint32_t(blocks)), 256, 0, stream>>>(
           a, ws, dim4);
-    if (a.d_x != nullptr && a.n > 0) norm_grad_long_kernel<T><<<dim3(uint32_t(a.n)), kLongThreads, 0, stream>>>(a);
+    if (a.d_x != nullptr && a.n > 0)
+      norm_grad_long_kernel<T, W><<<dim3(uint32_t(a.n)), kLongThreads, 0, stream>>>(a);
   };
-  a.type == ZERO_BF16 ? go(uint16_t()) : go(float());
+  by_types(a.type, a.weight_type, go);
   if (sums) {
     const dim3 grid(uint32_t((dim + 63) / 64), 2);
     if (a.grad_type == ZERO_BF16)

@@ -12,32 +12,32 @@
 
 namespace zero {
 
-// Sorted tokens that one wave of the table's gradient sums, and a workspace's
-// rows: two sums for each such piece.
-constexpr int kPiece = ZERO_EMBEDDING_PIECE;
+// Sorted tokens that one wave of the table's gradient sums (a multiple of 8), and
+// a workspace's rows: two sums for each such piece.
+inline int embedding_piece(int64_t n) { return n <= 4096 ? 8 : 32; }
+inline int64_t embedding_pieces(int64_t n) { return (n + embedding_piece(n) - 1) / embedding_piece(n); }
 
 // Tokens that one block of the sort takes, and the bits of one of its passes.
 constexpr int kSortThreads = 256, kSortItems = 8, kSortBlock = kSortThreads * kSortItems;
 constexpr int kSortBits = 9, kSortDigits = 1 << kSortBits;
 
 // Up to this many tokens are sorted by counting, in one launch.
-constexpr int64_t kRankTokens = 4096;
+constexpr int64_t kRankTokens = 8192;
 
 // The parts of an order, in 32-bit words from its start: head (word 0: how many
-// tokens lie in the table), the sorted tokens' rows and positions, a bit per
-// row of the table; then scratch of the sort: rows and positions between two
-// passes, and per block its tokens in the table and its digits' counts.
+// tokens lie in the table), the sorted tokens' rows and positions; then scratch of
+// the sort: rows and positions between two passes, and per block its tokens in
+// the table and its digits' counts.
 struct Order {
-  int64_t row, pos, bits, row2, pos2, live, digits, words;
+  int64_t row, pos, row2, pos2, live, digits, words;
   int64_t blocks;
-  Order(int64_t n, int64_t rows) {
-    auto up = [](int64_t k) { return (k + 3) / 4 * 4; };
+  Order(int64_t n) {
+    auto up = [](int64_t k) { return (k + 7) / 8 * 8; };
     blocks = (n + kSortBlock - 1) / kSortBlock;
     const int64_t scratch = n > kRankTokens ? 1 : 0;
-    row = 4;
-    pos = row + up(n);
-    bits = pos + up(n);
-    row2 = bits + up((rows + 31) / 32);
+    row = 8;
+    pos = row + up(n) + 8;      // read by eights and one more
+    row2 = pos + up(n) + 8;
     pos2 = row2 + scratch * up(n);
     live = pos2 + scratch * up(n);
     digits = live + scratch * up(blocks);

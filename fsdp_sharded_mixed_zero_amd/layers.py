@@ -11,8 +11,9 @@ one. Streams and errors are those of ``zero``.
 from __future__ import annotations
 
 import ctypes
+import struct
 
-from . import tensors, zero
+from . import zero
 from .tensors import ZERO_BF16, ZERO_F32  # noqa: F401 (the types of a call's arrays)
 
 ZERO_I32 = 2
@@ -20,7 +21,6 @@ ZERO_I64 = 3
 ZERO_LAYER_ROWS = 16777215
 ZERO_LAYER_DIM = 1048576
 ZERO_LAYER_ELEMS = 34359738368
-ZERO_EMBEDDING_PIECE = 32
 
 _VP = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -46,9 +46,9 @@ _SIGNATURES = {
     "zero_embedding_grad_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
     "zero_embedding_grad": (ctypes.c_int, [_VP, _I64, _I64, _I64, _VP, _I32, _I64, ctypes.c_double, _VP, _I32, _I64,
                                            _I64, _I32, _VP, ctypes.c_size_t, _VP]),
-    "zero_norm": (ctypes.c_int, [ctypes.POINTER(zero_norm_args), _VP]),
+    "zero_norm": (ctypes.c_int, [_VP, _VP]),
     "zero_norm_grad_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
-    "zero_norm_grad": (ctypes.c_int, [ctypes.POINTER(zero_norm_grad_args), _VP, ctypes.c_size_t, _VP]),
+    "zero_norm_grad": (ctypes.c_int, [_VP, _VP, ctypes.c_size_t, _VP]),
 }
 
 _lib = None
@@ -67,10 +67,17 @@ def library():
     return _lib
 
 
-def _call(name, stream, *args):
-    rc = getattr(_lib or library(), name)(*args, tensors._stream(stream))
-    if rc:
-        zero._check(name, rc)
+_torch = _C = _TYPES = _IDS = None
+
+
+def _load():
+    """torch and the library, at the first call."""
+    global _torch, _C, _TYPES, _IDS
+    import torch
+    library()
+    _TYPES = {torch.bfloat16: ZERO_BF16, torch.float32: ZERO_F32}
+    _IDS = {torch.int32: ZERO_I32, torch.int64: ZERO_I64}
+    _C, _torch = torch._C, torch
 
 
 def _sized(name, *sizes):
@@ -81,72 +88,87 @@ def _sized(name, *sizes):
     return nbytes
 
 
-class _Device:
-    """The device that a call's tensors share: the current one."""
+# The checks below cost a call 0.1 us each, of the 4 to 7 that it takes in all, so a tensor's
+# attributes are read once and what is wrong is found out after the fact.
 
-    def __init__(self):
-        import torch
-        self.torch = torch
-        self.at = torch.cuda.current_device() if torch.cuda.is_available() else None
-
-    def check(self, t, what):
-        if not getattr(t, "is_cuda", False):
-            raise TypeError(f"{what}: device memory expected, got {type(t).__name__}")
-        if t.device.index != self.at:
-            raise ValueError(f"{what} is on {t.device}, the current device is {self.at}")
-
-    def rows(self, t, what, shape=None, dtype=None):
-        """Address and stride of an array of rows."""
-        self.check(t, what)
-        if t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
-            raise ValueError(f"{what}: {'two dimensions' if shape is None else tuple(shape)} expected, got "
-                             f"{tuple(t.shape)}")
-        if dtype is not None and t.dtype != dtype:
-            raise TypeError(f"{what}: {dtype} expected, got {t.dtype}")
-        n, dim = t.shape
-        if dim > 1 and t.stride(1) != 1:
-            raise ValueError(f"{what}: the elements of a row have to be consecutive")
-        return t.data_ptr() if t.numel() else None, int(t.stride(0)) if n > 1 else int(dim)
-
-    def flat(self, t, what, count, dtypes):
-        """Address of an array without gaps of `count` elements (None: as many as it has)."""
-        self.check(t, what)
-        if t.dtype not in dtypes:
-            raise TypeError(f"{what}: {' or '.join(str(d) for d in dtypes)} expected, got {t.dtype}")
-        if count is not None and t.numel() != count:
-            raise ValueError(f"{what}: {t.numel()} elements, {count} expected")
-        if not t.is_contiguous():
-            raise ValueError(f"{what}: a contiguous tensor is expected")
-        return t.data_ptr() if t.numel() else None
-
-    def memory(self, t, what):
-        """Address and bytes of an order or a workspace."""
-        self.check(t, what)
-        if not t.is_contiguous():
-            raise ValueError(f"{what}: a contiguous tensor is expected")
-        return t.data_ptr(), t.numel() * t.element_size()
-
-    def tokens(self, t):
-        torch = self.torch
-        p = self.flat(t, "tokens", None, (torch.int32, torch.int64))
-        return p, ZERO_I32 if t.dtype == torch.int32 else ZERO_I64, t.numel()
+def _device():
+    """The current device, where the library's launches go."""
+    if _torch is None:
+        _load()
+    try:
+        return _C._cuda_getDevice()
+    except RuntimeError:        # no device: every tensor is refused
+        return -1
 
 
-def _type(t, what):
-    return tensors._type_of(t.dtype, what)
+def _elsewhere(t, what, dev):
+    """The error of a tensor that is not on the current device."""
+    if not getattr(t, "is_cuda", False):
+        raise TypeError(f"{what}: device memory expected, got {type(t).__name__}"
+                        f"{' on ' + str(t.device) if hasattr(t, 'device') else ''}")
+    raise ValueError(f"{what} is on {t.device}, the current device is {dev}")
+
+
+def _on(t, dev):
+    try:
+        return t.get_device() == dev and dev >= 0
+    except AttributeError:
+        return False
+
+
+def _rows(t, what, dev, shape=None, dtype=None):
+    """(address, stride, shape) of an array of rows."""
+    if not _on(t, dev):
+        _elsewhere(t, what, dev)
+    size = t.shape
+    if len(size) != 2 or (shape is not None and size != shape):
+        raise ValueError(f"{what}: {'two dimensions' if shape is None else tuple(shape)} expected, got {tuple(size)}")
+    if t.dtype is not dtype and (dtype is not None or t.dtype not in _TYPES):
+        raise TypeError(f"{what}: {'bfloat16 or float32' if dtype is None else dtype} expected, got {t.dtype}")
+    step, one = t.stride()
+    if one != 1 and size[1] > 1:
+        raise ValueError(f"{what}: the elements of a row have to be consecutive")
+    return t.data_ptr(), step if size[0] > 1 else size[1], size
+
+
+def _flat(t, what, dev, count, dtypes):
+    """Address of an array without gaps of `count` elements (None: as many as it has)."""
+    if not _on(t, dev):
+        _elsewhere(t, what, dev)
+    if t.dtype not in dtypes:
+        raise TypeError(f"{what}: {' or '.join(str(d) for d in dtypes)} expected, got {t.dtype}")
+    if count is not None and t.numel() != count:
+        raise ValueError(f"{what}: {t.numel()} elements, {count} expected")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous tensor is expected")
+    return t.data_ptr()
+
+
+def _memory(t, what, dev):
+    """(address, bytes) of an order or a workspace, of any type."""
+    if not _on(t, dev):
+        _elsewhere(t, what, dev)
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous tensor is expected")
+    return t.data_ptr(), t.nbytes
+
+
+def _stream(stream, dev):
+    return _C._cuda_getCurrentRawStream(dev) if stream is None else zero._stream(stream)
 
 
 def zero_embedding(tokens, table, out, scale: float = 1.0, stream=None):
     """``out`` [number of tokens, dim] = scale * rows of ``table`` [rows, dim]."""
-    dev = _Device()
-    ids, id_type, n = dev.tokens(tokens)
-    src, _ = dev.rows(table, "table")
-    if not table.is_contiguous():
-        raise ValueError("table: a contiguous tensor is expected")
-    rows, dim = table.shape
-    dst, stride = dev.rows(out, "out", (n, dim))
-    _call("zero_embedding", stream, ids, id_type, n, src, _type(table, "table"), rows, dim, scale, dst,
-          _type(out, "out"), stride)
+    dev = _device()
+    ids, n = _flat(tokens, "tokens", dev, None, _IDS), tokens.numel()
+    src, step, (rows, dim) = _rows(table, "table", dev)
+    if step != dim:
+        raise ValueError("table: rows without gaps are expected")
+    dst, stride, _ = _rows(out, "out", dev, (n, dim))
+    rc = _lib.zero_embedding(ids, _IDS[tokens.dtype], n, src, _TYPES[table.dtype], rows, dim, scale, dst,
+                             _TYPES[out.dtype], stride, _stream(stream, dev))
+    if rc:
+        zero._check("zero_embedding", rc)
 
 
 def zero_token_order_bytes(n: int, rows: int) -> int:
@@ -155,10 +177,12 @@ def zero_token_order_bytes(n: int, rows: int) -> int:
 
 def zero_token_order(tokens, rows: int, order, stream=None):
     """``order``: device memory of at least zero_token_order_bytes bytes, of any type."""
-    dev = _Device()
-    ids, id_type, n = dev.tokens(tokens)
-    p, nbytes = dev.memory(order, "order")
-    _call("zero_token_order", stream, ids, id_type, n, rows, p, nbytes)
+    dev = _device()
+    ids = _flat(tokens, "tokens", dev, None, _IDS)
+    p, nbytes = _memory(order, "order", dev)
+    rc = _lib.zero_token_order(ids, _IDS[tokens.dtype], tokens.numel(), rows, p, nbytes, _stream(stream, dev))
+    if rc:
+        zero._check("zero_token_order", rc)
 
 
 def zero_embedding_grad_workspace_bytes(n: int, dim: int) -> int:
@@ -170,26 +194,33 @@ def zero_embedding_grad(order, rows: int, d_out, grad, workspace, scale: float =
     """``d_out`` [number of tokens, dim], in the tokens' order; ``grad``: the
     elements of the flat [rows, dim] gradient from ``first`` on, as many as it has
     (the whole table's by default)."""
-    dev = _Device()
-    src, stride = dev.rows(d_out, "d_out")
-    n, dim = d_out.shape
-    p, order_bytes = dev.memory(order, "order")
-    zero._need(order, zero_token_order_bytes(n, rows), "order")
-    ws, ws_bytes = dev.memory(workspace, "workspace")
-    dst = dev.flat(grad, "grad", None, (dev.torch.bfloat16, dev.torch.float32))
-    _call("zero_embedding_grad", stream, p, n, rows, dim, src, _type(d_out, "d_out"), stride, scale, dst,
-          _type(grad, "grad"), first, grad.numel(), 1 if accumulate else 0, ws, ws_bytes)
+    dev = _device()
+    src, stride, (n, dim) = _rows(d_out, "d_out", dev)
+    p, order_bytes = _memory(order, "order", dev)
+    need = _lib.zero_token_order_bytes(n, rows)
+    if order_bytes < need:
+        raise ValueError(f"order: {order_bytes} bytes given, the call reaches {need}")
+    ws, ws_bytes = _memory(workspace, "workspace", dev)
+    dst = _flat(grad, "grad", dev, None, _TYPES)
+    rc = _lib.zero_embedding_grad(p, n, rows, dim, src, _TYPES[d_out.dtype], stride, scale, dst, _TYPES[grad.dtype],
+                                  first, grad.numel(), 1 if accumulate else 0, ws, ws_bytes, _stream(stream, dev))
+    if rc:
+        zero._check("zero_embedding_grad", rc)
 
 
-def _vectors(dev, dim, pairs):
-    """Addresses of the vectors that are there, which share one type, and that type."""
-    kind, at = None, {}
-    for name, t in pairs.items():
-        if t is None:
-            continue
-        at[name] = dev.flat(t, name, dim, (dev.torch.bfloat16, dev.torch.float32) if kind is None else (kind,))
-        kind = t.dtype
-    return at, ZERO_F32 if kind is None or kind == dev.torch.float32 else ZERO_BF16
+def _vectors(dev, dim, a, a_name, b, b_name):
+    """Addresses of two vectors, either of which may be missing, and the type that they share."""
+    if a is None and b is None:
+        return 0, 0, ZERO_F32
+    kind = (b if a is None else a).dtype
+    pa = 0 if a is None else _flat(a, a_name, dev, dim, _TYPES)
+    pb = 0 if b is None else _flat(b, b_name, dev, dim, _TYPES if a is None else (kind,))
+    return pa, pb, _TYPES[kind]
+
+
+# zero_norm_args and zero_norm_grad_args as bytes: a third of the time of a ctypes structure
+_NORM = struct.Struct("8Q6qd4i")
+_NORM_GRAD = struct.Struct("9Q6q6i")
 
 
 def zero_norm(x, y, mean=None, rstd=None, weight=None, bias=None, eps: float = 1e-5, residual=None, total=None,
@@ -197,23 +228,24 @@ def zero_norm(x, y, mean=None, rstd=None, weight=None, bias=None, eps: float = 1
     """``y`` = the norm of the rows of ``x`` [n, dim], or of ``total`` = x +
     ``residual``; ``mean`` and ``rstd`` [n], float32, for the backward pass.
     ``rms``: without the mean."""
-    dev = _Device()
-    n, dim = x.shape if x.dim() == 2 else (0, 0)
-    a = zero_norm_args(n=n, dim=dim, eps=eps, type=_type(x, "x"), rms=1 if rms else 0)
-    for name, t in (("x", x), ("y", y), ("residual", residual), ("total", total)):
-        if t is not None:
-            p, stride = dev.rows(t, name, None if t is x else (n, dim), x.dtype)
-            setattr(a, name, p)
-            setattr(a, name + "_stride", stride)
+    dev = _device()
+    px, sx, size = _rows(x, "x", dev)
+    kind, (n, dim) = x.dtype, size
+    py, sy, _ = _rows(y, "y", dev, size, kind)
     if (residual is None) != (total is None):
         raise ValueError("residual and total: both or neither")
-    at, a.weight_type = _vectors(dev, dim, {"weight": weight, "bias": bias})
-    for name, p in at.items():
-        setattr(a, name, p)
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        if t is not None:
-            setattr(a, name, dev.flat(t, name, n, (dev.torch.float32,)))
-    _call("zero_norm", stream, ctypes.byref(a))
+    pr = pt = sr = st = 0
+    if total is not None:
+        pr, sr, _ = _rows(residual, "residual", dev, size, kind)
+        pt, st, _ = _rows(total, "total", dev, size, kind)
+    pw, pb, w_type = _vectors(dev, dim, weight, "weight", bias, "bias")
+    f32 = (_torch.float32,)
+    pm = 0 if mean is None else _flat(mean, "mean", dev, n, f32)
+    ps = 0 if rstd is None else _flat(rstd, "rstd", dev, n, f32)
+    rc = _lib.zero_norm(_NORM.pack(px, pr, pt, py, pw, pb, pm, ps, n, dim, sx, sr, st, sy, eps, _TYPES[kind], w_type,
+                                   1 if rms else 0, 0), _stream(stream, dev))
+    if rc:
+        zero._check("zero_norm", rc)
 
 
 def zero_norm_grad_workspace_bytes(n: int, dim: int) -> int:
@@ -226,20 +258,25 @@ def zero_norm_grad(d_y, x, mean, rstd, d_x=None, workspace=None, weight=None, d_
     residual was added); ``d_total``: the gradient that reaches it by the skip path;
     ``d_x``: of x and of the residual alike. ``accumulate``: add to ``d_weight``
     and ``d_bias``."""
-    dev = _Device()
-    n, dim = x.shape if x.dim() == 2 else (0, 0)
-    a = zero_norm_grad_args(n=n, dim=dim, type=_type(x, "x"), rms=1 if rms else 0, accumulate=1 if accumulate else 0)
-    for name, t in (("x", x), ("d_y", d_y), ("d_total", d_total), ("d_x", d_x)):
-        if t is not None:
-            p, stride = dev.rows(t, name, None if t is x else (n, dim), x.dtype)
-            setattr(a, name, p)
-            setattr(a, name + "_stride", stride)
-    at, a.weight_type = _vectors(dev, dim, {"weight": weight})
-    more, a.grad_type = _vectors(dev, dim, {"d_weight": d_weight, "d_bias": d_bias})
-    for name, p in {**at, **more}.items():
-        setattr(a, name, p)
-    for name, t in (("mean", None if rms else mean), ("rstd", rstd)):
-        if t is not None:
-            setattr(a, name, dev.flat(t, name, n, (dev.torch.float32,)))
-    ws, ws_bytes = (None, 0) if workspace is None else dev.memory(workspace, "workspace")
-    _call("zero_norm_grad", stream, ctypes.byref(a), ws, ws_bytes)
+    dev = _device()
+    px, sx, size = _rows(x, "x", dev)
+    kind, (n, dim) = x.dtype, size
+    py, sy, _ = _rows(d_y, "d_y", dev, size, kind)
+    pt = st = pd = sd = ws = ws_bytes = pm = 0
+    if d_total is not None:
+        pt, st, _ = _rows(d_total, "d_total", dev, size, kind)
+    if d_x is not None:
+        pd, sd, _ = _rows(d_x, "d_x", dev, size, kind)
+    pw, _, w_type = _vectors(dev, dim, weight, "weight", None, "")
+    pgw, pgb, g_type = _vectors(dev, dim, d_weight, "d_weight", d_bias, "d_bias")
+    f32 = (_torch.float32,)
+    if not rms:
+        pm = _flat(mean, "mean", dev, n, f32)
+    ps = _flat(rstd, "rstd", dev, n, f32)
+    if workspace is not None:
+        ws, ws_bytes = _memory(workspace, "workspace", dev)
+    rc = _lib.zero_norm_grad(_NORM_GRAD.pack(py, px, pt, pd, pw, pm, ps, pgw, pgb, n, dim, sy, sx, st, sd, _TYPES[kind],
+                                             w_type, g_type, 1 if rms else 0, 1 if accumulate else 0, 0),
+                             ws, ws_bytes, _stream(stream, dev))
+    if rc:
+        zero._check("zero_norm_grad", rc)

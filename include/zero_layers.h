@@ -66,8 +66,8 @@ int zero_embedding(const void* tokens, int32_t token_type, int64_t n, const void
  * zero_embedding_grad calls on the same tokens (parts of the table, several
  * tables with the same tokens).
  *   order       device memory of at least zero_token_order_bytes(n, rows) bytes,
- *               16-byte aligned: the sorted tokens, a bit per row, and scratch.
- *               It holds until the next call on it
+ *               16-byte aligned: the sorted tokens and scratch. It holds until the next
+ *               call on it
  * Errors: as zero_embedding; ZERO_EINVAL for too few bytes.
  * zero_token_order_bytes returns 0 for sizes outside the limits. */
 size_t zero_token_order_bytes(int64_t n, int64_t rows);
@@ -82,8 +82,8 @@ int zero_token_order(const void* tokens, int32_t token_type, int64_t n, int64_t 
  * inside a row, as a shard does (zero_layout's segments: first = src_off, grad at
  * dst_off of the shard). Written, rows without a token get zeros; added, they are
  * neither read nor written.
- * A row's terms are added in fp32 in ascending position, in pieces of up to
- * ZERO_EMBEDDING_PIECE sorted tokens whose sums are then added in order.
+ * A row's terms are added in fp32 in ascending position, in pieces of consecutive
+ * sorted tokens whose sums are then added in order.
  *   order       as zero_token_order has written it for the same n and rows
  *   d_out       [n, dim] with its stride, ZERO_BF16 or ZERO_F32; rows of tokens
  *               outside the table are not read
@@ -95,7 +95,6 @@ int zero_token_order(const void* tokens, int32_t token_type, int64_t n, int64_t 
  * the table, a scale that is not finite, a workspace that is too small, or an output
  * or workspace that overlaps another array; ZERO_EHIP if a launch fails.
  * zero_embedding_grad_workspace_bytes returns 0 for sizes outside the limits. */
-#define ZERO_EMBEDDING_PIECE 32
 size_t zero_embedding_grad_workspace_bytes(int64_t n, int64_t dim);
 int zero_embedding_grad(const void* order, int64_t n, int64_t rows, int64_t dim, const void* d_out,
                         int32_t out_type, int64_t out_stride, double scale, void* grad, int32_t grad_type,
