@@ -160,22 +160,16 @@ __device__ __forceinline__ void store_row(T* p, const Span& s, const Words<E, T>
 
 // ------------------------------------------------------------------- lookup
 
-// Token t's row, or `rows` for a token outside the table.
-__device__ __forceinline__ int table_row(const void* tokens, bool wide, int64_t t, int rows) {
-  const int64_t k = wide ? static_cast<const int64_t*>(tokens)[t] : int64_t(static_cast<const int32_t*>(tokens)[t]);
-  return k >= 0 && k < rows ? int(k) : rows;
-}
-__device__ __forceinline__ int uniform_row(const void* tokens, bool wide, int64_t t, int rows) {
-  const int64_t k = wide ? uniform_load(static_cast<const int64_t*>(tokens) + t)
-                         : int64_t(uniform_load(static_cast<const int32_t*>(tokens) + t));
-  return k >= 0 && k < rows ? int(k) : rows;
+// A token's row, or `rows` for one outside the table.
+template <typename I>
+__device__ __forceinline__ int table_row(I token, int rows) {
+  return token >= 0 && token < I(rows) ? int(token) : rows;
 }
 
 constexpr int kLookupRows = 4;      // rows of a wave: as many loads in flight
 
-template <typename T, typename O, int E>
-__global__ __launch_bounds__(256) void embedding_kernel(const void* __restrict__ tokens, int wide, int n,
-                                                        const T* __restrict__ table, int rows, int dim, int tiles,
+template <typename I, typename T, typename O, int E>
+__global__ __launch_bounds__(256) void embedding_kernel(const I* __restrict__ tokens, int n, const T* __restrict__ table, int rows, int dim, int tiles,
                                                         float scale, O* __restrict__ out, int64_t stride) {
   const uint32_t w = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t0 = int64_t(w / uint32_t(tiles)) * kLookupRows;
@@ -184,7 +178,7 @@ __global__ __launch_bounds__(256) void embedding_kernel(const void* __restrict__
   int row[kLookupRows];
   Words<E, T> x[kLookupRows];
 #pragma unroll
-  for (int k = 0; k < kLookupRows; ++k) row[k] = t0 + k < n ? uniform_row(tokens, wide, t0 + k, rows) : rows;
+  for (int k = 0; k < kLookupRows; ++k) row[k] = table_row(uniform_load(tokens + min(t0 + k, int64_t(n - 1))), rows);
 #pragma unroll
   for (int k = 0; k < kLookupRows; ++k)
     x[k] = load_row<E, false>(table + int64_t(row[k] < rows ? row[k] : 0) * dim, s, dim);
@@ -202,59 +196,67 @@ __global__ __launch_bounds__(256) void embedding_kernel(const void* __restrict__
 // --------------------------------------------------------------------- sort
 
 // Few tokens: a token's place is the number of tokens before it, those of lower
-// rows and those of its own row at lower positions: n^2 comparisons, two
-// instructions for each 64 of them. A block takes 32 tokens, each in both halves
-// of a wave, and its 32 half waves take a part of the tokens to compare with
-// each, from LDS.
-constexpr int kRankThreads = 1024, kRankParts = kRankThreads / 32;
+// rows and those of its own row at lower positions: n^2 comparisons. Row numbers
+// are exact in fp32, where a comparison and its count are two instructions that
+// need no wait between them: the difference clamped to [0, 1], and the sum. A
+// block takes 32 tokens, two in each of 16 lanes; its 64 such groups take a part
+// of the tokens to compare with each, from LDS.
+constexpr int kRankThreads = 1024, kRankParts = kRankThreads / 16, kRankEach = 32;
+static_assert(ZERO_LAYER_ROWS < 1 << 24, "rows and counts are exact in fp32");
 
-__global__ __launch_bounds__(kRankThreads) void order_rank_kernel(const void* __restrict__ tokens, int wide, int n,
-                                                                  int rows, int32_t* __restrict__ head,
+template <typename I>
+__global__ __launch_bounds__(kRankThreads) void order_rank_kernel(const I* __restrict__ tokens, int n, int rows,
                                                                   int32_t* __restrict__ row, int32_t* __restrict__ pos) {
-  __shared__ alignas(16) int32_t key[zero::kRankTokens + 4 * kRankParts];
-  __shared__ int32_t part[kRankParts][32];
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  // a half wave's part: whole fours of tokens
+  __shared__ alignas(16) float key[zero::kRankTokens + 4 * kRankParts];
+  __shared__ float part[kRankThreads / 64][kRankEach];
+  const int t = threadIdx.x, lane = t & 63;
+  // a group's part: whole fours of tokens
   const int each = ((n + kRankParts - 1) / kRankParts + 3) / 4 * 4;
-  for (int k = t; k < each * kRankParts; k += kRankThreads) key[k] = k < n ? table_row(tokens, wide, k, rows) : 0x7FFFFFFF;
+  constexpr int kLoads = int(zero::kRankTokens) / kRankThreads;
+  I token[kLoads];
+#pragma unroll
+  for (int k = 0; k < kLoads; ++k)       // not guarded one by one: all are on their way at once
+    if (k * kRankThreads < n) token[k] = tokens[min(k * kRankThreads + t, n - 1)];
+#pragma unroll
+  for (int k = 0; k < kLoads; ++k) {
+    const int i = k * kRankThreads + t;
+    if (i < each * kRankParts) key[i] = i < n ? float(table_row(token[k], rows)) : 0x1p30f;
+  }
   __syncthreads();
-  const int i0 = int(blockIdx.x) * 32, i = i0 + (lane & 31), half = t >> 5;
-  const int mine = i < n ? key[i] : 0;
-  const int j0 = half * each, j1 = j0 + each;
+  const int i0 = int(blockIdx.x) * kRankEach;
+  const int i[2] = {i0 + (t & 15), i0 + 16 + (t & 15)};
+  const float mine[2] = {i[0] < n ? key[i[0]] : 0.f, i[1] < n ? key[i[1]] : 0.f};
+  const int j0 = (t >> 4) * each, j1 = j0 + each;
   // before the block's tokens an equal row counts, behind them it does not
-  const int before = min(max(i0, j0), j1), behind = max(min(i0 + 32, j1), before);
-  int place = 0;
-  const auto count = [&](int from, int to, int limit) {
+  const int before = min(max(i0, j0), j1), behind = max(min(i0 + kRankEach, j1), before);
+  float place[2] = {0.f, 0.f};
+  const auto count = [&](int from, int to, auto limit) {       // limit: of token h against the one at j
 #pragma unroll 4
     for (int j = from; j < to; j += 4) {
-      const int4 k = *reinterpret_cast<const int4*>(&key[j]);
-      place += (k.x < limit) + (k.y < limit) + (k.z < limit) + (k.w < limit);
+      const f32x4 k = *reinterpret_cast<const f32x4*>(&key[j]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) place[h] += __builtin_amdgcn_fmed3f(limit(h, j + e) - k[e], 0.f, 1.f);
     }
   };
-  count(j0, before, mine + 1);
-  for (int j = before; j < behind; ++j) place += (key[j] < mine || (key[j] == mine && j < i)) ? 1 : 0;
-  count(behind, j1, mine);
-  part[half][lane & 31] = place;
-  __syncthreads();
-  if (t < 32 && i < n) {
-    int at = 0;
+  const float after[2] = {mine[0] + 1.f, mine[1] + 1.f};
+  count(j0, before, [&](int h, int) { return after[h]; });
+  count(before, behind, [&](int h, int j) { return j < i[h] ? after[h] : mine[h]; });
+  count(behind, j1, [&](int h, int) { return mine[h]; });
 #pragma unroll
-    for (int k = 0; k < kRankParts; ++k) at += part[k][t];
-    row[at] = mine;
-    pos[at] = i;
+  for (int h = 0; h < 2; ++h) {
+    place[h] += __shfl_xor(place[h], 16, 64);
+    place[h] += __shfl_xor(place[h], 32, 64);
+    if (lane < 16) part[t >> 6][h * 16 + lane] = place[h];
   }
-  if (blockIdx.x == 0) {       // how many lie in the table
-    int live = 0;
-    for (int k = t; k < n; k += kRankThreads) live += key[k] < rows ? 1 : 0;
-    for (int off = 32; off >= 1; off >>= 1) live += __shfl_xor(live, off, 64);
-    __syncthreads();
-    if (lane == 0) part[0][wave] = live;
-    __syncthreads();
-    if (t == 0) {
-      int sum = 0;
-      for (int k = 0; k < kRankThreads / 64; ++k) sum += part[0][k];
-      *head = sum;
-    }
+  __syncthreads();
+  if (t < kRankEach && i0 + t < n) {
+    float at = 0.f;
+#pragma unroll
+    for (int k = 0; k < kRankThreads / 64; ++k) at += part[k][t];
+    row[int(at)] = int(key[i0 + t]);
+    pos[int(at)] = i0 + t;
   }
 }
 
@@ -263,40 +265,34 @@ __global__ __launch_bounds__(kRankThreads) void order_rank_kernel(const void* __
 // digits of every block's 2048 tokens, then places every token behind those of
 // lower digits, those of earlier blocks and those before it in its block.
 struct SortArgs {
-  const void* tokens;      // of the first pass; later ones read row_in and pos_in
-  int32_t wide, n, rows, shift, bits, blocks;
-  const int32_t *row_in, *pos_in;
+  const void* in;          // tokens in the first pass, rows in later ones
+  const int32_t* pos_in;   // of later ones
+  int32_t n, rows, shift, bits, blocks;
   int32_t *row_out, *pos_out;
-  int32_t *digits, *live, *head;
+  int32_t* digits;
 };
 
-template <bool FIRST>
+template <typename I>
 __global__ __launch_bounds__(kSortThreads) void order_count_kernel(SortArgs a) {
   __shared__ int32_t count[kSortDigits];
-  const int t = threadIdx.x;
+  const int t = threadIdx.x, first = int(blockIdx.x) * kSortBlock;
+  const I* in = static_cast<const I*>(a.in);
+  I x[kSortItems];
+#pragma unroll
+  for (int k = 0; k < kSortItems; ++k) x[k] = in[min(first + k * kSortThreads + t, a.n - 1)];
   for (int k = t; k < kSortDigits; k += kSortThreads) count[k] = 0;
   __syncthreads();
-  int live = 0;
 #pragma unroll
   for (int k = 0; k < kSortItems; ++k) {
-    const int i = int(blockIdx.x) * kSortBlock + k * kSortThreads + t;
-    if (i >= a.n) break;
-    const int r = FIRST ? table_row(a.tokens, a.wide, i, a.rows) : a.row_in[i];
+    if (first + k * kSortThreads + t >= a.n) continue;
+    const int r = table_row(x[k], a.rows);
     atomicAdd(&count[(r >> a.shift) & ((1 << a.bits) - 1)], 1);
-    live += r < a.rows ? 1 : 0;
   }
   __syncthreads();
-  for (int k = t; k < (1 << a.bits); k += kSortThreads) a.digits[int64_t(blockIdx.x) * kSortDigits + k] = count[k];
-  if (FIRST) {
-    __shared__ int32_t sum[kSortThreads / 64];
-    for (int off = 32; off >= 1; off >>= 1) live += __shfl_xor(live, off, 64);
-    if ((t & 63) == 0) sum[t >> 6] = live;
-    __syncthreads();
-    if (t == 0) a.live[blockIdx.x] = sum[0] + sum[1] + sum[2] + sum[3];
-  }
+  for (int k = t; k < kSortDigits; k += kSortThreads) a.digits[int64_t(blockIdx.x) * kSortDigits + k] = count[k];
 }
 
-template <bool FIRST, bool LAST>
+template <typename I, bool FIRST>
 __global__ __launch_bounds__(kSortThreads) void order_scatter_kernel(SortArgs a) {
   constexpr int kWaves = kSortThreads / 64;
   __shared__ int32_t base[kSortDigits];             // where the block's tokens of a digit begin
@@ -306,38 +302,43 @@ __global__ __launch_bounds__(kSortThreads) void order_scatter_kernel(SortArgs a)
   const int n_digits = 1 << a.bits;
   // a wave's tokens are consecutive: 64 at a time, each one's rank among those of its digit
   const int first = int(blockIdx.x) * kSortBlock + wave * 64 * kSortItems;
+  const I* in = static_cast<const I*>(a.in);
+  I x[kSortItems];
   int row[kSortItems], pos[kSortItems], rank[kSortItems];
 #pragma unroll
   for (int k = 0; k < kSortItems; ++k) {
-    const int i = first + k * 64 + lane;
-    row[k] = i >= a.n ? -1 : FIRST ? table_row(a.tokens, a.wide, i, a.rows) : a.row_in[i];
-    pos[k] = i >= a.n ? 0 : FIRST ? i : a.pos_in[i];
+    const int i = min(first + k * 64 + lane, a.n - 1);
+    x[k] = in[i];
+    pos[k] = FIRST ? i : a.pos_in[i];
   }
-  for (int k = t; k < kWaves * kSortDigits; k += kSortThreads) (&seen[0][0])[k] = 0;
-  // two digits a thread: all blocks' tokens of lower digits, and the earlier blocks' of its own
-  int total[2] = {0, 0}, before[2] = {0, 0};
-#pragma unroll 8
-  for (int b = 0; b < a.blocks; ++b) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int d = 2 * t + k;
-      const int c = d < n_digits ? a.digits[int64_t(b) * kSortDigits + d] : 0;
-      total[k] += c;
-      before[k] += b < int(blockIdx.x) ? c : 0;
+  for (int k = 0; k < kSortItems; ++k) row[k] = first + k * 64 + lane < a.n ? table_row(x[k], a.rows) : -1;
+  for (int k = t; k < kWaves * kSortDigits; k += kSortThreads) (&seen[0][0])[k] = 0;
+  // a digit a thread: all blocks' tokens of lower digits, and the earlier blocks' of its own
+  static_assert(kSortThreads == kSortDigits, "a digit a thread");
+  int total = 0, before = 0;
+  constexpr int kAtOnce = 16;
+  for (int b0 = 0; b0 < a.blocks; b0 += kAtOnce) {
+    int c[kAtOnce];
+#pragma unroll
+    for (int b = 0; b < kAtOnce; ++b) c[b] = a.digits[int64_t(min(b0 + b, a.blocks - 1)) * kSortDigits + t];
+#pragma unroll
+    for (int b = 0; b < kAtOnce; ++b) {
+      // by selection: a branch would put each load behind it
+      total += c[b] & (b0 + b < a.blocks ? -1 : 0);
+      before += c[b] & (b0 + b < int(blockIdx.x) ? -1 : 0);
     }
   }
-  int up = total[0] + total[1];
-  const int own = up;
+  int up = total;
   for (int off = 1; off < 64; off <<= 1) {
     const int x = __shfl_up(up, off, 64);
     if (lane >= off) up += x;
   }
   if (lane == 63) wave_sum[wave] = up;
   __syncthreads();
-  int lower = up - own;
+  int lower = up - total;
   for (int w = 0; w < wave; ++w) lower += wave_sum[w];
-  base[2 * t] = lower + before[0];
-  base[2 * t + 1] = lower + total[0] + before[1];
+  base[t] = lower + before;
 #pragma unroll
   for (int k = 0; k < kSortItems; ++k) {
     const bool there = row[k] >= 0;
@@ -374,30 +375,28 @@ __global__ __launch_bounds__(kSortThreads) void order_scatter_kernel(SortArgs a)
     a.row_out[at] = row[k];
     a.pos_out[at] = pos[k];
   }
-  if (LAST && blockIdx.x == 0 && wave == 0) {
-    int live = 0;
-    for (int b = lane; b < a.blocks; b += 64) live += a.live[b];
-    for (int off = 32; off >= 1; off >>= 1) live += __shfl_xor(live, off, 64);
-    if (lane == 0) *a.head = live;
-  }
 }
 
 // ---------------------------------------------------- the table's gradient
 
 struct EmbeddingGradArgs {
-  const int32_t *head, *row, *pos;
+  const int32_t *row, *pos;  // the rows of tokens outside the table lie past row_hi
   const void* d_out;
   void* grad;
   float* ws;                 // [pieces][2][dim4]: sums of a run's middle or end, and of its beginning
   int64_t stride, first, count;
   float scale;
-  int32_t dim, dim4, tiles, pieces, piece;
+  int32_t n, dim, dim4, tiles, pieces, piece;
   int32_t row_lo, row_hi;    // rows that the part touches
-  int32_t sum_blocks, fill_rows, accumulate;
+  int32_t sum_blocks, accumulate;
 };
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef i32x8 i32x8_any __attribute__((aligned(4)));
+
+__device__ __forceinline__ i32x8 load8(const int32_t* p) {
+  return *(const __attribute__((address_space(4))) i32x8_any*)p;
+}
 
 // The elements of row r that are the lane's and in the part: those of `s`, cut
 // where the part begins or ends inside the row.
@@ -438,20 +437,21 @@ __device__ __forceinline__ void write_sum(const EmbeddingGradArgs& a, int r, con
   write_grad<E, G>(a, r, s, narrow<E, G>(v));
 }
 
-// The first of the sorted rows [from, live) that is at or above r, 64 compared at
-// a time: their spacing goes down by 64 each round.
-__device__ __forceinline__ int first_at(const int32_t* row, int from, int live, int r) {
+// Whether r is among the n sorted rows: 64 compared at a time, their spacing
+// divided by 64 each round.
+__device__ __forceinline__ bool has_token(const int32_t* row, int n, int r) {
   const int lane = threadIdx.x & 63;
-  int lo = from, n = live - from;      // the answer is in [lo, lo + n]
+  int lo = 0;                          // the first row at or above r, if there is one, is in [lo, lo + n)
   while (n > 0) {
-    const int step = (n + 63) >> 6, i = lo + min((lane + 1) * step, n) - 1;
-    const int below = __popcll(__ballot(row[i] < r));       // of the lanes' last rows: so many steps lie below
-    if (below == 64) return lo + n;
+    const int step = (n + 63) >> 6;
+    const int last = row[lo + min((lane + 1) * step, n) - 1];      // of the lane's rows
+    const int below = __popcll(__ballot(last < r));                // so many lanes' rows lie below r
+    if (below == 64) return false;
+    if (step == 1) return __builtin_amdgcn_readlane(last, below) == r;
     lo = __builtin_amdgcn_readfirstlane(lo + below * step);
-    if (step == 1) return lo;
-    n = __builtin_amdgcn_readfirstlane(min(step, live - lo));
+    n = __builtin_amdgcn_readfirstlane(min(step, n - below * step));
   }
-  return lo;
+  return false;
 }
 
 constexpr int kBatch = 8;      // rows that a wave loads before it adds them
@@ -459,49 +459,36 @@ constexpr int kBatch = 8;      // rows that a wave loads before it adds them
 template <typename T, typename G, int E>
 __global__ __launch_bounds__(256) void embedding_grad_kernel(const EmbeddingGradArgs a) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int live = uniform_load(a.head);
-  if (int(blockIdx.x) >= a.sum_blocks) {      // zeros, for the rows without a token
-    const int r0 = a.row_lo + ((int(blockIdx.x) - a.sum_blocks) * 4 + wave) * a.fill_rows;
-    const int r1 = min(r0 + a.fill_rows, a.row_hi);
-    if (r0 >= r1) return;
-    const int from = first_at(a.row, 0, live, r0), to = first_at(a.row, from, live, r1);
-    // a lane a row: is it among the sorted ones between
-    int lo = from, hi = to;
-    const int mine = r0 + lane;
-    while (__ballot(lo < hi)) {
-      const int mid = (lo + hi) >> 1;
-      if (lo < hi) {
-        if (a.row[mid] < mine) lo = mid + 1;
-        else hi = mid;
-      }
-    }
-    const bool absent = lo >= to || a.row[lo < to ? lo : 0] != mine;
-    const uint64_t rows = __ballot(absent && mine < r1);
-    for (int k = 0; k < r1 - r0; ++k)
-      if (rows >> k & 1)
-        for (int c = 0; c < a.tiles; ++c) write_grad<E, G>(a, r0 + k, span_of<E>(c * 64 + lane, a.dim), Words<E, G>{});
+  if (int(blockIdx.x) >= a.sum_blocks) {
+    // zeros for a row without a token, a wave a row (16 rows a wave: the whole gradient of 50257 x 2944 in
+    // 75 us instead of 61)
+    const int r = a.row_lo + (int(blockIdx.x) - a.sum_blocks) * 4 + wave;
+    if (r >= a.row_hi || has_token(a.row, a.n, r)) return;
+    for (int k = 0; k < a.tiles; ++k) write_grad<E, G>(a, r, span_of<E>(k * 64 + lane, a.dim), Words<E, G>{});
     return;
   }
   const uint32_t w = blockIdx.x * 4 + wave;
   const int piece = int(w / uint32_t(a.tiles));
   if (piece >= a.pieces) return;
   const Span s = span_of<E>(int(w % uint32_t(a.tiles)) * 64 + lane, a.dim);
-  const int i0 = piece * a.piece, i1 = min(i0 + a.piece, live);
-  if (i0 >= i1) return;
-  const int r_first = uniform_load(a.row + i0), r_last = uniform_load(a.row + i1 - 1);
-  if (r_last < a.row_lo || r_first >= a.row_hi) return;
-  bool head = i0 > 0 && uniform_load(a.row + max(i0 - 1, 0)) == r_first;     // the run at hand began in an earlier piece
+  const int i0 = piece * a.piece, i1 = min(i0 + a.piece, a.n);
+  // rows and positions by eights: the arrays go on that far behind their last entry
+  i32x8 r8 = load8(a.row + i0), p8 = load8(a.pos + i0);
+  const int prior = uniform_load(a.row + max(i0 - 1, 0)), r_last = uniform_load(a.row + i1 - 1);
+  if (r_last < a.row_lo || r8[0] >= a.row_hi) return;
+  bool head = i0 > 0 && prior == r8[0];      // the run at hand began in an earlier piece
   float sum[E] = {};
   for (int i = i0; i < i1; i += kBatch) {
-    // rows and positions by eights: the arrays go on that far behind their last entry
-    const i32x8 r8 = *(const __attribute__((address_space(4))) i32x8_any*)(a.row + i);
-    const i32x8 p8 = *(const __attribute__((address_space(4))) i32x8_any*)(a.pos + i);
+    if (i > i0) {
+      r8 = load8(a.row + i);
+      p8 = load8(a.pos + i);
+    }
     const int r9 = uniform_load(a.row + i + kBatch);
     int r[kBatch + 1];
     Words<E, T> x[kBatch];
     Words<E, G> old[kBatch];
 #pragma unroll
-    for (int k = 0; k <= kBatch; ++k) r[k] = i + k >= live ? -1 : k < kBatch ? r8[k % kBatch] : r9;
+    for (int k = 0; k <= kBatch; ++k) r[k] = i + k >= a.n ? -1 : k < kBatch ? r8[k % kBatch] : r9;
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const bool mine = i + k < i1 && r[k] >= a.row_lo && r[k] < a.row_hi;
@@ -541,17 +528,17 @@ __global__ __launch_bounds__(256) void embedding_join_kernel(const EmbeddingGrad
   const int piece = int(w / uint32_t(a.tiles));
   if (piece >= a.pieces) return;
   const Span s = span_of<E>(int(w % uint32_t(a.tiles)) * 64 + lane, a.dim);
-  const int live = uniform_load(a.head);
   const int i0 = piece * a.piece, i1 = i0 + a.piece;
-  if (i1 >= live) return;
-  const int r = uniform_load(a.row + i1);
-  if (uniform_load(a.row + i1 - 1) != r || r < a.row_lo || r >= a.row_hi) return;
-  if (i0 > 0 && uniform_load(a.row + i0) == r && uniform_load(a.row + max(i0 - 1, 0)) == r) return;    // began earlier
+  if (i1 >= a.n) return;
+  const int r = uniform_load(a.row + i1), end = uniform_load(a.row + i1 - 1), begin = uniform_load(a.row + i0),
+            prior = uniform_load(a.row + max(i0 - 1, 0));
+  if (end != r || r < a.row_lo || r >= a.row_hi) return;
+  if (i0 > 0 && begin == r && prior == r) return;      // began earlier
   // the pieces whose first token goes on with the run: 64 compared at a time
   int last = piece;
   for (;;) {
     const int64_t i = int64_t(last + 1 + lane) * a.piece;
-    const uint64_t on = __ballot(i < live && a.row[i < live ? i : 0] == r);
+    const uint64_t on = __ballot(i < a.n && a.row[i < a.n ? i : 0] == r);
     const int more = on == ~uint64_t(0) ? 64 : __builtin_ctzll(~on);
     last += more;
     if (more < 64) break;
@@ -796,13 +783,13 @@ __global__ __launch_bounds__(kLongThreads) void norm_long_kernel(const zero_norm
 // A block takes every gridDim.x-th group of rows, TPR threads a row, and keeps the
 // sums of d_weight and d_bias over its rows in registers; the groups' sums meet in
 // LDS and go to the workspace, which norm_grad_join_kernel adds up.
-constexpr int kGradThreads = 1024;
+constexpr int grad_threads(int per_row) { return per_row >= 512 ? per_row : 512 / per_row * per_row; }
 
 template <typename T, typename W, int TPR, int V>
-__global__ __launch_bounds__(kGradThreads) void norm_grad_kernel(const zero_norm_grad_args a, float* ws, int dim4) {
+__global__ __launch_bounds__(grad_threads(TPR)) void norm_grad_kernel(const zero_norm_grad_args a, float* ws, int dim4) {
   constexpr int E = 16 / int(sizeof(T));
-  constexpr int kRows = kGradThreads / TPR;
-  __shared__ float lds[kGradThreads * V * E];      // row sums, then the groups' column sums
+  constexpr int kThreads = grad_threads(TPR), kRows = kThreads / TPR;
+  __shared__ float lds[kThreads * V * E];      // row sums, then the groups' column sums
   const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
   const int dim = int(a.dim);
   const bool skip = a.d_total != nullptr;
@@ -816,16 +803,14 @@ __global__ __launch_bounds__(kGradThreads) void norm_grad_kernel(const zero_norm
 #pragma unroll
     for (int e = 0; e < E; ++e) sum_w[k][e] = sum_b[k][e] = 0.f;
   }
-  // the next rows are read before this one's sums
   struct Row {
     Words<E, T> dy[V], x[V], total[V];
     float mean, rstd;
   };
-  const auto read = [&](int64_t row0) {
+  const auto read = [&](int64_t row0, Row& r) {
     const int64_t row = row0 + group < a.n ? row0 + group : row0;
     const T* dy = static_cast<const T*>(a.d_y) + row * a.d_y_stride;
     const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
-    Row r;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       r.dy[k] = load_row<E>(dy, s[k], dim);
@@ -838,70 +823,76 @@ __global__ __launch_bounds__(kGradThreads) void norm_grad_kernel(const zero_norm
     }
     r.mean = a.rms ? 0.f : a.mean[row];
     r.rstd = a.rstd[row];
-    return r;
   };
   int turn = 0;
   const int64_t step = int64_t(gridDim.x) * kRows;
-  Row now, next;
-  if (int64_t(blockIdx.x) * kRows < a.n) next = read(int64_t(blockIdx.x) * kRows);
-  for (int64_t row0 = int64_t(blockIdx.x) * kRows; row0 < a.n; row0 += step) {
+  const auto pass = [&](int64_t row0, Row& now) {
     const bool there = row0 + group < a.n;
     const int64_t row = row0 + group;
-    now = next;
-    if (row0 + step < a.n) next = read(row0 + step);
     const float mean = now.mean, rstd = now.rstd;
+    float g[V][E], xh[V][E];
     float c[2] = {0.f, 0.f};
-    if (there) {
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        float g[E], xh[E], w[E];
-        widen<E, T>(now.dy[k], g);
-        widen<E, T>(now.x[k], xh);
-        widen<E, W>(w_raw[k], w);
+    for (int k = 0; k < V; ++k) {
+      float w[E];
+      widen<E, T>(now.dy[k], g[k]);
+      widen<E, T>(now.x[k], xh[k]);
+      widen<E, W>(w_raw[k], w);
+      if (kRows == 1 || there) {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          xh[e] = (xh[e] - mean) * rstd;
-          sum_w[k][e] = fmaf(g[e], xh[e], sum_w[k][e]);
-          sum_b[k][e] += g[e];
-          g[e] *= w[e];
+          xh[k][e] = (xh[k][e] - mean) * rstd;
+          sum_w[k][e] = fmaf(g[k][e], xh[k][e], sum_w[k][e]);
+          sum_b[k][e] += g[k][e];
+          g[k][e] *= w[e];
         }
-        only_own<E>(s[k], g);
-        only_own<E>(s[k], xh);
+      }
+      if (s[k].lo > 0) {       // the neighbour's: computed, not summed
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (e >= s[k].lo) {
+            c[0] += g[k][e];
+            c[1] = fmaf(g[k][e], xh[k][e], c[1]);
+          }
+      } else {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          c[0] += g[e];
-          c[1] = fmaf(g[e], xh[e], c[1]);
+          c[0] += g[k][e];
+          c[1] = fmaf(g[k][e], xh[k][e], c[1]);
         }
       }
     }
-    if (a.d_x == nullptr) continue;
+    if (a.d_x == nullptr) return;
     row_sum<TPR, 2>(c, lds, turn);
     turn ^= 1;
-    if (!there) continue;
-    // widened again: kept over the sum as fp32, the three rows do not fit the registers
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      opaque(now.dy[k]);
-      opaque(now.x[k]);
-      opaque(w_raw[k]);
-    }
+    if (!there) return;
     const float c0 = a.rms ? 0.f : c[0] / float(dim), c1 = c[1] / float(dim);
     T* dx = static_cast<T*>(a.d_x) + row * a.d_x_stride;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      float g[E], xh[E], w[E], m[E];
-      widen<E, T>(now.dy[k], g);
-      widen<E, T>(now.x[k], xh);
-      widen<E, W>(w_raw[k], w);
+      float m[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) m[e] = 0.f;
       if (skip) widen<E, T>(now.total[k], m);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        xh[e] = (xh[e] - mean) * rstd;
-        g[e] = fmaf(fmaf(-xh[e], c1, g[e] * w[e] - c0), rstd, m[e]);
-      }
-      store_row<E>(dx, s[k], narrow<E, T>(g));
+      for (int e = 0; e < E; ++e) g[k][e] = fmaf(fmaf(-xh[k][e], c1, g[k][e] - c0), rstd, m[e]);
+      store_row<E>(dx, s[k], narrow<E, T>(g[k]));
+    }
+  };
+  // the next rows are on their way while these are summed
+  constexpr int kAhead = V * E > 8 ? 0 : 1;
+  Row ring[kAhead + 1];
+  int64_t row0 = int64_t(blockIdx.x) * kRows;
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k)
+    if (row0 + k * step < a.n) read(row0 + k * step, ring[k]);
+  while (row0 < a.n) {
+#pragma unroll
+    for (int k = 0; k <= kAhead; ++k) {
+      if (row0 >= a.n) break;
+      if (row0 + kAhead * step < a.n) read(row0 + kAhead * step, ring[(k + kAhead) % (kAhead + 1)]);
+      pass(row0, ring[k]);
+      row0 += step;
     }
   }
   if (a.d_weight == nullptr && a.d_bias == nullptr) return;
@@ -923,7 +914,7 @@ __global__ __launch_bounds__(kGradThreads) void norm_grad_kernel(const zero_norm
         for (int e = 0; e < E; ++e)
           lds[(group * V * E + k * E + e) * TPR + t] = which ? sum_b[k][e] : sum_w[k][e];
       __syncthreads();
-      for (int j = threadIdx.x; j < V * E * TPR; j += kGradThreads) {
+      for (int j = threadIdx.x; j < V * E * TPR; j += kThreads) {
         float x = 0.f;
 #pragma unroll
         for (int g = 0; g < kRows; ++g) x += lds[g * V * E * TPR + j];
@@ -1026,7 +1017,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void norm_grad_join_kernel(const f
   const int col = int(blockIdx.x) * 64 + lane;
   float s = 0.f;
   if (col < dim)
-#pragma unroll 8
+#pragma unroll 16
     for (int b = wave; b < blocks; b += kJoinWaves) s += ws[(int64_t(b) * 2 + blockIdx.y) * dim4 + col];
   part[wave][lane] = s;
   __syncthreads();
@@ -1063,7 +1054,7 @@ NormShape norm_shape(int64_t vectors) {
 // The same for the gradient, whose two sums a column limit a thread to 8 elements, 16 for the longest rows.
 NormShape norm_grad_shape(int64_t dim, int per) {
   const int64_t vectors = (dim + per - 1) / per;
-  static const int threads[] = {64, 128, 256, 512, 1024};
+  static const int threads[] = {64, 128, 192, 256, 384, 512, 768, 1024};
   if (vectors <= 16) return {16, 1};
   for (int t : threads)
     if (int64_t(t) * (8 / per) >= vectors) return {t, 8 / per};
@@ -1076,8 +1067,9 @@ namespace zero {
 
 int64_t norm_grad_blocks(int64_t n, int64_t dim) {
   const NormShape s = norm_grad_shape(dim, 8);
-  const int64_t rows = s.threads == 0 ? 16 : kGradThreads / s.threads;
-  return std::max<int64_t>(1, std::min<int64_t>((n + rows - 1) / rows, 512));
+  const int64_t rows = s.threads == 0 ? 16 : grad_threads(s.threads) / s.threads;
+  const int64_t groups = (n + rows - 1) / rows;
+  return std::max<int64_t>(1, std::min<int64_t>(groups, std::min<int64_t>(512, std::max<int64_t>(256, groups / 2))));
 }
 
 int launch_embedding(const void* tokens, bool wide, int64_t n, const void* table, int32_t table_type, int64_t rows,
@@ -1089,9 +1081,13 @@ int launch_embedding(const void* tokens, bool wide, int64_t n, const void* table
     constexpr int E = sizeof(T) == 2 && sizeof(O) == 2 ? 8 : 4;
     const int64_t tiles = (dim + 64 * E - 1) / (64 * E);
     const int64_t waves = (n + kLookupRows - 1) / kLookupRows * tiles;
-    embedding_kernel<T, O, E><<<dim3(uint32_t((waves + 3) / 4)), 256, 0, stream>>>(
-        tokens, wide, int(n), static_cast<const T*>(table), int(rows), int(dim), int(tiles), scale,
-        static_cast<O*>(out), out_stride);
+    const auto run = [&](auto iv) {
+      using I = decltype(iv);
+      embedding_kernel<I, T, O, E><<<dim3(uint32_t((waves + 3) / 4)), 256, 0, stream>>>(
+          static_cast<const I*>(tokens), int(n), static_cast<const T*>(table), int(rows), int(dim), int(tiles), scale,
+          static_cast<O*>(out), out_stride);
+    };
+    wide ? run(int64_t()) : run(int32_t());
   };
   by_types(table_type, out_type, go);
   return launched(who);
@@ -1101,37 +1097,40 @@ int launch_token_order(const void* tokens, bool wide, int64_t n, int64_t rows, i
                        const char* who) {
   const Order o(n);
   if (n <= kRankTokens) {
-    order_rank_kernel<<<dim3(uint32_t(std::max<int64_t>(1, (n + 31) / 32))), kRankThreads, 0, stream>>>(
-        tokens, wide, int(n), int(rows), order, order + o.row, order + o.pos);
+    const auto run = [&](auto iv) {
+      using I = decltype(iv);
+      order_rank_kernel<I><<<dim3(uint32_t((n + kRankEach - 1) / kRankEach)), kRankThreads, 0, stream>>>(
+          static_cast<const I*>(tokens), int(n), int(rows), order + o.row, order + o.pos);
+    };
+    if (n > 0) wide ? run(int64_t()) : run(int32_t());
     return launched(who);
   }
   const int bits = row_bits(rows), passes = (bits + kSortBits - 1) / kSortBits, each = (bits + passes - 1) / passes;
   SortArgs a{};
-  a.tokens = tokens;
-  a.wide = wide;
   a.n = int32_t(n);
   a.rows = int32_t(rows);
   a.blocks = int32_t(o.blocks);
   a.digits = order + o.digits;
-  a.live = order + o.live;
-  a.head = order;
   int32_t *row[2] = {order + o.row, order + o.row2}, *pos[2] = {order + o.pos, order + o.pos2};
   for (int p = 0; p < passes; ++p) {
     const int to = (passes - 1 - p) & 1;       // the last pass ends in the order's own arrays
+    const bool first = p == 0;
     a.shift = p * each;
     a.bits = std::min(each, bits - a.shift);
-    a.row_in = row[to ^ 1];
+    a.in = first ? tokens : row[to ^ 1];
     a.pos_in = pos[to ^ 1];
     a.row_out = row[to];
     a.pos_out = pos[to];
-    const dim3 grid{uint32_t(o.blocks)};
-    const bool first = p == 0, last = p == passes - 1;
-    if (first) order_count_kernel<true><<<grid, kSortThreads, 0, stream>>>(a);
-    else order_count_kernel<false><<<grid, kSortThreads, 0, stream>>>(a);
-    if (first && last) order_scatter_kernel<true, true><<<grid, kSortThreads, 0, stream>>>(a);
-    else if (first) order_scatter_kernel<true, false><<<grid, kSortThreads, 0, stream>>>(a);
-    else if (last) order_scatter_kernel<false, true><<<grid, kSortThreads, 0, stream>>>(a);
-    else order_scatter_kernel<false, false><<<grid, kSortThreads, 0, stream>>>(a);
+    const auto run = [&](auto iv, auto fv) {
+      using I = decltype(iv);
+      constexpr bool FIRST = decltype(fv)::value;
+      const dim3 grid{uint32_t(o.blocks)};
+      order_count_kernel<I><<<grid, kSortThreads, 0, stream>>>(a);
+      order_scatter_kernel<I, FIRST><<<grid, kSortThreads, 0, stream>>>(a);
+    };
+    if (!first) run(int32_t(), std::false_type());
+    else if (wide) run(int64_t(), std::true_type());
+    else run(int32_t(), std::true_type());
   }
   return launched(who);
 }
@@ -1142,7 +1141,6 @@ int launch_embedding_grad(const int32_t* order, int64_t n, int64_t rows, int64_t
                           const char* who) {
   const Order o(n);
   EmbeddingGradArgs a{};
-  a.head = order;
   a.row = order + o.row;
   a.pos = order + o.pos;
   a.d_out = d_out;
@@ -1152,6 +1150,7 @@ int launch_embedding_grad(const int32_t* order, int64_t n, int64_t rows, int64_t
   a.first = first;
   a.count = count;
   a.scale = scale;
+  a.n = int32_t(n);
   a.dim = int32_t(dim);
   a.dim4 = int32_t((dim + 3) / 4 * 4);
   a.piece = embedding_piece(n);
@@ -1166,8 +1165,7 @@ int launch_embedding_grad(const int32_t* order, int64_t n, int64_t rows, int64_t
     a.tiles = int32_t((dim + 64 * E - 1) / (64 * E));
     const int64_t sums = (int64_t(a.pieces) * a.tiles + 3) / 4;
     const int touched = a.row_hi - a.row_lo;
-    a.fill_rows = std::min(std::max(touched / 2048, 1), 16);
-    const int64_t fills = accumulate ? 0 : (touched + 4 * a.fill_rows - 1) / (4 * a.fill_rows);
+    const int64_t fills = accumulate ? 0 : (touched + 3) / 4;
     a.sum_blocks = int32_t(sums);
     if (sums + fills > 0)
       embedding_grad_kernel<T, G, E><<<dim3(uint32_t(sums + fills)), 256, 0, stream>>>(a);
@@ -1216,13 +1214,16 @@ int launch_norm_grad(const zero_norm_grad_args& a, float* ws, hipStream_t stream
     const auto spread = [&](auto threads, auto vectors) {
       constexpr int TPR = decltype(threads)::value, V = decltype(vectors)::value;
       if (s.threads != TPR || s.vectors != V) return;
-      norm_grad_kernel<T, W, TPR, V><<<dim3(uint32_t(blocks)), kGradThreads, 0, stream>>>(a, ws, dim4);
+      norm_grad_kernel<T, W, TPR, V><<<dim3(uint32_t(blocks)), grad_threads(TPR), 0, stream>>>(a, ws, dim4);
     };
     spread(Int<16>(), Int<1>());
     spread(Int<64>(), Int<8 / E>());
     spread(Int<128>(), Int<8 / E>());
+    spread(Int<192>(), Int<8 / E>());
     spread(Int<256>(), Int<8 / E>());
+    spread(Int<384>(), Int<8 / E>());
     spread(Int<512>(), Int<8 / E>());
+    spread(Int<768>(), Int<8 / E>());
     spread(Int<1024>(), Int<8 / E>());
     spread(Int<1024>(), Int<16 / E>());
     if (s.threads != 0) return;

@@ -18,29 +18,27 @@ inline int embedding_piece(int64_t n) { return n <= 4096 ? 8 : 32; }
 inline int64_t embedding_pieces(int64_t n) { return (n + embedding_piece(n) - 1) / embedding_piece(n); }
 
 // Tokens that one block of the sort takes, and the bits of one of its passes.
-constexpr int kSortThreads = 256, kSortItems = 8, kSortBlock = kSortThreads * kSortItems;
+constexpr int kSortThreads = 512, kSortItems = 4, kSortBlock = kSortThreads * kSortItems;
 constexpr int kSortBits = 9, kSortDigits = 1 << kSortBits;
 
 // Up to this many tokens are sorted by counting, in one launch.
-constexpr int64_t kRankTokens = 8192;
+constexpr int64_t kRankTokens = 12288;
 
-// The parts of an order, in 32-bit words from its start: head (word 0: how many
-// tokens lie in the table), the sorted tokens' rows and positions; then scratch of
-// the sort: rows and positions between two passes, and per block its tokens in
-// the table and its digits' counts.
+// The parts of an order, in 32-bit words from its start: the sorted tokens' rows,
+// `rows` for those outside the table, and positions; then scratch of the sort: rows
+// and positions between two passes, and per block its digits' counts.
 struct Order {
-  int64_t row, pos, row2, pos2, live, digits, words;
+  int64_t row, pos, row2, pos2, digits, words;
   int64_t blocks;
   Order(int64_t n) {
     auto up = [](int64_t k) { return (k + 7) / 8 * 8; };
     blocks = (n + kSortBlock - 1) / kSortBlock;
     const int64_t scratch = n > kRankTokens ? 1 : 0;
-    row = 8;
+    row = 0;
     pos = row + up(n) + 8;      // read by eights and one more
     row2 = pos + up(n) + 8;
     pos2 = row2 + scratch * up(n);
-    live = pos2 + scratch * up(n);
-    digits = live + scratch * up(blocks);
+    digits = pos2 + scratch * up(n);
     words = digits + scratch * blocks * kSortDigits;
   }
 };

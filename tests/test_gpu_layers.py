@@ -63,15 +63,15 @@ def order_of(tokens, rows):
 @pytest.mark.parametrize("kind", ["mixed", "same", "distinct", "none"])
 def test_token_order(n, rows, kind):
     """The gradient of one column of ones and of positions shows the order only as sums, so the
-    order's first parts are read here: the count, the rows and the positions."""
+    order's first parts are read here: the rows and the positions."""
     ids = torch.int32 if (n + rows) % 2 else torch.int64
     tokens = C.draw_tokens(n, rows, n + rows, kind, ids)
     order = order_of(tokens, rows).cpu().numpy()
     row, pos = O.token_order(tokens.cpu().numpy(), rows)
     up = (n + 7) // 8 * 8 + 8
-    assert order[0] == len(row)
-    assert order[8:8 + len(row)].tolist() == row
-    assert order[8 + up:8 + up + len(row)].tolist() == pos
+    assert order[:len(row)].tolist() == row
+    assert order[up:up + len(row)].tolist() == pos
+    assert (order[len(row):n] == rows).all()
 
 
 def test_token_order_of_a_wide_table():
@@ -82,8 +82,7 @@ def test_token_order_of_a_wide_table():
         order = order_of(t, rows).cpu().numpy()
         row, pos = O.token_order(t.cpu().numpy(), rows)
         up = (len(t) + 7) // 8 * 8 + 8
-        assert order[0] == len(row)
-        assert order[8:8 + len(row)].tolist() == row and order[8 + up:8 + up + len(row)].tolist() == pos
+        assert order[:len(row)].tolist() == row and order[up:up + len(row)].tolist() == pos
 
 
 # -------------------------------------------------------- table's gradient
