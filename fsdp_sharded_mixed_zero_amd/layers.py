@@ -67,16 +67,17 @@ def library():
     return _lib
 
 
-_torch = _C = _TYPES = _IDS = None
+_torch = _C = _TYPES = _IDS = _F32 = None
 
 
 def _load():
     """torch and the library, at the first call."""
-    global _torch, _C, _TYPES, _IDS
+    global _torch, _C, _TYPES, _IDS, _F32
     import torch
     library()
     _TYPES = {torch.bfloat16: ZERO_BF16, torch.float32: ZERO_F32}
     _IDS = {torch.int32: ZERO_I32, torch.int64: ZERO_I64}
+    _F32 = (torch.float32,)
     _C, _torch = torch._C, torch
 
 
@@ -88,8 +89,8 @@ def _sized(name, *sizes):
     return nbytes
 
 
-# The checks below cost a call 0.1 us each, of the 4 to 7 that it takes in all, so a tensor's
-# attributes are read once and what is wrong is found out after the fact.
+# The checks cost a call 0.5 us a tensor, of the 4 to 7 that it takes in all: each tensor's
+# attributes are read once, and what is wrong is found out only where something is.
 
 def _device():
     """The current device, where the library's launches go."""
@@ -101,70 +102,76 @@ def _device():
         return -1
 
 
-def _elsewhere(t, what, dev):
-    """The error of a tensor that is not on the current device."""
+def _refuse(t, what, dev, dtypes):
+    """The error of a tensor that is not on the current device or not of these types."""
     if not getattr(t, "is_cuda", False):
         raise TypeError(f"{what}: device memory expected, got {type(t).__name__}"
                         f"{' on ' + str(t.device) if hasattr(t, 'device') else ''}")
-    raise ValueError(f"{what} is on {t.device}, the current device is {dev}")
+    if t.get_device() != dev:
+        raise ValueError(f"{what} is on {t.device}, the current device is {dev}")
+    if dtypes is not None and t.dtype not in dtypes:
+        raise TypeError(f"{what}: {' or '.join(str(d) for d in dtypes)} expected, got {t.dtype}")
 
 
-def _on(t, dev):
+def _rows(t, what, dev, shape, dtypes):
+    """(address, stride) of an array of rows of this shape (a pair; None: any)."""
     try:
-        return t.get_device() == dev and dev >= 0
-    except AttributeError:
-        return False
-
-
-def _rows(t, what, dev, shape=None, dtype=None):
-    """(address, stride, shape) of an array of rows."""
-    if not _on(t, dev):
-        _elsewhere(t, what, dev)
-    size = t.shape
-    if len(size) != 2 or (shape is not None and size != shape):
-        raise ValueError(f"{what}: {'two dimensions' if shape is None else tuple(shape)} expected, got {tuple(size)}")
-    if t.dtype is not dtype and (dtype is not None or t.dtype not in _TYPES):
-        raise TypeError(f"{what}: {'bfloat16 or float32' if dtype is None else dtype} expected, got {t.dtype}")
-    step, one = t.stride()
-    if one != 1 and size[1] > 1:
-        raise ValueError(f"{what}: the elements of a row have to be consecutive")
-    return t.data_ptr(), step if size[0] > 1 else size[1], size
+        step, one = t.stride()
+        size = t.shape
+        if t.get_device() == dev >= 0 and t.dtype in dtypes and (shape is None or size == shape):
+            if one == 1 or size[1] <= 1:
+                return t.data_ptr(), step if size[0] > 1 else size[1]
+    except (AttributeError, ValueError, TypeError):      # no tensor, or not of two dimensions
+        pass
+    _refuse(t, what, dev, dtypes)
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{what}: {'two dimensions' if shape is None else tuple(shape)} expected, got {tuple(t.shape)}")
+    raise ValueError(f"{what}: the elements of a row have to be consecutive")
 
 
 def _flat(t, what, dev, count, dtypes):
-    """Address of an array without gaps of `count` elements (None: as many as it has)."""
-    if not _on(t, dev):
-        _elsewhere(t, what, dev)
-    if t.dtype not in dtypes:
-        raise TypeError(f"{what}: {' or '.join(str(d) for d in dtypes)} expected, got {t.dtype}")
-    if count is not None and t.numel() != count:
+    """Address of an array without gaps of `count` elements."""
+    try:
+        if t.get_device() == dev >= 0 and t.dtype in dtypes and t.numel() == count and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, what, dev, dtypes)
+    if t.numel() != count:
         raise ValueError(f"{what}: {t.numel()} elements, {count} expected")
-    if not t.is_contiguous():
-        raise ValueError(f"{what}: a contiguous tensor is expected")
-    return t.data_ptr()
+    raise ValueError(f"{what}: a contiguous tensor is expected")
 
 
 def _memory(t, what, dev):
     """(address, bytes) of an order or a workspace, of any type."""
-    if not _on(t, dev):
-        _elsewhere(t, what, dev)
-    if not t.is_contiguous():
-        raise ValueError(f"{what}: a contiguous tensor is expected")
-    return t.data_ptr(), t.nbytes
+    try:
+        if t.get_device() == dev >= 0 and t.is_contiguous():
+            return t.data_ptr(), t.nbytes
+    except AttributeError:
+        pass
+    _refuse(t, what, dev, None)
+    raise ValueError(f"{what}: a contiguous tensor is expected")
 
 
 def _stream(stream, dev):
     return _C._cuda_getCurrentRawStream(dev) if stream is None else zero._stream(stream)
 
 
+def _tokens(tokens, dev):
+    """(address, number) of the tokens."""
+    n = tokens.numel() if hasattr(tokens, "numel") else 0
+    return _flat(tokens, "tokens", dev, n, _IDS), n
+
+
 def zero_embedding(tokens, table, out, scale: float = 1.0, stream=None):
     """``out`` [number of tokens, dim] = scale * rows of ``table`` [rows, dim]."""
     dev = _device()
-    ids, n = _flat(tokens, "tokens", dev, None, _IDS), tokens.numel()
-    src, step, (rows, dim) = _rows(table, "table", dev)
+    ids, n = _tokens(tokens, dev)
+    src, step = _rows(table, "table", dev, None, _TYPES)
+    rows, dim = table.shape
     if step != dim:
         raise ValueError("table: rows without gaps are expected")
-    dst, stride, _ = _rows(out, "out", dev, (n, dim))
+    dst, stride = _rows(out, "out", dev, (n, dim), _TYPES)
     rc = _lib.zero_embedding(ids, _IDS[tokens.dtype], n, src, _TYPES[table.dtype], rows, dim, scale, dst,
                              _TYPES[out.dtype], stride, _stream(stream, dev))
     if rc:
@@ -178,9 +185,9 @@ def zero_token_order_bytes(n: int, rows: int) -> int:
 def zero_token_order(tokens, rows: int, order, stream=None):
     """``order``: device memory of at least zero_token_order_bytes bytes, of any type."""
     dev = _device()
-    ids = _flat(tokens, "tokens", dev, None, _IDS)
+    ids, n = _tokens(tokens, dev)
     p, nbytes = _memory(order, "order", dev)
-    rc = _lib.zero_token_order(ids, _IDS[tokens.dtype], tokens.numel(), rows, p, nbytes, _stream(stream, dev))
+    rc = _lib.zero_token_order(ids, _IDS[tokens.dtype], n, rows, p, nbytes, _stream(stream, dev))
     if rc:
         zero._check("zero_token_order", rc)
 
@@ -195,27 +202,30 @@ def zero_embedding_grad(order, rows: int, d_out, grad, workspace, scale: float =
     elements of the flat [rows, dim] gradient from ``first`` on, as many as it has
     (the whole table's by default)."""
     dev = _device()
-    src, stride, (n, dim) = _rows(d_out, "d_out", dev)
+    src, stride = _rows(d_out, "d_out", dev, None, _TYPES)
+    n, dim = d_out.shape
     p, order_bytes = _memory(order, "order", dev)
     need = _lib.zero_token_order_bytes(n, rows)
     if order_bytes < need:
         raise ValueError(f"order: {order_bytes} bytes given, the call reaches {need}")
     ws, ws_bytes = _memory(workspace, "workspace", dev)
-    dst = _flat(grad, "grad", dev, None, _TYPES)
+    count = grad.numel() if hasattr(grad, "numel") else 0
+    dst = _flat(grad, "grad", dev, count, _TYPES)
     rc = _lib.zero_embedding_grad(p, n, rows, dim, src, _TYPES[d_out.dtype], stride, scale, dst, _TYPES[grad.dtype],
-                                  first, grad.numel(), 1 if accumulate else 0, ws, ws_bytes, _stream(stream, dev))
+                                  first, count, 1 if accumulate else 0, ws, ws_bytes, _stream(stream, dev))
     if rc:
         zero._check("zero_embedding_grad", rc)
 
 
 def _vectors(dev, dim, a, a_name, b, b_name):
     """Addresses of two vectors, either of which may be missing, and the type that they share."""
-    if a is None and b is None:
-        return 0, 0, ZERO_F32
-    kind = (b if a is None else a).dtype
-    pa = 0 if a is None else _flat(a, a_name, dev, dim, _TYPES)
-    pb = 0 if b is None else _flat(b, b_name, dev, dim, _TYPES if a is None else (kind,))
-    return pa, pb, _TYPES[kind]
+    if a is None:
+        if b is None:
+            return 0, 0, ZERO_F32
+        return 0, _flat(b, b_name, dev, dim, _TYPES), _TYPES[b.dtype]
+    pa = _flat(a, a_name, dev, dim, _TYPES)
+    kind = a.dtype
+    return pa, 0 if b is None else _flat(b, b_name, dev, dim, (kind,)), _TYPES[kind]
 
 
 # zero_norm_args and zero_norm_grad_args as bytes: a third of the time of a ctypes structure
@@ -229,19 +239,19 @@ def zero_norm(x, y, mean=None, rstd=None, weight=None, bias=None, eps: float = 1
     ``residual``; ``mean`` and ``rstd`` [n], float32, for the backward pass.
     ``rms``: without the mean."""
     dev = _device()
-    px, sx, size = _rows(x, "x", dev)
-    kind, (n, dim) = x.dtype, size
-    py, sy, _ = _rows(y, "y", dev, size, kind)
+    px, sx = _rows(x, "x", dev, None, _TYPES)
+    size, kind = x.shape, x.dtype
+    (n, dim), kinds = size, (kind,)
+    py, sy = _rows(y, "y", dev, size, kinds)
     if (residual is None) != (total is None):
         raise ValueError("residual and total: both or neither")
     pr = pt = sr = st = 0
     if total is not None:
-        pr, sr, _ = _rows(residual, "residual", dev, size, kind)
-        pt, st, _ = _rows(total, "total", dev, size, kind)
+        pr, sr = _rows(residual, "residual", dev, size, kinds)
+        pt, st = _rows(total, "total", dev, size, kinds)
     pw, pb, w_type = _vectors(dev, dim, weight, "weight", bias, "bias")
-    f32 = (_torch.float32,)
-    pm = 0 if mean is None else _flat(mean, "mean", dev, n, f32)
-    ps = 0 if rstd is None else _flat(rstd, "rstd", dev, n, f32)
+    pm = 0 if mean is None else _flat(mean, "mean", dev, n, _F32)
+    ps = 0 if rstd is None else _flat(rstd, "rstd", dev, n, _F32)
     rc = _lib.zero_norm(_NORM.pack(px, pr, pt, py, pw, pb, pm, ps, n, dim, sx, sr, st, sy, eps, _TYPES[kind], w_type,
                                    1 if rms else 0, 0), _stream(stream, dev))
     if rc:
@@ -259,20 +269,20 @@ def zero_norm_grad(d_y, x, mean, rstd, d_x=None, workspace=None, weight=None, d_
     ``d_x``: of x and of the residual alike. ``accumulate``: add to ``d_weight``
     and ``d_bias``."""
     dev = _device()
-    px, sx, size = _rows(x, "x", dev)
-    kind, (n, dim) = x.dtype, size
-    py, sy, _ = _rows(d_y, "d_y", dev, size, kind)
+    px, sx = _rows(x, "x", dev, None, _TYPES)
+    size, kind = x.shape, x.dtype
+    (n, dim), kinds = size, (kind,)
+    py, sy = _rows(d_y, "d_y", dev, size, kinds)
     pt = st = pd = sd = ws = ws_bytes = pm = 0
     if d_total is not None:
-        pt, st, _ = _rows(d_total, "d_total", dev, size, kind)
+        pt, st = _rows(d_total, "d_total", dev, size, kinds)
     if d_x is not None:
-        pd, sd, _ = _rows(d_x, "d_x", dev, size, kind)
+        pd, sd = _rows(d_x, "d_x", dev, size, kinds)
     pw, _, w_type = _vectors(dev, dim, weight, "weight", None, "")
     pgw, pgb, g_type = _vectors(dev, dim, d_weight, "d_weight", d_bias, "d_bias")
-    f32 = (_torch.float32,)
     if not rms:
-        pm = _flat(mean, "mean", dev, n, f32)
-    ps = _flat(rstd, "rstd", dev, n, f32)
+        pm = _flat(mean, "mean", dev, n, _F32)
+    ps = _flat(rstd, "rstd", dev, n, _F32)
     if workspace is not None:
         ws, ws_bytes = _memory(workspace, "workspace", dev)
     rc = _lib.zero_norm_grad(_NORM_GRAD.pack(py, px, pt, pd, pw, pm, ps, pgw, pgb, n, dim, sy, sx, st, sd, _TYPES[kind],
