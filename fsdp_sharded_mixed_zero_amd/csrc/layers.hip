@@ -33,73 +33,68 @@ using zero::Order;
 // lane's load is one instruction that no branch guards (a guarded one has to wait
 // for those before it), also of a lane with nothing to do, whose lo is E. Rows
 // start at any element, so the accesses are declared with their element's
-// alignment: the hardware takes them at any address. A row shorter than a vector
-// goes element by element.
+// alignment: the hardware takes them at any address. Rows shorter than a vector go
+// with E = 1.
 
 struct Span {
-  int col, lo, hi;     // elements [col + lo, col + hi) of the row are the lane's
+  int col, lo;         // elements [col + lo, col + E) of the row are the lane's
 };
 template <int E>
 __device__ __forceinline__ Span span_of(int vector, int dim) {
-  const int col = vector * E;
-  if (dim < E) return {0, 0, vector == 0 ? dim : 0};
-  const int over = max(0, col + E - dim);
-  return {col - over, min(over, E), E};
+  const int over = max(0, vector * E + E - dim);
+  return {vector * E - over, min(over, E)};
 }
 
 template <int E, typename T> struct Words;
 template <> struct Words<8, uint16_t> { u32x4 w; };
 template <> struct Words<4, uint16_t> { u32x2 w; };
+template <> struct Words<1, uint16_t> { uint16_t w; };
 template <> struct Words<4, float> { f32x4 w; };
 template <> struct Words<8, float> { f32x4 w, w2; };
+template <> struct Words<1, float> { float w; };
 
 template <typename V>
 __device__ __forceinline__ V plain_load(const void* p) { return *(const ZERO_GLOBAL V*)p; }
+template <typename V>
+__device__ __forceinline__ void plain_store(void* p, V x) { *(ZERO_GLOBAL V*)p = x; }
 
+// The E elements at p; STREAM: not kept in the caches.
 template <int E, bool STREAM, typename T>
 __device__ __forceinline__ Words<E, T> load_vector(const T* p) {
   Words<E, T> r;
-  if constexpr (sizeof(T) == 2 && E == 8) r.w = STREAM ? stream_load<words4_any>(p) : plain_load<words4_any>(p);
-  else if constexpr (sizeof(T) == 2) r.w = STREAM ? stream_load<bf16x4_any>(p) : plain_load<bf16x4_any>(p);
-  else r.w = STREAM ? stream_load<f32x4_any>(p) : plain_load<f32x4_any>(p);
-  if constexpr (sizeof(T) == 4 && E == 8) r.w2 = STREAM ? stream_load<f32x4_any>(p + 4) : plain_load<f32x4_any>(p + 4);
-  return r;
-}
-
-// The elements [lo, hi) of the E at p, zeros beside them.
-template <int E, typename T>
-__device__ __forceinline__ Words<E, T> load_some(const T* p, int lo, int hi) {
-  Words<E, T> r{};
-#pragma unroll
-  for (int k = 0; k < E; ++k) {
-    if (k < lo || k >= hi) continue;
-    if constexpr (sizeof(T) == 2) r.w[k >> 1] |= uint32_t(p[k]) << (16 * (k & 1));
-    else if constexpr (E == 8) { if (k < 4) r.w[k & 3] = p[k]; else r.w2[k & 3] = p[k]; }
-    else r.w[k] = p[k];
+  if constexpr (E == 1) {
+    r.w = STREAM ? stream_load<T>(p) : plain_load<T>(p);
+  } else if constexpr (sizeof(T) == 2 && E == 8) {
+    r.w = STREAM ? stream_load<words4_any>(p) : plain_load<words4_any>(p);
+  } else if constexpr (sizeof(T) == 2) {
+    r.w = STREAM ? stream_load<bf16x4_any>(p) : plain_load<bf16x4_any>(p);
+  } else {
+    r.w = STREAM ? stream_load<f32x4_any>(p) : plain_load<f32x4_any>(p);
+    if constexpr (E == 8) r.w2 = STREAM ? stream_load<f32x4_any>(p + 4) : plain_load<f32x4_any>(p + 4);
   }
   return r;
 }
 
-// The lane's vector of the row at p, the neighbour's elements included.
-template <int E, bool STREAM = true, typename T>
-__device__ __forceinline__ Words<E, T> load_row(const T* p, const Span& s, int dim) {
-  if (dim >= E) return load_vector<E, STREAM>(p + s.col);
-  return load_some<E, T>(p, 0, s.hi);
-}
-
-// The neighbour's elements zeroed.
-template <int E>
-__device__ __forceinline__ void only_own(const Span& s, float (&x)[E]) {
-  if (s.lo > 0)
-#pragma unroll
-    for (int k = 0; k < E; ++k) x[k] = k < s.lo ? 0.f : x[k];
+template <int E, bool STREAM, typename T>
+__device__ __forceinline__ void store_vector(T* p, const Words<E, T>& r) {
+  const auto put = [](void* to, auto any, auto x) {
+    if constexpr (STREAM) stream_store<decltype(any)>(to, x);
+    else plain_store<decltype(any)>(to, x);
+  };
+  if constexpr (E == 1) put(p, T(), r.w);
+  else if constexpr (sizeof(T) == 2 && E == 8) put(p, words4_any(), r.w);
+  else if constexpr (sizeof(T) == 2) put(p, bf16x4_any(), r.w);
+  else put(p, f32x4_any(), r.w);
+  if constexpr (sizeof(T) == 4 && E == 8) put(p + 4, f32x4_any(), r.w2);
 }
 
 template <int E, typename T>
 __device__ __forceinline__ void widen(const Words<E, T>& r, float (&x)[E]) {
 #pragma unroll
   for (int k = 0; k < E; ++k) {
-    if constexpr (sizeof(T) == 2) x[k] = (k & 1) ? bf16_hi(r.w[k >> 1]) : bf16_lo(r.w[k >> 1]);
+    if constexpr (E == 1 && sizeof(T) == 2) x[k] = bf16_lo(r.w);
+    else if constexpr (E == 1) x[k] = r.w;
+    else if constexpr (sizeof(T) == 2) x[k] = (k & 1) ? bf16_hi(r.w[k >> 1]) : bf16_lo(r.w[k >> 1]);
     else if constexpr (E == 8) x[k] = k < 4 ? r.w[k & 3] : r.w2[k & 3];
     else x[k] = r.w[k];
   }
@@ -111,51 +106,59 @@ __device__ __forceinline__ Words<E, T> narrow(const float (&x)[E]) {
   Words<E, T> r;
 #pragma unroll
   for (int k = 0; k < E; ++k) {
-    if constexpr (sizeof(T) == 2) { if ((k & 1) == 0) r.w[k >> 1] = pack_bf16x2(x[k], x[k + 1]); }
+    if constexpr (E == 1 && sizeof(T) == 2) r.w = to_bf16(x[k]);
+    else if constexpr (E == 1) r.w = x[k];
+    else if constexpr (sizeof(T) == 2) { if ((k & 1) == 0) r.w[k >> 1] = pack_bf16x2(x[k], x[k + 1]); }
     else if constexpr (E == 8) { if (k < 4) r.w[k & 3] = x[k]; else r.w2[k & 3] = x[k]; }
     else r.w[k] = x[k];
   }
   return r;
 }
 
-// The words as if just read: what was computed from them before is not kept.
+// The elements [lo, hi) of the E at p, zeros beside them.
 template <int E, typename T>
-__device__ __forceinline__ void opaque(Words<E, T>& r) {
-  asm volatile("" : "+v"(r.w));
-  if constexpr (sizeof(T) == 4 && E == 8) asm volatile("" : "+v"(r.w2));
-}
-
-// The elements [lo, cnt) of the lane's E.
-template <int E, typename T>
-__device__ __forceinline__ void store_some(T* p, int lo, int cnt, const Words<E, T>& r) {
+__device__ __forceinline__ Words<E, T> load_some(const T* p, int lo, int hi) {
+  Words<E, T> r{};
 #pragma unroll
   for (int k = 0; k < E; ++k) {
-    if (k < lo || k >= cnt) continue;
-    if constexpr (sizeof(T) == 2) p[k] = uint16_t(r.w[k >> 1] >> (16 * (k & 1)));
+    if (k < lo || k >= hi) continue;
+    if constexpr (E == 1) r.w = p[k];
+    else if constexpr (sizeof(T) == 2) r.w[k >> 1] |= uint32_t(p[k]) << (16 * (k & 1));
+    else r.w[k] = p[k];
+  }
+  return r;
+}
+
+template <int E, typename T>
+__device__ __forceinline__ void store_some(T* p, int lo, int hi, const Words<E, T>& r) {
+#pragma unroll
+  for (int k = 0; k < E; ++k) {
+    if (k < lo || k >= hi) continue;
+    if constexpr (E == 1) p[k] = r.w;
+    else if constexpr (sizeof(T) == 2) p[k] = uint16_t(r.w[k >> 1] >> (16 * (k & 1)));
     else if constexpr (E == 8) p[k] = k < 4 ? r.w[k & 3] : r.w2[k & 3];
     else p[k] = r.w[k];
   }
 }
 
-template <int E, bool STREAM, typename T>
-__device__ __forceinline__ void store_vector(T* p, const Words<E, T>& r) {
-  if constexpr (STREAM) {
-    if constexpr (sizeof(T) == 2 && E == 8) stream_store<words4_any>(p, r.w);
-    else if constexpr (sizeof(T) == 2) stream_store<bf16x4_any>(p, r.w);
-    else stream_store<f32x4_any>(p, r.w);
-    if constexpr (sizeof(T) == 4 && E == 8) stream_store<f32x4_any>(p + 4, r.w2);
-  } else {
-    if constexpr (sizeof(T) == 2 && E == 8) *(ZERO_GLOBAL words4_any*)p = r.w;
-    else if constexpr (sizeof(T) == 2) *(ZERO_GLOBAL bf16x4_any*)p = r.w;
-    else *(ZERO_GLOBAL f32x4_any*)p = r.w;
-    if constexpr (sizeof(T) == 4 && E == 8) *(ZERO_GLOBAL f32x4_any*)(p + 4) = r.w2;
-  }
+// The lane's vector of the row at p, the neighbour's elements included.
+template <int E, bool STREAM = true, typename T>
+__device__ __forceinline__ Words<E, T> load_row(const T* p, const Span& s) {
+  return load_vector<E, STREAM>(p + s.col);
 }
 
 template <int E, bool STREAM = true, typename T>
 __device__ __forceinline__ void store_row(T* p, const Span& s, const Words<E, T>& r) {
-  if (s.lo == 0 && s.hi == E) store_vector<E, STREAM>(p + s.col, r);
-  else store_some<E, T>(p + s.col, s.lo, s.hi, r);
+  if (s.lo == 0) store_vector<E, STREAM>(p + s.col, r);
+  else store_some<E, T>(p + s.col, s.lo, E, r);
+}
+
+// The neighbour's elements zeroed.
+template <int E>
+__device__ __forceinline__ void only_own(const Span& s, float (&x)[E]) {
+  if (s.lo > 0)
+#pragma unroll
+    for (int k = 0; k < E; ++k) x[k] = k < s.lo ? 0.f : x[k];
 }
 
 // ------------------------------------------------------------------- lookup
@@ -181,7 +184,7 @@ __global__ __launch_bounds__(256) void embedding_kernel(const I* __restrict__ to
   for (int k = 0; k < kLookupRows; ++k) row[k] = table_row(uniform_load(tokens + min(t0 + k, int64_t(n - 1))), rows);
 #pragma unroll
   for (int k = 0; k < kLookupRows; ++k)
-    x[k] = load_row<E, false>(table + int64_t(row[k] < rows ? row[k] : 0) * dim, s, dim);
+    x[k] = load_row<E, false>(table + int64_t(row[k] < rows ? row[k] : 0) * dim, s);
 #pragma unroll
   for (int k = 0; k < kLookupRows; ++k) {
     if (t0 + k >= n) break;
@@ -388,7 +391,7 @@ struct EmbeddingGradArgs {
   float scale;
   int32_t n, dim, dim4, tiles, pieces, piece;
   int32_t row_lo, row_hi;    // rows that the part touches
-  int32_t sum_blocks, accumulate;
+  int32_t sum_blocks;
 };
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
@@ -398,35 +401,34 @@ __device__ __forceinline__ i32x8 load8(const int32_t* p) {
   return *(const __attribute__((address_space(4))) i32x8_any*)p;
 }
 
-// The elements of row r that are the lane's and in the part: those of `s`, cut
-// where the part begins or ends inside the row.
-__device__ __forceinline__ Span in_part(const EmbeddingGradArgs& a, int64_t base, Span s) {
-  if (base < 0) s.lo = max(s.lo, int(min(-base - s.col, int64_t(64))));
-  if (base + a.dim > a.count) s.hi = min(s.hi, int(max(a.count - base - s.col, int64_t(0))));
-  return s;
-}
-
-// grad's elements of row r at the lane's span, before the sum is added.
+// grad's elements of row r at the lane's span. Where the part begins or ends inside
+// the row, only those of the lane's elements that lie in it.
 template <int E, typename G>
 __device__ __forceinline__ Words<E, G> read_grad(const EmbeddingGradArgs& a, int r, const Span& s) {
   const int64_t base = int64_t(r) * a.dim - a.first;      // grad's index of the row's first element
   const G* g = static_cast<const G*>(a.grad) + base;
-  if (base >= 0 && base + a.dim <= a.count) return load_row<E>(g, s, a.dim);
-  const Span p = in_part(a, base, s);
-  return load_some<E, G>(g + p.col, p.lo, p.hi);
+  if (base >= 0 && base + a.dim <= a.count) return load_row<E>(g, s);
+  const int lo = int(max(int64_t(s.lo), -base - s.col)), hi = int(min(int64_t(E), a.count - base - s.col));
+  return load_some<E, G>(g + s.col, lo, hi);
 }
 
 template <int E, typename G>
 __device__ __forceinline__ void write_grad(const EmbeddingGradArgs& a, int r, const Span& s, const Words<E, G>& w) {
   const int64_t base = int64_t(r) * a.dim - a.first;
-  store_row<E>(static_cast<G*>(a.grad) + base, in_part(a, base, s), w);
+  G* g = static_cast<G*>(a.grad) + base;
+  if (base >= 0 && base + a.dim <= a.count) {
+    store_row<E>(g, s, w);
+    return;
+  }
+  const int lo = int(max(int64_t(s.lo), -base - s.col)), hi = int(min(int64_t(E), a.count - base - s.col));
+  store_some<E, G>(g + s.col, lo, hi, w);
 }
 
-template <int E, typename G>
+template <int E, typename G, bool ADD>
 __device__ __forceinline__ void write_sum(const EmbeddingGradArgs& a, int r, const Span& s, const Words<E, G>& old,
                                           const float (&sum)[E]) {
   float v[E];
-  if (a.accumulate) {
+  if constexpr (ADD) {
     widen<E, G>(old, v);
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] = fmaf(sum[e], a.scale, v[e]);
@@ -437,34 +439,53 @@ __device__ __forceinline__ void write_sum(const EmbeddingGradArgs& a, int r, con
   write_grad<E, G>(a, r, s, narrow<E, G>(v));
 }
 
-// Whether r is among the n sorted rows: 64 compared at a time, their spacing
-// divided by 64 each round.
-__device__ __forceinline__ bool has_token(const int32_t* row, int n, int r) {
+// The first of the n sorted rows at or above r, or n: 64 compared at a time, their
+// spacing divided by 64 each round.
+__device__ __forceinline__ int first_at(const int32_t* row, int n, int r) {
   const int lane = threadIdx.x & 63;
-  int lo = 0;                          // the first row at or above r, if there is one, is in [lo, lo + n)
-  while (n > 0) {
-    const int step = (n + 63) >> 6;
-    const int last = row[lo + min((lane + 1) * step, n) - 1];      // of the lane's rows
+  int lo = 0, len = n;                 // it is in [lo, lo + len]
+  while (len > 0) {
+    const int step = (len + 63) >> 6;
+    const int last = row[lo + min((lane + 1) * step, len) - 1];    // of the lane's rows
     const int below = __popcll(__ballot(last < r));                // so many lanes' rows lie below r
-    if (below == 64) return false;
-    if (step == 1) return __builtin_amdgcn_readlane(last, below) == r;
+    if (below == 64) return lo + len;
+    len = __builtin_amdgcn_readfirstlane(min(step, len - below * step));
     lo = __builtin_amdgcn_readfirstlane(lo + below * step);
-    n = __builtin_amdgcn_readfirstlane(min(step, n - below * step));
+    if (step == 1) return lo;
   }
-  return false;
+  return lo;
 }
 
+// Of the rows [r0, r1), at most 64, those that are not among the sorted ones, a
+// bit each: between the first sorted one and the last, every lane looks for its own.
+__device__ __forceinline__ uint64_t rows_without(const int32_t* row, int n, int r0, int r1) {
+  const int mine = r0 + int(threadIdx.x & 63);
+  const int from = first_at(row, n, r0), to = first_at(row, n, r1);
+  int lo = from, hi = to;
+  while (__ballot(lo < hi)) {
+    const int mid = (lo + hi) >> 1;
+    const int x = row[min(mid, n - 1)];
+    const bool up = lo < hi && x < mine;
+    hi = lo < hi && !up ? mid : hi;
+    lo = up ? mid + 1 : lo;
+  }
+  const bool there = lo < to && row[max(min(lo, n - 1), 0)] == mine;
+  return __ballot(mine < r1 && !there);
+}
+
+constexpr int kFillRows = 4;   // rows that a wave looks for and clears
 constexpr int kBatch = 8;      // rows that a wave loads before it adds them
 
-template <typename T, typename G, int E>
+template <typename T, typename G, int E, bool ADD>
 __global__ __launch_bounds__(256) void embedding_grad_kernel(const EmbeddingGradArgs a) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (int(blockIdx.x) >= a.sum_blocks) {
-    // zeros for a row without a token, a wave a row (16 rows a wave: the whole gradient of 50257 x 2944 in
-    // 75 us instead of 61)
-    const int r = a.row_lo + (int(blockIdx.x) - a.sum_blocks) * 4 + wave;
-    if (r >= a.row_hi || has_token(a.row, a.n, r)) return;
-    for (int k = 0; k < a.tiles; ++k) write_grad<E, G>(a, r, span_of<E>(k * 64 + lane, a.dim), Words<E, G>{});
+  if (!ADD && int(blockIdx.x) >= a.sum_blocks) {      // zeros for the rows without a token
+    const uint32_t w = (blockIdx.x - a.sum_blocks) * 4 + wave;
+    const int r0 = a.row_lo + int(w / uint32_t(a.tiles)) * kFillRows, r1 = min(r0 + kFillRows, a.row_hi);
+    if (r0 >= r1) return;
+    const Span s = span_of<E>(int(w % uint32_t(a.tiles)) * 64 + lane, a.dim);
+    for (uint64_t absent = rows_without(a.row, a.n, r0, r1); absent != 0; absent &= absent - 1)
+      write_grad<E, G>(a, r0 + __builtin_ctzll(absent), s, Words<E, G>{});
     return;
   }
   const uint32_t w = blockIdx.x * 4 + wave;
@@ -486,15 +507,15 @@ __global__ __launch_bounds__(256) void embedding_grad_kernel(const EmbeddingGrad
     const int r9 = uniform_load(a.row + i + kBatch);
     int r[kBatch + 1];
     Words<E, T> x[kBatch];
-    Words<E, G> old[kBatch];
+    Words<E, G> old[ADD ? kBatch : 1];
 #pragma unroll
     for (int k = 0; k <= kBatch; ++k) r[k] = i + k >= a.n ? -1 : k < kBatch ? r8[k % kBatch] : r9;
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const bool mine = i + k < i1 && r[k] >= a.row_lo && r[k] < a.row_hi;
-      x[k] = load_row<E>(static_cast<const T*>(a.d_out) + (mine ? int64_t(p8[k]) * a.stride : 0), s, a.dim);
+      const int p = i + k < i1 && r[k] >= a.row_lo && r[k] < a.row_hi ? p8[k] : 0;      // a row that is there
+      x[k] = load_row<E>(static_cast<const T*>(a.d_out) + int64_t(p) * a.stride, s);
     }
-    if (a.accumulate) {
+    if constexpr (ADD) {
 #pragma unroll
       for (int k = 0; k < kBatch; ++k)
         if (i + k < i1 && r[k] != r[k + 1] && r[k] >= a.row_lo && r[k] < a.row_hi) old[k] = read_grad<E, G>(a, r[k], s);
@@ -512,7 +533,7 @@ __global__ __launch_bounds__(256) void embedding_grad_kernel(const EmbeddingGrad
         if (head || !end)
           store_row<E, false>(a.ws + (int64_t(piece) * 2 + (head ? 0 : 1)) * a.dim4, s, narrow<E, float>(sum));
         else
-          write_sum<E, G>(a, r[k], s, old[k], sum);
+          write_sum<E, G, ADD>(a, r[k], s, old[ADD ? k : 0], sum);
       }
       head = false;
 #pragma unroll
@@ -521,7 +542,7 @@ __global__ __launch_bounds__(256) void embedding_grad_kernel(const EmbeddingGrad
   }
 }
 
-template <typename G, int E>
+template <typename G, int E, bool ADD>
 __global__ __launch_bounds__(256) void embedding_join_kernel(const EmbeddingGradArgs a) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t w = blockIdx.x * 4 + wave;
@@ -545,25 +566,25 @@ __global__ __launch_bounds__(256) void embedding_join_kernel(const EmbeddingGrad
   }
   const float* p = a.ws + int64_t(piece) * 2 * a.dim4;
   float sum[E];
-  widen<E, float>(load_row<E, false>(p + a.dim4, s, a.dim), sum);
+  widen<E, float>(load_row<E, false>(p + a.dim4, s), sum);
 #pragma unroll 8
   for (int j = piece + 1; j <= last; ++j) {
     float v[E];
-    widen<E, float>(load_row<E, false>(p + int64_t(j - piece) * 2 * a.dim4, s, a.dim), v);
+    widen<E, float>(load_row<E, false>(p + int64_t(j - piece) * 2 * a.dim4, s), v);
 #pragma unroll
     for (int e = 0; e < E; ++e) sum[e] += v[e];
   }
   Words<E, G> old{};
-  if (a.accumulate) old = read_grad<E, G>(a, r, s);
-  write_sum<E, G>(a, r, s, old, sum);
+  if constexpr (ADD) old = read_grad<E, G>(a, r, s);
+  write_sum<E, G, ADD>(a, r, s, old, sum);
 }
 
 // --------------------------------------------------------------------- norm
 
 // E elements of a vector; ones or zeros where there is none.
 template <int E, typename W>
-__device__ __forceinline__ Words<E, W> load_weight(const void* w, const Span& s, int dim, float none) {
-  if (w != nullptr) return load_row<E, false>(static_cast<const W*>(w), s, dim);
+__device__ __forceinline__ Words<E, W> load_weight(const void* w, const Span& s, float none) {
+  if (w != nullptr) return load_row<E, false>(static_cast<const W*>(w), s);
   float x[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) x[e] = none;
@@ -619,9 +640,8 @@ __device__ __forceinline__ void row_sum(float (&x)[K], float* lds, int turn) {
   }
 }
 
-template <typename T, typename W, int TPR, int V>
+template <typename T, typename W, int E, int TPR, int V>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(const zero_norm_args a) {
-  constexpr int E = 16 / int(sizeof(T));
   constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
   __shared__ float lds[2 * (TPR < 256 ? 4 : TPR / 64)];
   const int64_t row = int64_t(blockIdx.x) * kRows + threadIdx.x / TPR;
@@ -635,7 +655,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(const zero_
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     s[k] = span_of<E>(t + k * TPR, dim);
-    raw[k] = load_row<E>(x, s[k], dim);
+    raw[k] = load_row<E>(x, s[k]);
   }
   float v[V][E];
   if (a.residual != nullptr) {
@@ -643,11 +663,11 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(const zero_
     T* total = static_cast<T*>(a.total) + row * a.total_stride;
     Words<E, T> more[V];
 #pragma unroll
-    for (int k = 0; k < V; ++k) more[k] = load_row<E>(res, s[k], dim);
+    for (int k = 0; k < V; ++k) more[k] = load_row<E>(res, s[k]);
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      w[k] = load_weight<E, W>(a.weight, s[k], dim, 1.f);
-      b[k] = load_weight<E, W>(a.bias, s[k], dim, 0.f);
+      w[k] = load_weight<E, W>(a.weight, s[k], 1.f);
+      b[k] = load_weight<E, W>(a.bias, s[k], 0.f);
     }
 #pragma unroll
     for (int k = 0; k < V; ++k) {
@@ -662,8 +682,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(const zero_
   } else {
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      w[k] = load_weight<E, W>(a.weight, s[k], dim, 1.f);
-      b[k] = load_weight<E, W>(a.bias, s[k], dim, 0.f);
+      w[k] = load_weight<E, W>(a.weight, s[k], 1.f);
+      b[k] = load_weight<E, W>(a.bias, s[k], 0.f);
     }
   }
   float sum[1] = {0.f};
@@ -685,10 +705,6 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(const zero_
 #pragma unroll
     for (int e = 0; e < E; ++e) v[k][e] -= mean;
     only_own<E>(s[k], v[k]);
-    if (dim < E) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[k][e] = e < s[k].hi ? v[k][e] : 0.f;
-    }
 #pragma unroll
     for (int e = 0; e < E; ++e) sum[0] = fmaf(v[k][e], v[k][e], sum[0]);
   }
@@ -727,11 +743,11 @@ __global__ __launch_bounds__(kLongThreads) void norm_long_kernel(const zero_norm
   for (int k = threadIdx.x; k < vectors; k += kLongThreads) {
     const Span s = span_of<E>(k, dim);
     float v[E];
-    Words<E, T> raw = load_row<E, false>(x, s, dim);
+    Words<E, T> raw = load_row<E, false>(x, s);
     widen<E, T>(raw, v);
     if (res != nullptr) {
       float r[E];
-      widen<E, T>(load_row<E, false>(res, s, dim), r);
+      widen<E, T>(load_row<E, false>(res, s), r);
 #pragma unroll
       for (int e = 0; e < E; ++e) v[e] += r[e];
       raw = narrow<E, T>(v);
@@ -752,7 +768,7 @@ __global__ __launch_bounds__(kLongThreads) void norm_long_kernel(const zero_norm
   for (int k = threadIdx.x; k < vectors; k += kLongThreads) {
     const Span s = span_of<E>(k, dim);
     float v[E];
-    widen<E, T>(load_row<E, false>(x, s, dim), v);
+    widen<E, T>(load_row<E, false>(x, s), v);
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] -= mean;
     only_own<E>(s, v);
@@ -769,9 +785,9 @@ __global__ __launch_bounds__(kLongThreads) void norm_long_kernel(const zero_norm
   for (int k = threadIdx.x; k < vectors; k += kLongThreads) {
     const Span s = span_of<E>(k, dim);
     float v[E], w[E], b[E];
-    widen<E, T>(load_row<E, false>(x, s, dim), v);
-    widen<E, W>(load_weight<E, W>(a.weight, s, dim, 1.f), w);
-    widen<E, W>(load_weight<E, W>(a.bias, s, dim, 0.f), b);
+    widen<E, T>(load_row<E, false>(x, s), v);
+    widen<E, W>(load_weight<E, W>(a.weight, s, 1.f), w);
+    widen<E, W>(load_weight<E, W>(a.bias, s, 0.f), b);
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] = fmaf((v[e] - mean) * rstd, w[e], b[e]);
     store_row<E, false>(y, s, narrow<E, T>(v));
@@ -785,9 +801,8 @@ __global__ __launch_bounds__(kLongThreads) void norm_long_kernel(const zero_norm
 // LDS and go to the workspace, which norm_grad_join_kernel adds up.
 constexpr int grad_threads(int per_row) { return per_row >= 512 ? per_row : 512 / per_row * per_row; }
 
-template <typename T, typename W, int TPR, int V>
+template <typename T, typename W, int E, int TPR, int V>
 __global__ __launch_bounds__(grad_threads(TPR)) void norm_grad_kernel(const zero_norm_grad_args a, float* ws, int dim4) {
-  constexpr int E = 16 / int(sizeof(T));
   constexpr int kThreads = grad_threads(TPR), kRows = kThreads / TPR;
   __shared__ float lds[kThreads * V * E];      // row sums, then the groups' column sums
   const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
@@ -799,7 +814,7 @@ __global__ __launch_bounds__(grad_threads(TPR)) void norm_grad_kernel(const zero
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     s[k] = span_of<E>(t + k * TPR, dim);
-    w_raw[k] = load_weight<E, W>(a.weight, s[k], dim, 1.f);
+    w_raw[k] = load_weight<E, W>(a.weight, s[k], 1.f);
 #pragma unroll
     for (int e = 0; e < E; ++e) sum_w[k][e] = sum_b[k][e] = 0.f;
   }
@@ -813,13 +828,13 @@ __global__ __launch_bounds__(grad_threads(TPR)) void norm_grad_kernel(const zero
     const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      r.dy[k] = load_row<E>(dy, s[k], dim);
-      r.x[k] = load_row<E>(x, s[k], dim);
+      r.dy[k] = load_row<E>(dy, s[k]);
+      r.x[k] = load_row<E>(x, s[k]);
     }
     if (skip) {
 #pragma unroll
       for (int k = 0; k < V; ++k)
-        r.total[k] = load_row<E>(static_cast<const T*>(a.d_total) + row * a.d_total_stride, s[k], dim);
+        r.total[k] = load_row<E>(static_cast<const T*>(a.d_total) + row * a.d_total_stride, s[k]);
     }
     r.mean = a.rms ? 0.f : a.mean[row];
     r.rstd = a.rstd[row];
@@ -920,7 +935,7 @@ __global__ __launch_bounds__(grad_threads(TPR)) void norm_grad_kernel(const zero
         for (int g = 0; g < kRows; ++g) x += lds[g * V * E * TPR + j];
         const int ke = j / TPR, e = ke % E;
         const Span at = span_of<E>(j % TPR + ke / E * TPR, dim);
-        if (e >= at.lo && e < at.hi) out[which * dim4 + at.col + e] = x;
+        if (e >= at.lo) out[which * dim4 + at.col + e] = x;
       }
     }
   }
@@ -942,9 +957,9 @@ __global__ __launch_bounds__(kLongThreads) void norm_grad_long_kernel(const zero
   for (int k = threadIdx.x; k < vectors; k += kLongThreads) {
     const Span s = span_of<E>(k, dim);
     float g[E], xh[E], w[E];
-    widen<E, T>(load_row<E, false>(dy, s, dim), g);
-    widen<E, T>(load_row<E, false>(x, s, dim), xh);
-    widen<E, W>(load_weight<E, W>(a.weight, s, dim, 1.f), w);
+    widen<E, T>(load_row<E, false>(dy, s), g);
+    widen<E, T>(load_row<E, false>(x, s), xh);
+    widen<E, W>(load_weight<E, W>(a.weight, s, 1.f), w);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       g[e] *= w[e];
@@ -963,12 +978,12 @@ __global__ __launch_bounds__(kLongThreads) void norm_grad_long_kernel(const zero
   for (int k = threadIdx.x; k < vectors; k += kLongThreads) {
     const Span s = span_of<E>(k, dim);
     float g[E], xh[E], w[E], m[E];
-    widen<E, T>(load_row<E, false>(dy, s, dim), g);
-    widen<E, T>(load_row<E, false>(x, s, dim), xh);
-    widen<E, W>(load_weight<E, W>(a.weight, s, dim, 1.f), w);
+    widen<E, T>(load_row<E, false>(dy, s), g);
+    widen<E, T>(load_row<E, false>(x, s), xh);
+    widen<E, W>(load_weight<E, W>(a.weight, s, 1.f), w);
 #pragma unroll
     for (int e = 0; e < E; ++e) m[e] = 0.f;
-    if (d_total != nullptr) widen<E, T>(load_row<E, false>(d_total, s, dim), m);
+    if (d_total != nullptr) widen<E, T>(load_row<E, false>(d_total, s), m);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       xh[e] = (xh[e] - mean) * rstd;
@@ -989,8 +1004,8 @@ __global__ __launch_bounds__(256) void norm_grad_columns_kernel(const zero_norm_
   for (int64_t row = blockIdx.y; row < a.n; row += gridDim.y) {
     const float mean = a.rms ? 0.f : uniform_load(a.mean + row), rstd = uniform_load(a.rstd + row);
     float g[E], xh[E];
-    widen<E, T>(load_row<E, false>(static_cast<const T*>(a.d_y) + row * a.d_y_stride, s, dim), g);
-    widen<E, T>(load_row<E, false>(static_cast<const T*>(a.x) + row * a.x_stride, s, dim), xh);
+    widen<E, T>(load_row<E, false>(static_cast<const T*>(a.d_y) + row * a.d_y_stride, s), g);
+    widen<E, T>(load_row<E, false>(static_cast<const T*>(a.x) + row * a.x_stride, s), xh);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       sum_w[e] = fmaf(g[e], (xh[e] - mean) * rstd, sum_w[e]);
@@ -1042,6 +1057,13 @@ void by_types(int32_t first, int32_t second, const F& go) {
   else second == ZERO_BF16 ? go(float(), uint16_t()) : go(float(), float());
 }
 
+// With E elements a vector, or 1 where a row has fewer.
+template <int E, typename F>
+void by_width(int64_t dim, const F& go) {
+  if (dim >= E) go(Int<E>());
+  else go(Int<1>());
+}
+
 // How a row of `vectors` 16-byte vectors is spread over threads: few vectors a
 // thread, so that many waves share the latency.
 NormShape norm_shape(int64_t vectors) {
@@ -1078,16 +1100,18 @@ int launch_embedding(const void* tokens, bool wide, int64_t n, const void* table
   const auto go = [&](auto tv, auto ov) {
     using T = decltype(tv);
     using O = decltype(ov);
-    constexpr int E = sizeof(T) == 2 && sizeof(O) == 2 ? 8 : 4;
-    const int64_t tiles = (dim + 64 * E - 1) / (64 * E);
-    const int64_t waves = (n + kLookupRows - 1) / kLookupRows * tiles;
-    const auto run = [&](auto iv) {
-      using I = decltype(iv);
-      embedding_kernel<I, T, O, E><<<dim3(uint32_t((waves + 3) / 4)), 256, 0, stream>>>(
-          static_cast<const I*>(tokens), int(n), static_cast<const T*>(table), int(rows), int(dim), int(tiles), scale,
-          static_cast<O*>(out), out_stride);
-    };
-    wide ? run(int64_t()) : run(int32_t());
+    by_width<sizeof(T) == 2 && sizeof(O) == 2 ? 8 : 4>(dim, [&](auto ev) {
+      constexpr int E = decltype(ev)::value;
+      const int64_t tiles = (dim + 64 * E - 1) / (64 * E);
+      const int64_t waves = (n + kLookupRows - 1) / kLookupRows * tiles;
+      const auto run = [&](auto iv) {
+        using I = decltype(iv);
+        embedding_kernel<I, T, O, E><<<dim3(uint32_t((waves + 3) / 4)), 256, 0, stream>>>(
+            static_cast<const I*>(tokens), int(n), static_cast<const T*>(table), int(rows), int(dim), int(tiles), scale,
+            static_cast<O*>(out), out_stride);
+      };
+      wide ? run(int64_t()) : run(int32_t());
+    });
   };
   by_types(table_type, out_type, go);
   return launched(who);
@@ -1157,19 +1181,23 @@ int launch_embedding_grad(const int32_t* order, int64_t n, int64_t rows, int64_t
   a.pieces = int32_t(embedding_pieces(n));
   a.row_lo = int32_t(first / dim);
   a.row_hi = int32_t((first + count + dim - 1) / dim);
-  a.accumulate = accumulate;
   const auto go = [&](auto tv, auto gv) {
     using T = decltype(tv);
     using G = decltype(gv);
-    constexpr int E = sizeof(T) == 2 && sizeof(G) == 2 ? 8 : 4;
-    a.tiles = int32_t((dim + 64 * E - 1) / (64 * E));
-    const int64_t sums = (int64_t(a.pieces) * a.tiles + 3) / 4;
-    const int touched = a.row_hi - a.row_lo;
-    const int64_t fills = accumulate ? 0 : (touched + 3) / 4;
-    a.sum_blocks = int32_t(sums);
-    if (sums + fills > 0)
-      embedding_grad_kernel<T, G, E><<<dim3(uint32_t(sums + fills)), 256, 0, stream>>>(a);
-    if (a.pieces > 1) embedding_join_kernel<G, E><<<dim3(uint32_t(sums)), 256, 0, stream>>>(a);
+    by_width<sizeof(T) == 2 && sizeof(G) == 2 ? 8 : 4>(dim, [&](auto ev) {
+      constexpr int E = decltype(ev)::value;
+      a.tiles = int32_t((dim + 64 * E - 1) / (64 * E));
+      const int64_t sums = (int64_t(a.pieces) * a.tiles + 3) / 4;
+      a.sum_blocks = int32_t(sums);
+      const int64_t groups = (a.row_hi - a.row_lo + kFillRows - 1) / kFillRows;
+      const int64_t fills = accumulate ? 0 : (groups * a.tiles + 3) / 4;
+      const auto run = [&](auto add) {
+        constexpr bool ADD = decltype(add)::value;
+        if (sums + fills > 0) embedding_grad_kernel<T, G, E, ADD><<<dim3(uint32_t(sums + fills)), 256, 0, stream>>>(a);
+        if (a.pieces > 1) embedding_join_kernel<G, E, ADD><<<dim3(uint32_t(sums)), 256, 0, stream>>>(a);
+      };
+      accumulate ? run(std::true_type()) : run(std::false_type());
+    });
   };
   by_types(out_type, grad_type, go);
   return launched(who);
@@ -1185,9 +1213,12 @@ int launch_norm(const zero_norm_args& a, hipStream_t stream, const char* who) {
     const dim3 grid{uint32_t((a.n + rows - 1) / rows)};
     const auto spread = [&](auto threads, auto vectors) {
       constexpr int TPR = decltype(threads)::value, V = decltype(vectors)::value;
-      if (s.threads != TPR || s.vectors != V) return;
-      norm_kernel<T, W, TPR, V><<<grid, TPR < 256 ? 256 : TPR, 0, stream>>>(a);
+      if (s.threads == TPR && s.vectors == V) norm_kernel<T, W, E, TPR, V><<<grid, TPR < 256 ? 256 : TPR, 0, stream>>>(a);
     };
+    if (a.dim < E) {
+      norm_kernel<T, W, 1, 16, 1><<<grid, 256, 0, stream>>>(a);
+      return;
+    }
     spread(Int<16>(), Int<1>());
     spread(Int<64>(), Int<1>());
     spread(Int<64>(), Int<2>());
@@ -1214,8 +1245,12 @@ int launch_norm_grad(const zero_norm_grad_args& a, float* ws, hipStream_t stream
     const auto spread = [&](auto threads, auto vectors) {
       constexpr int TPR = decltype(threads)::value, V = decltype(vectors)::value;
       if (s.threads != TPR || s.vectors != V) return;
-      norm_grad_kernel<T, W, TPR, V><<<dim3(uint32_t(blocks)), grad_threads(TPR), 0, stream>>>(a, ws, dim4);
+      norm_grad_kernel<T, W, E, TPR, V><<<dim3(uint32_t(blocks)), grad_threads(TPR), 0, stream>>>(a, ws, dim4);
     };
+    if (a.dim < E) {
+      norm_grad_kernel<T, W, 1, 16, 1><<<dim3(uint32_t(blocks)), grad_threads(16), 0, stream>>>(a, ws, dim4);
+      return;
+    }
     spread(Int<16>(), Int<1>());
     spread(Int<64>(), Int<8 / E>());
     spread(Int<128>(), Int<8 / E>());

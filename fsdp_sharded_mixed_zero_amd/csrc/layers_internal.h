@@ -14,7 +14,7 @@ namespace zero {
 
 // Sorted tokens that one wave of the table's gradient sums (a multiple of 8), and
 // a workspace's rows: two sums for each such piece.
-inline int embedding_piece(int64_t n) { return n <= 4096 ? 8 : 32; }
+inline int embedding_piece(int64_t n) { return n <= 4096 ? 8 : 16; }
 inline int64_t embedding_pieces(int64_t n) { return (n + embedding_piece(n) - 1) / embedding_piece(n); }
 
 // Tokens that one block of the sort takes, and the bits of one of its passes.
