@@ -895,7 +895,7 @@ __global__ __launch_bounds__(grad_threads(TPR)) void norm_grad_kernel(const zero
     }
   };
   // the next rows are on their way while these are summed
-  constexpr int kAhead = V * E > 8 ? 0 : 1;
+  constexpr int kAhead = V * E > 8 ? 0 : V * E > 4 ? 1 : 2;
   Row ring[kAhead + 1];
   int64_t row0 = int64_t(blockIdx.x) * kRows;
 #pragma unroll
@@ -915,13 +915,14 @@ __global__ __launch_bounds__(grad_threads(TPR)) void norm_grad_kernel(const zero
   if constexpr (kRows == 1) {
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      store_row<E, false>(out, s[k], narrow<E, float>(sum_w[k]));
-      store_row<E, false>(out + dim4, s[k], narrow<E, float>(sum_b[k]));
+      if (a.d_weight != nullptr) store_row<E, false>(out, s[k], narrow<E, float>(sum_w[k]));
+      if (a.d_bias != nullptr) store_row<E, false>(out + dim4, s[k], narrow<E, float>(sum_b[k]));
     }
   } else {
     // [group][V][E][TPR], lanes side by side; a vector's neighbour's elements are left out
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
+      if ((which ? a.d_bias : a.d_weight) == nullptr) continue;
       __syncthreads();
 #pragma unroll
       for (int k = 0; k < V; ++k)
@@ -1078,6 +1079,9 @@ NormShape norm_grad_shape(int64_t dim, int per) {
   const int64_t vectors = (dim + per - 1) / per;
   static const int threads[] = {64, 128, 192, 256, 384, 512, 768, 1024};
   if (vectors <= 16) return {16, 1};
+  if (per == 4)
+    for (int t : {64, 128, 192, 256, 320, 384, 512, 768})
+      if (t >= vectors) return {t, 1};
   for (int t : threads)
     if (int64_t(t) * (8 / per) >= vectors) return {t, 8 / per};
   return vectors <= 2 * 1024 * (8 / per) ? NormShape{1024, 16 / per} : NormShape{0, 0};
@@ -1253,6 +1257,16 @@ int launch_norm_grad(const zero_norm_grad_args& a, float* ws, hipStream_t stream
     }
     spread(Int<16>(), Int<1>());
     spread(Int<64>(), Int<8 / E>());
+    if constexpr (E == 4) {
+      spread(Int<64>(), Int<1>());
+      spread(Int<128>(), Int<1>());
+      spread(Int<192>(), Int<1>());
+      spread(Int<256>(), Int<1>());
+      spread(Int<320>(), Int<1>());
+      spread(Int<384>(), Int<1>());
+      spread(Int<512>(), Int<1>());
+      spread(Int<768>(), Int<1>());
+    }
     spread(Int<128>(), Int<8 / E>());
     spread(Int<192>(), Int<8 / E>());
     spread(Int<256>(), Int<8 / E>());
