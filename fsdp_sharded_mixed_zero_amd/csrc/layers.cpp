@@ -151,7 +151,9 @@ extern "C" int zero_token_order(const void* tokens, int32_t token_type, int64_t 
 
 extern "C" size_t zero_embedding_grad_workspace_bytes(int64_t n, int64_t dim) {
   if (!sizes_fit(n, dim)) return 0;
-  return size_t(std::max<int64_t>(1, zero::embedding_pieces(n))) * 2 * size_t((dim + 3) / 4 * 4) * sizeof(float);
+  // never less than for fewer tokens, whose pieces are shorter
+  const int64_t pieces = std::max<int64_t>({1, zero::embedding_pieces(n), zero::embedding_pieces(std::min(n, zero::kShortPieces))});
+  return size_t(pieces) * 2 * size_t((dim + 3) / 4 * 4) * sizeof(float);
 }
 
 extern "C" int zero_embedding_grad(const void* order, int64_t n, int64_t rows, int64_t dim, const void* d_out,

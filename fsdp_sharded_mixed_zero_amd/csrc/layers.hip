@@ -23,6 +23,7 @@ using zero::kSortBlock;
 using zero::kSortDigits;
 using zero::kSortItems;
 using zero::kSortThreads;
+using zero::grad_threads;
 using zero::NormShape;
 using zero::Order;
 
@@ -799,8 +800,6 @@ __global__ __launch_bounds__(kLongThreads) void norm_long_kernel(const zero_norm
 // A block takes every gridDim.x-th group of rows, TPR threads a row, and keeps the
 // sums of d_weight and d_bias over its rows in registers; the groups' sums meet in
 // LDS and go to the workspace, which norm_grad_join_kernel adds up.
-constexpr int grad_threads(int per_row) { return per_row >= 512 ? per_row : 512 / per_row * per_row; }
-
 template <typename T, typename W, int E, int TPR, int V>
 __global__ __launch_bounds__(grad_threads(TPR)) void norm_grad_kernel(const zero_norm_grad_args a, float* ws, int dim4) {
   constexpr int kThreads = grad_threads(TPR), kRows = kThreads / TPR;
@@ -1065,38 +1064,9 @@ void by_width(int64_t dim, const F& go) {
   else go(Int<1>());
 }
 
-// How a row of `vectors` 16-byte vectors is spread over threads: few vectors a
-// thread, so that many waves share the latency.
-NormShape norm_shape(int64_t vectors) {
-  static const NormShape shapes[] = {{16, 1}, {64, 1}, {64, 2}, {256, 1}, {256, 2}, {256, 4}, {1024, 2}, {1024, 4}};
-  for (const NormShape& s : shapes)
-    if (int64_t(s.threads) * s.vectors >= vectors) return s;
-  return {0, 0};
-}
-
-// The same for the gradient, whose two sums a column limit a thread to 8 elements, 16 for the longest rows.
-NormShape norm_grad_shape(int64_t dim, int per) {
-  const int64_t vectors = (dim + per - 1) / per;
-  static const int threads[] = {64, 128, 192, 256, 384, 512, 768, 1024};
-  if (vectors <= 16) return {16, 1};
-  if (per == 4)
-    for (int t : {64, 128, 192, 256, 320, 384, 512, 768})
-      if (t >= vectors) return {t, 1};
-  for (int t : threads)
-    if (int64_t(t) * (8 / per) >= vectors) return {t, 8 / per};
-  return vectors <= 2 * 1024 * (8 / per) ? NormShape{1024, 16 / per} : NormShape{0, 0};
-}
-
 }  // namespace
 
 namespace zero {
-
-int64_t norm_grad_blocks(int64_t n, int64_t dim) {
-  const NormShape s = norm_grad_shape(dim, 8);
-  const int64_t rows = s.threads == 0 ? 16 : grad_threads(s.threads) / s.threads;
-  const int64_t groups = (n + rows - 1) / rows;
-  return std::max<int64_t>(1, std::min<int64_t>(groups, std::min<int64_t>(512, std::max<int64_t>(256, groups / 2))));
-}
 
 int launch_embedding(const void* tokens, bool wide, int64_t n, const void* table, int32_t table_type, int64_t rows,
                      int64_t dim, float scale, void* out, int32_t out_type, int64_t out_stride, hipStream_t stream,
@@ -1256,23 +1226,18 @@ int launch_norm_grad(const zero_norm_grad_args& a, float* ws, hipStream_t stream
       return;
     }
     spread(Int<16>(), Int<1>());
-    spread(Int<64>(), Int<8 / E>());
+    spread(Int<64>(), Int<1>());
+    spread(Int<128>(), Int<1>());
+    spread(Int<192>(), Int<1>());
+    spread(Int<256>(), Int<1>());
+    spread(Int<384>(), Int<1>());
+    spread(Int<512>(), Int<1>());
+    spread(Int<768>(), Int<1>());
     if constexpr (E == 4) {
-      spread(Int<64>(), Int<1>());
-      spread(Int<128>(), Int<1>());
-      spread(Int<192>(), Int<1>());
-      spread(Int<256>(), Int<1>());
       spread(Int<320>(), Int<1>());
-      spread(Int<384>(), Int<1>());
-      spread(Int<512>(), Int<1>());
-      spread(Int<768>(), Int<1>());
+      spread(Int<512>(), Int<2>());
+      spread(Int<768>(), Int<2>());
     }
-    spread(Int<128>(), Int<8 / E>());
-    spread(Int<192>(), Int<8 / E>());
-    spread(Int<256>(), Int<8 / E>());
-    spread(Int<384>(), Int<8 / E>());
-    spread(Int<512>(), Int<8 / E>());
-    spread(Int<768>(), Int<8 / E>());
     spread(Int<1024>(), Int<8 / E>());
     spread(Int<1024>(), Int<16 / E>());
     if (s.threads != 0) return;

@@ -13,8 +13,12 @@
 namespace zero {
 
 // Sorted tokens that one wave of the table's gradient sums (a multiple of 8), and
-// a workspace's rows: two sums for each such piece.
-inline int embedding_piece(int64_t n) { return n <= 4096 ? 8 : 16; }
+// a workspace's rows: two sums for each such piece. Short pieces, so that a few
+// tokens are many waves (512 tokens, 1600 wide: 13 us of a call with 8, 17 with 16),
+// until the sums cost more than that (32768 tokens, 8192 wide, an eighth of the
+// table: 67 us with 8, 59 with 16, 61 with 32).
+constexpr int64_t kShortPieces = 4096;
+inline int embedding_piece(int64_t n) { return n <= kShortPieces ? 8 : 16; }
 inline int64_t embedding_pieces(int64_t n) { return (n + embedding_piece(n) - 1) / embedding_piece(n); }
 
 // Tokens that one block of the sort takes, and the bits of one of its passes.
@@ -50,15 +54,49 @@ inline int row_bits(int64_t rows) {
   return b;
 }
 
-// How a norm's row is spread: threads that share it, and the 16-byte vectors
-// that each takes; vectors 0: a row too long for the registers.
+// How a norm's row of 16-byte vectors is spread: the threads that share it, and
+// the vectors that each takes, few of them, so that many waves share the latency
+// (8 rows of 1600 bf16: 3.6 us with 256 threads, 6.0 with a wave a row). threads 0:
+// a row too long for the registers.
 struct NormShape {
   int threads, vectors;
 };
 
+inline NormShape norm_shape(int64_t vectors) {
+  static const NormShape shapes[] = {{16, 1}, {64, 1}, {64, 2}, {256, 1}, {256, 2}, {256, 4}, {1024, 2}, {1024, 4}};
+  for (const NormShape& s : shapes)
+    if (int64_t(s.threads) * s.vectors >= vectors) return s;
+  return {0, 0};
+}
+
+// The same for the gradient, rows of `dim` elements, `per` of them a vector. Its two
+// sums a column take 16 registers for a vector of bf16, so a thread takes one, or
+// one of fp32 (5003 rows of 1111: 20 us of a call, 21.4 with two) while 768 threads
+// suffice and two beyond; twice as many for the longest rows.
+inline NormShape norm_grad_shape(int64_t dim, int per) {
+  const int64_t vectors = (dim + per - 1) / per;
+  if (vectors <= 16) return {16, 1};
+  if (per == 4)
+    for (int t : {64, 128, 192, 256, 320, 384, 512, 768})
+      if (t >= vectors) return {t, 1};
+  for (int t : {64, 128, 192, 256, 384, 512, 768, 1024})
+    if (int64_t(t) * (8 / per) >= vectors) return {t, 8 / per};   // fp32: from 512 on
+  return vectors <= 2 * 1024 * (8 / per) ? NormShape{1024, 16 / per} : NormShape{0, 0};
+}
+
+// Threads of a block of the gradient: as many rows at a time as 512 threads take.
+constexpr int grad_threads(int per_row) { return per_row >= 512 ? per_row : 512 / per_row * per_row; }
+
 // Blocks of the norm's gradient, each of which leaves one row of partial sums of
-// d_weight and one of d_bias.
-int64_t norm_grad_blocks(int64_t n, int64_t dim);
+// d_weight and one of d_bias: two a CU where there are rows enough (16384 rows of
+// 2944 bf16: 74 us of a call with 512, 84 with 384 and 768, 95 with 256), and two
+// rows a block, or group of its threads, where they are few.
+inline int64_t norm_grad_blocks(int64_t n, int64_t dim) {
+  const NormShape s = norm_grad_shape(dim, 8);
+  const int64_t rows = s.threads == 0 ? 16 : grad_threads(s.threads) / s.threads;
+  const int64_t groups = (n + rows - 1) / rows;
+  return std::max<int64_t>(1, std::min<int64_t>(groups, std::min<int64_t>(512, std::max<int64_t>(256, groups / 2))));
+}
 
 // The launches of calls whose arguments have been checked.
 int launch_embedding(const void* tokens, bool wide, int64_t n, const void* table, int32_t table_type, int64_t rows,

@@ -36,6 +36,12 @@ padded buffers, every tensor is a view into them, and the shard is the rank's
 slice of each. The step then reads the gradient slice in place (no pack) and
 AdamW writes the bf16 parameters straight into the flat parameter buffer (no
 unpack): sum of squares -> clip + AdamW + bf16 cast.
+
+With ``tables`` (and accum_steps > 1) the gradients of token tables reach the
+accumulator by their tokens: each micro-batch gives the tokens and the gradient
+of the rows that were looked up, and zero_embedding_grad adds the rows that lie in
+this rank's part of the table; the dense gradient, zero but for the batch's
+tokens, is neither held nor packed nor accumulated.
 """
 
 from __future__ import annotations
@@ -44,7 +50,7 @@ import warnings
 
 import torch
 
-from . import synth, tensors, zero
+from . import layers, synth, tensors, zero
 
 
 def other_rank_slices(sizes, shard, rank):
@@ -68,7 +74,11 @@ class RankShard:
     def __init__(self, wl: synth.Workload, rank: int | None = None, device="cuda",
                  fill: bool = True, bucket: int | None = None, fused_norm: bool = True,
                  accum_steps: int = 1, flat: bool = False, fused_unpack: bool = True, streams: int = 2,
-                 state_arrays: bool = False):
+                 state_arrays: bool = False, tables=None):
+        """``tables``: the token tables by tensor index, each a dict of ``dim``
+        (elements of a row), ``tokens`` (the most that one micro-batch has) and
+        ``dense`` (default False; True for a table that has a dense gradient as
+        well, as one whose LM head shares it)."""
         self.wl = wl
         self.rank = wl.rank if rank is None else rank
         self.device = torch.device(device)
@@ -88,6 +98,14 @@ class RankShard:
         if state_arrays and (flat or accum_steps > 1):
             raise ValueError("three state arrays are used with the packed step without accumulation only")
         self.state_arrays = state_arrays
+        if tables and accum_steps < 2:
+            raise ValueError("token tables are accumulated in fp32: accum_steps > 1")
+        self.tables = {}
+        for i, t in (tables or {}).items():
+            if not 0 <= i < n_t or wl.sizes[i] % t["dim"]:
+                raise ValueError(f"tensor {i} is no table of rows of {t['dim']} elements")
+            self.tables[i] = {"dense": False, **t, "rows": wl.sizes[i] // t["dim"]}
+        by_tokens = [i for i, t in self.tables.items() if not t["dense"]]
         if flat:
             if accum_steps > 1:
                 raise ValueError("flat buffers are not combined with gradient accumulation here")
@@ -106,7 +124,8 @@ class RankShard:
             self.param_shard = self.param_flat[lo:lo + S]
         else:
             for i in self.touched:
-                self.grads[i] = torch.empty(wl.sizes[i], dtype=torch.bfloat16, device=dev)
+                if i not in by_tokens:
+                    self.grads[i] = torch.empty(wl.sizes[i], dtype=torch.bfloat16, device=dev)
                 self.params[i] = torch.full((wl.sizes[i],), synth.SENTINEL, dtype=torch.int16,
                                             device=dev).view(torch.bfloat16)
             self.grad_shard = torch.empty(S, dtype=torch.bfloat16, device=dev)
@@ -126,6 +145,20 @@ class RankShard:
         ws = max(max(zero.zero_sqnorm_workspace_bytes(n),
                      zero.zero_pack_sqnorm_workspace_bytes(self.layout, b, n)) for b, n in self.pieces())
         self.workspace = torch.empty((ws + 7) // 8, dtype=torch.float64, device=dev)
+        # the shard without the tables whose gradients come by tokens alone
+        self.dense_pieces = self.pieces()
+        for i, _, d, n in self.segments:
+            if i in by_tokens:
+                cuts = [((b, min(b + c, d) - b), (max(b, d + n), b + c - max(b, d + n))) for b, c in self.dense_pieces]
+                self.dense_pieces = [p for two in cuts for p in two if p[1] > 0]
+        for i, t in self.tables.items():
+            if i in self.touched:
+                order = layers.zero_token_order_bytes(t["tokens"], t["rows"])
+                ws = layers.zero_embedding_grad_workspace_bytes(t["tokens"], t["dim"])
+                t["order"] = torch.empty(order // 4, dtype=torch.int32, device=dev)
+                t["workspace"] = torch.empty(ws // 4, dtype=torch.float32, device=dev)
+                t["none"] = (torch.empty(0, dtype=torch.int32, device=dev),
+                             torch.empty(0, t["dim"], dtype=torch.bfloat16, device=dev))
         # buckets of the default step: each bucket's sum of squares in its own
         # slot, combined once (zero_sum_partials), and the buckets dealt out
         # to `streams` streams in turn
@@ -182,6 +215,8 @@ class RankShard:
 
     def fill_grads(self, step):
         for i in self.touched:
+            if self.grads[i] is None:       # a table whose gradient comes by tokens
+                continue
             synth.device_grad_(self.grads[i], self.wl, step, salt=i)
 
     def fill_other_ranks(self, step=None):
@@ -234,7 +269,9 @@ class RankShard:
         record costs GPU time between launches). A bucketed default step times
         each phase as a whole (its buckets overlap on several streams).
         ``before_micro(mb)`` runs before each micro-batch when accumulating (to
-        refill the gradients)."""
+        refill the gradients). With ``tables`` it returns their gradients, a dict by
+        tensor index of (tokens, d_out) or (tokens, d_out, scale), as
+        layers.zero_token_order and zero_embedding_grad take them."""
         hp = self.hparams(step)
         own = self.rank_sq[self.rank:self.rank + 1]
         pieces = self.pieces()
@@ -369,13 +406,14 @@ class RankShard:
 
     def _step_accumulated(self, hp, own, pieces, stream, mark, before_micro):
         for mb in range(self.accum_steps):
-            if before_micro is not None:
-                before_micro(mb)
-            for b, n in pieces:
+            by_tokens = before_micro(mb) if before_micro is not None else None
+            for b, n in self.dense_pieces:
                 mark("pack", lambda: zero.zero_pack_grads(self.layout, self.grad_ptrs, self.grad_shard, b, n,
                                                           stream))
                 mark("accumulate", lambda: zero.zero_accumulate_grads(self.grad_shard[b:], self.acc[b:], n,
                                                                       mb == 0, stream))
+            if self.tables:
+                mark("tables", lambda: self._accumulate_tables(by_tokens or {}, mb == 0, stream))
         for k, (b, n) in enumerate(pieces):
             mark("sqnorm", lambda: zero.zero_shard_sqnorm_f32(self.acc[b:], n, own, k > 0, self.workspace,
                                                               stream=stream))
@@ -390,6 +428,25 @@ class RankShard:
                 self.wl.n_d, stream))
             mark("unpack", lambda: zero.zero_unpack_params(self.layout, self.param_shard, self.param_ptrs,
                                                           b, n, stream))
+
+    def _accumulate_tables(self, by_tokens, first, stream):
+        """The micro-batch's table gradients into the accumulator: the rank's
+        part of each table, written by the first micro-batch where nothing dense
+        was. A table without an entry has no tokens."""
+        for i in by_tokens:
+            if i not in self.tables:
+                raise ValueError(f"tensor {i} is not among the rank's tables")
+        for i, t in self.tables.items():
+            if "order" not in t:            # no part of it in this shard
+                continue
+            tokens, d_out, *scale = by_tokens.get(i, t["none"])
+            if tokens.numel() > t["tokens"]:
+                raise ValueError(f"tensor {i}: {tokens.numel()} tokens, the rank's table takes {t['tokens']}")
+            layers.zero_token_order(tokens, t["rows"], t["order"], stream=stream)
+            for j, s, d, n in self.segments:
+                if j == i:
+                    layers.zero_embedding_grad(t["order"], t["rows"], d_out, self.acc[d:d + n], t["workspace"],
+                                               *scale, first=s, accumulate=t["dense"] or not first, stream=stream)
 
     def bytes_per_step(self):
         """Algorithmic HBM bytes of one step: pack 4, sum of squares 2 (0 when

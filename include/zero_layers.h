@@ -23,8 +23,9 @@
  * suits their element type. "Stride" is the distance of two rows in elements;
  * within a row the elements are consecutive. An output's rows do not overlap
  * (stride >= dim with more than one row); an input's may (stride 0: one row, used
- * for all). Workspaces: contents on entry do not matter, and calls that may run at
- * the same time need one each.
+ * for all). Workspaces: contents on entry do not matter, calls that may run at the
+ * same time need one each, and the bytes asked for do not fall as n grows, so one
+ * for the largest batch serves all.
  */
 #ifndef ZERO_LAYERS_MI355X_H
 #define ZERO_LAYERS_MI355X_H
