@@ -474,26 +474,15 @@ __device__ __forceinline__ uint64_t rows_without(const int32_t* row, int n, int 
   return __ballot(mine < r1 && !there);
 }
 
-constexpr int kFillRows = 4;   // rows that a wave looks for and clears
-constexpr int kBatch = 8;      // rows that a wave loads before it adds them
+constexpr int kFillRows = 4;       // rows that a wave looks for and clears
+constexpr int64_t kFewTokens = 96;
+constexpr int kBatch = 8;          // rows that a wave loads before it adds them
 
-template <typename T, typename G, int E, bool ADD>
-__global__ __launch_bounds__(256) void embedding_grad_kernel(const EmbeddingGradArgs a) {
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (!ADD && int(blockIdx.x) >= a.sum_blocks) {      // zeros for the rows without a token
-    const uint32_t w = (blockIdx.x - a.sum_blocks) * 4 + wave;
-    const int r0 = a.row_lo + int(w / uint32_t(a.tiles)) * kFillRows, r1 = min(r0 + kFillRows, a.row_hi);
-    if (r0 >= r1) return;
-    const Span s = span_of<E>(int(w % uint32_t(a.tiles)) * 64 + lane, a.dim);
-    for (uint64_t absent = rows_without(a.row, a.n, r0, r1); absent != 0; absent &= absent - 1)
-      write_grad<E, G>(a, r0 + __builtin_ctzll(absent), s, Words<E, G>{});
-    return;
-  }
-  const uint32_t w = blockIdx.x * 4 + wave;
-  const int piece = int(w / uint32_t(a.tiles));
-  if (piece >= a.pieces) return;
-  const Span s = span_of<E>(int(w % uint32_t(a.tiles)) * 64 + lane, a.dim);
-  const int i0 = piece * a.piece, i1 = min(i0 + a.piece, a.n);
+// The sums of the sorted tokens [i0, i1), a piece, at the lane's span: of a run that
+// lies in the piece to grad, of a run that goes on beyond it to put(1, sum), of one
+// that began before it to put(0, sum).
+template <typename T, typename G, int E, bool ADD, typename Put>
+__device__ __forceinline__ void sum_piece(const EmbeddingGradArgs& a, int i0, int i1, const Span& s, const Put& put) {
   // rows and positions by eights: the arrays go on that far behind their last entry
   i32x8 r8 = load8(a.row + i0), p8 = load8(a.pos + i0);
   const int prior = uniform_load(a.row + max(i0 - 1, 0)), r_last = uniform_load(a.row + i1 - 1);
@@ -531,10 +520,8 @@ __global__ __launch_bounds__(256) void embedding_grad_kernel(const EmbeddingGrad
       const bool end = r[k] != r[k + 1];
       if (!end && i + k + 1 < i1) continue;
       if (r[k] >= a.row_lo && r[k] < a.row_hi) {
-        if (head || !end)
-          store_row<E, false>(a.ws + (int64_t(piece) * 2 + (head ? 0 : 1)) * a.dim4, s, narrow<E, float>(sum));
-        else
-          write_sum<E, G, ADD>(a, r[k], s, old[ADD ? k : 0], sum);
+        if (head || !end) put(head ? 0 : 1, sum);
+        else write_sum<E, G, ADD>(a, r[k], s, old[ADD ? k : 0], sum);
       }
       head = false;
 #pragma unroll
@@ -543,40 +530,166 @@ __global__ __launch_bounds__(256) void embedding_grad_kernel(const EmbeddingGrad
   }
 }
 
-template <typename G, int E, bool ADD>
-__global__ __launch_bounds__(256) void embedding_join_kernel(const EmbeddingGradArgs a) {
+// Of the run that begins in the piece and goes on beyond it: its row, in *r, and how
+// many pieces more it reaches; 0 where there is none, or none in the part.
+__device__ __forceinline__ int pieces_beyond(const EmbeddingGradArgs& a, int piece, int* r) {
+  const int i0 = piece * a.piece, i1 = i0 + a.piece;
+  if (i1 >= a.n) return 0;
+  *r = uniform_load(a.row + i1);
+  const int end = uniform_load(a.row + i1 - 1), begin = uniform_load(a.row + i0),
+            prior = uniform_load(a.row + max(i0 - 1, 0));
+  if (end != *r || *r < a.row_lo || *r >= a.row_hi) return 0;
+  if (i0 > 0 && begin == *r && prior == *r) return 0;      // began earlier
+  // the pieces whose first token goes on with the run: 64 compared at a time
+  for (int more = 0;;) {
+    const int64_t i = int64_t(piece + 1 + more + int(threadIdx.x & 63)) * a.piece;
+    const uint64_t on = __ballot(i < a.n && a.row[i < a.n ? i : 0] == *r);
+    if (on != ~uint64_t(0)) return more + __builtin_ctzll(~on);
+    more += 64;
+  }
+}
+
+// sum += what the pieces [from, to) have left of a run that began before them, read
+// eight at a time.
+template <int E>
+__device__ __forceinline__ void add_pieces(const EmbeddingGradArgs& a, float (&sum)[E], int from, int to, const Span& s) {
+  constexpr int N = 8;
+  for (int j = from; j < to; j += N) {
+    Words<E, float> x[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      x[k] = load_row<E, false>(a.ws + int64_t(min(j + k, to - 1)) * 2 * a.dim4, s);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      float v[E];
+      widen<E, float>(x[k], v);
+#pragma unroll
+      for (int e = 0; e < E; ++e) sum[e] += j + k < to ? v[e] : 0.f;
+    }
+  }
+}
+
+template <int E, typename G>
+__device__ __forceinline__ void clear_rows(const EmbeddingGradArgs& a, uint32_t w, int lane) {
+  const int r0 = a.row_lo + int(w / uint32_t(a.tiles)) * kFillRows, r1 = min(r0 + kFillRows, a.row_hi);
+  if (r0 >= r1) return;
+  const Span s = span_of<E>(int(w % uint32_t(a.tiles)) * 64 + lane, a.dim);
+  for (uint64_t absent = rows_without(a.row, a.n, r0, r1); absent != 0; absent &= absent - 1)
+    write_grad<E, G>(a, r0 + __builtin_ctzll(absent), s, Words<E, G>{});
+}
+
+// Many tokens: a wave a piece and a tile of 64 vectors, its sums of shared runs in
+// the workspace for embedding_join_kernel. The blocks behind those write zeros.
+template <typename T, typename G, int E, bool ADD>
+__global__ __launch_bounds__(256) void embedding_grad_kernel(const EmbeddingGradArgs a) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (!ADD && int(blockIdx.x) >= a.sum_blocks) {
+    clear_rows<E, G>(a, (blockIdx.x - a.sum_blocks) * 4 + wave, lane);
+    return;
+  }
   const uint32_t w = blockIdx.x * 4 + wave;
   const int piece = int(w / uint32_t(a.tiles));
   if (piece >= a.pieces) return;
   const Span s = span_of<E>(int(w % uint32_t(a.tiles)) * 64 + lane, a.dim);
-  const int i0 = piece * a.piece, i1 = i0 + a.piece;
-  if (i1 >= a.n) return;
-  const int r = uniform_load(a.row + i1), end = uniform_load(a.row + i1 - 1), begin = uniform_load(a.row + i0),
-            prior = uniform_load(a.row + max(i0 - 1, 0));
-  if (end != r || r < a.row_lo || r >= a.row_hi) return;
-  if (i0 > 0 && begin == r && prior == r) return;      // began earlier
-  // the pieces whose first token goes on with the run: 64 compared at a time
-  int last = piece;
-  for (;;) {
-    const int64_t i = int64_t(last + 1 + lane) * a.piece;
-    const uint64_t on = __ballot(i < a.n && a.row[i < a.n ? i : 0] == r);
-    const int more = on == ~uint64_t(0) ? 64 : __builtin_ctzll(~on);
-    last += more;
-    if (more < 64) break;
+  const int i0 = piece * a.piece;
+  sum_piece<T, G, E, ADD>(a, i0, min(i0 + a.piece, a.n), s, [&](int which, const float (&sum)[E]) {
+    store_row<E, false>(a.ws + (int64_t(piece) * 2 + which) * a.dim4, s, narrow<E, float>(sum));
+  });
+}
+
+// The runs that several pieces share: a block for the one that begins in a piece and
+// four tiles, a wave a tile. A run over more than kAlone pieces (half of a batch on one
+// row, as one that is padded with a real token has it) is left to the blocks of its
+// first four pieces, which take one of the four tiles each, their waves a quarter of
+// the pieces. Four vectors of fp32 whatever the gradient's type: so many more waves.
+// (A block for four pieces instead of four tiles waits for the longest of their runs:
+// 10 us instead of 7 at 32768 tokens, 8192 wide.)
+constexpr int kJoinTiles = 4, kAlone = 64;
+
+template <typename G, int E, bool ADD>
+__global__ __launch_bounds__(64 * kJoinTiles) void embedding_join_kernel(const EmbeddingGradArgs a) {
+  __shared__ float part[kJoinTiles][64 * E];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t across = uint32_t(a.tiles + kJoinTiles - 1) / kJoinTiles;
+  const int piece = int(blockIdx.x / across), tile0 = int(blockIdx.x % across) * kJoinTiles;
+  // a run begins in the piece and goes on; or one that began at most three pieces before is a long one, as the
+  // token far behind tells. All of it read at once: most blocks have nothing to do.
+  const int64_t i0 = int64_t(piece) * a.piece, i1 = i0 + a.piece, far = i0 + int64_t(kAlone - kJoinTiles) * a.piece;
+  const int prior = uniform_load(a.row + max(i0 - 1, int64_t(0))), first = uniform_load(a.row + i0),
+            end = uniform_load(a.row + min(i1, int64_t(a.n)) - 1), next = uniform_load(a.row + min(i1, int64_t(a.n) - 1)),
+            distant = uniform_load(a.row + min(far, int64_t(a.n) - 1));
+  const bool earlier = piece > 0 && prior == first;
+  if (i1 >= a.n || end != next || next < a.row_lo || next >= a.row_hi) return;
+  if (earlier && first == next && (far >= a.n || prior != distant)) return;
+  int r = 0, begin = piece, more = 0;
+  if (!(earlier && first == next)) {
+    more = pieces_beyond(a, piece, &r);
+  } else {
+    for (int q = 1; q < kJoinTiles && q <= piece && more == 0; ++q) {
+      begin = piece - q;
+      more = pieces_beyond(a, begin, &r);
+      if (more < q) more = 0;         // a run that ends before this piece
+    }
+    if (more <= kAlone) return;
   }
-  const float* p = a.ws + int64_t(piece) * 2 * a.dim4;
+  if (more == 0) return;
+  const bool alone = more <= kAlone;
+  const int tile = tile0 + (alone ? wave : piece - begin);
+  if (tile >= a.tiles && !alone) return;
+  const bool there = tile < a.tiles && (alone || wave == 0);
+  const Span s = span_of<E>(min(tile, a.tiles - 1) * 64 + lane, a.dim);
+  Words<E, G> old{};
+  if constexpr (ADD) {
+    if (there) old = read_grad<E, G>(a, r, s);
+  }
   float sum[E];
-  widen<E, float>(load_row<E, false>(p + a.dim4, s), sum);
-#pragma unroll 8
-  for (int j = piece + 1; j <= last; ++j) {
-    float v[E];
-    widen<E, float>(load_row<E, false>(p + int64_t(j - piece) * 2 * a.dim4, s), v);
+  widen<E, float>(load_row<E, false>(a.ws + (int64_t(begin) * 2 + 1) * a.dim4, s), sum);
+  if (alone) {
+    add_pieces<E>(a, sum, begin + 1, begin + 1 + more, s);
+  } else {
+    const int each = (more + kJoinTiles - 1) / kJoinTiles;
+    float some[E] = {};
+    add_pieces<E>(a, some, begin + 1 + min(wave * each, more), begin + 1 + min((wave + 1) * each, more), s);
 #pragma unroll
-    for (int e = 0; e < E; ++e) sum[e] += v[e];
+    for (int e = 0; e < E; ++e) part[wave][e * 64 + lane] = some[e];
+    __syncthreads();
+    for (int k = 0; k < kJoinTiles; ++k)
+#pragma unroll
+      for (int e = 0; e < E; ++e) sum[e] += part[k][e * 64 + lane];
   }
+  if (there) write_sum<E, G, ADD>(a, r, s, old, sum);
+}
+
+constexpr int kWide = 16;
+
+// Few tokens: a block a tile, a wave a sixteenth of the tokens, and the sums of
+// shared runs in LDS: one launch instead of two.
+template <typename T, typename G, int E, bool ADD>
+__global__ __launch_bounds__(64 * kWide) void embedding_grad_few_kernel(const EmbeddingGradArgs a) {
+  __shared__ float part[kWide][2][64 * E];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (!ADD && int(blockIdx.x) >= a.sum_blocks) {
+    clear_rows<E, G>(a, (blockIdx.x - a.sum_blocks) * kWide + wave, lane);
+    return;
+  }
+  const Span s = span_of<E>(int(blockIdx.x) * 64 + lane, a.dim);
+  if (wave < a.pieces)
+    sum_piece<T, G, E, ADD>(a, wave * a.piece, min((wave + 1) * a.piece, a.n), s, [&](int which, const float (&sum)[E]) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) part[wave][which][e * 64 + lane] = sum[e];
+    });
+  __syncthreads();
+  int r = 0;
+  const int more = wave < a.pieces ? pieces_beyond(a, wave, &r) : 0;
+  if (more == 0) return;
   Words<E, G> old{};
   if constexpr (ADD) old = read_grad<E, G>(a, r, s);
+  float sum[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) sum[e] = part[wave][1][e * 64 + lane];
+  for (int j = 1; j <= more; ++j)
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum[e] += part[wave + j][0][e * 64 + lane];
   write_sum<E, G, ADD>(a, r, s, old, sum);
 }
 
@@ -797,6 +910,17 @@ __global__ __launch_bounds__(kLongThreads) void norm_long_kernel(const zero_norm
 
 // ---------------------------------------------------------- norm's gradient
 
+// A column's sum, written or added, to a vector of either type.
+__device__ __forceinline__ void put_sum(void* out, int32_t type, int col, float sum, int32_t add) {
+  if (type == ZERO_BF16) {
+    uint16_t* p = static_cast<uint16_t*>(out) + col;
+    *p = to_bf16(add ? bf16_lo(*p) + sum : sum);
+  } else {
+    float* p = static_cast<float*>(out) + col;
+    *p = add ? *p + sum : sum;
+  }
+}
+
 // A block takes every gridDim.x-th group of rows, TPR threads a row, and keeps the
 // sums of d_weight and d_bias over its rows in registers; the groups' sums meet in
 // LDS and go to the workspace, which norm_grad_join_kernel adds up.
@@ -910,6 +1034,38 @@ __global__ __launch_bounds__(grad_threads(TPR)) void norm_grad_kernel(const zero
     }
   }
   if (a.d_weight == nullptr && a.d_bias == nullptr) return;
+  if (gridDim.x == 1) {        // nothing to join: no workspace, no second launch
+    for (int which = 0; which < 2; ++which) {
+      void* out = which ? a.d_bias : a.d_weight;
+      if (out == nullptr) continue;
+      float sum[V][E];
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+#pragma unroll
+        for (int e = 0; e < E; ++e) sum[k][e] = which ? sum_b[k][e] : sum_w[k][e];
+      if constexpr (kRows > 1) {
+        // the other groups' sums to the first
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+#pragma unroll
+          for (int e = 0; e < E; ++e) lds[(group * V * E + k * E + e) * TPR + t] = sum[k][e];
+        __syncthreads();
+        if (group != 0) continue;
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            for (int g = 1; g < kRows; ++g) sum[k][e] += lds[(g * V * E + k * E + e) * TPR + t];
+      }
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (e >= s[k].lo) put_sum(out, a.grad_type, s[k].col + e, sum[k][e], a.accumulate);
+    }
+    return;
+  }
   float* out = ws + int64_t(blockIdx.x) * 2 * dim4;
   if constexpr (kRows == 1) {
 #pragma unroll
@@ -1021,11 +1177,10 @@ __global__ __launch_bounds__(256) void norm_grad_columns_kernel(const zero_norm_
 // 16th row of the workspace. blockIdx.y: d_weight, d_bias.
 constexpr int kJoinWaves = 16;
 
-template <typename G>
 __global__ __launch_bounds__(64 * kJoinWaves) void norm_grad_join_kernel(const float* __restrict__ ws, int blocks, int dim,
-                                                                         int dim4, G* d_weight, G* d_bias,
-                                                                         int accumulate) {
-  G* out = blockIdx.y == 0 ? d_weight : d_bias;
+                                                                         int dim4, void* d_weight, void* d_bias,
+                                                                         int32_t type, int32_t accumulate) {
+  void* out = blockIdx.y == 0 ? d_weight : d_bias;
   if (out == nullptr) return;
   __shared__ float part[kJoinWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -1040,11 +1195,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void norm_grad_join_kernel(const f
   s = 0.f;
 #pragma unroll
   for (int k = 0; k < kJoinWaves; ++k) s += part[k][lane];
-  if constexpr (sizeof(G) == 2) {
-    out[col] = to_bf16(accumulate ? __uint_as_float(uint32_t(out[col]) << 16) + s : s);
-  } else {
-    out[col] = accumulate ? out[col] + s : s;
-  }
+  put_sum(out, type, col, s, accumulate);
 }
 
 template <int N>
@@ -1151,26 +1302,36 @@ int launch_embedding_grad(const int32_t* order, int64_t n, int64_t rows, int64_t
   a.n = int32_t(n);
   a.dim = int32_t(dim);
   a.dim4 = int32_t((dim + 3) / 4 * 4);
-  a.piece = embedding_piece(n);
-  a.pieces = int32_t(embedding_pieces(n));
+  const bool few = n <= kFewTokens;
+  a.piece = few ? int32_t(std::max<int64_t>(1, (n + kWide - 1) / kWide)) : embedding_piece(n);
+  a.pieces = int32_t((n + a.piece - 1) / a.piece);
   a.row_lo = int32_t(first / dim);
   a.row_hi = int32_t((first + count + dim - 1) / dim);
   const auto go = [&](auto tv, auto gv) {
     using T = decltype(tv);
     using G = decltype(gv);
-    by_width<sizeof(T) == 2 && sizeof(G) == 2 ? 8 : 4>(dim, [&](auto ev) {
+    const auto with = [&](auto ev, auto add) {
       constexpr int E = decltype(ev)::value;
+      constexpr bool ADD = decltype(add)::value;
       a.tiles = int32_t((dim + 64 * E - 1) / (64 * E));
-      const int64_t sums = (int64_t(a.pieces) * a.tiles + 3) / 4;
+      const int waves = few ? kWide : 4;
+      const int64_t sums = few ? (n > 0 ? a.tiles : 0) : (int64_t(a.pieces) * a.tiles + 3) / 4;
+      const int64_t fills = (int64_t(a.row_hi - a.row_lo + kFillRows - 1) / kFillRows * a.tiles + waves - 1) / waves;
       a.sum_blocks = int32_t(sums);
-      const int64_t groups = (a.row_hi - a.row_lo + kFillRows - 1) / kFillRows;
-      const int64_t fills = accumulate ? 0 : (groups * a.tiles + 3) / 4;
-      const auto run = [&](auto add) {
-        constexpr bool ADD = decltype(add)::value;
-        if (sums + fills > 0) embedding_grad_kernel<T, G, E, ADD><<<dim3(uint32_t(sums + fills)), 256, 0, stream>>>(a);
-        if (a.pieces > 1) embedding_join_kernel<G, E, ADD><<<dim3(uint32_t(sums)), 256, 0, stream>>>(a);
-      };
-      accumulate ? run(std::true_type()) : run(std::false_type());
+      const dim3 grid(uint32_t(sums + (ADD ? 0 : fills)));
+      if (grid.x == 0) return;
+      if (few) {
+        embedding_grad_few_kernel<T, G, E, ADD><<<grid, 64 * kWide, 0, stream>>>(a);
+        return;
+      }
+      embedding_grad_kernel<T, G, E, ADD><<<grid, 256, 0, stream>>>(a);
+      constexpr int J = E == 1 ? 1 : 4;
+      a.tiles = int32_t((dim + 64 * J - 1) / (64 * J));
+      embedding_join_kernel<G, J, ADD>
+          <<<dim3(uint32_t(a.pieces * ((a.tiles + kJoinTiles - 1) / kJoinTiles))), 64 * kJoinTiles, 0, stream>>>(a);
+    };
+    by_width<sizeof(T) == 2 && sizeof(G) == 2 ? 8 : 4>(dim, [&](auto ev) {
+      accumulate ? with(ev, std::true_type()) : with(ev, std::false_type());
     });
   };
   by_types(out_type, grad_type, go);
@@ -1248,15 +1409,9 @@ int launch_norm_grad(const zero_norm_grad_args& a, float* ws, hipStream_t stream
       norm_grad_long_kernel<T, W><<<dim3(uint32_t(a.n)), kLongThreads, 0, stream>>>(a);
   };
   by_types(a.type, a.weight_type, go);
-  if (sums) {
-    const dim3 grid(uint32_t((dim + 63) / 64), 2);
-    if (a.grad_type == ZERO_BF16)
-      norm_grad_join_kernel<uint16_t><<<grid, 64 * kJoinWaves, 0, stream>>>(
-          ws, int(blocks), dim, dim4, static_cast<uint16_t*>(a.d_weight), static_cast<uint16_t*>(a.d_bias), a.accumulate);
-    else
-      norm_grad_join_kernel<float><<<grid, 64 * kJoinWaves, 0, stream>>>(
-          ws, int(blocks), dim, dim4, static_cast<float*>(a.d_weight), static_cast<float*>(a.d_bias), a.accumulate);
-  }
+  if (sums && (blocks > 1 || norm_grad_shape(a.dim, 8).threads == 0))
+    norm_grad_join_kernel<<<dim3(uint32_t((dim + 63) / 64), 2), 64 * kJoinWaves, 0, stream>>>(
+        ws, int(blocks), dim, dim4, a.d_weight, a.d_bias, a.grad_type, a.accumulate);
   return launched(who);
 }
 

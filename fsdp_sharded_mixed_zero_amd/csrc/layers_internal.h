@@ -95,6 +95,7 @@ inline int64_t norm_grad_blocks(int64_t n, int64_t dim) {
   const NormShape s = norm_grad_shape(dim, 8);
   const int64_t rows = s.threads == 0 ? 16 : grad_threads(s.threads) / s.threads;
   const int64_t groups = (n + rows - 1) / rows;
+  if (groups <= 2 && s.threads != 0) return 1;         // which then needs no second launch
   return std::max<int64_t>(1, std::min<int64_t>(groups, std::min<int64_t>(512, std::max<int64_t>(256, groups / 2))));
 }
 

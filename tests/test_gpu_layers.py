@@ -156,6 +156,29 @@ def test_embedding_grad_of_long_runs():
     assert torch.equal(grad, again)
 
 
+@pytest.mark.parametrize("runs", [[64] * 9, [63, 65, 64, 128, 1, 7, 500], [128, 256, 3, 125, 1000], [1, 127, 128, 384, 9], [2000],
+                                  [17, 4096, 15], [5, 20000, 200, 128, 1], [128] * 40, [8192 + 128 * 3 - 1, 1, 4000], [120, 5000, 8]])
+@pytest.mark.parametrize("dim", [5, 300, 1100])
+def test_embedding_grad_of_runs_at_the_pieces_borders(runs, dim):
+    """Runs that begin and end on, before and behind the borders of pieces and of groups of them, with whole numbers:
+    every sum is exact, in any order."""
+    rows = len(runs)
+    r = np.random.default_rng(sum(runs) + dim)
+    tokens = np.repeat(np.arange(rows), runs)
+    at = r.permutation(len(tokens))
+    d = r.integers(-4, 5, (len(tokens), dim)).astype(np.float32)
+    want = np.stack([d[tokens == k].sum(0) for k in range(rows)])
+    shuffled = torch.from_numpy(tokens[at]).to(DEV)
+    for grad_type in (F32, BF16):
+        d_out = torch.from_numpy(d[at]).to(DEV).to(BF16 if grad_type == F32 else F32)
+        grad = torch.full((rows, dim), 2.0, dtype=grad_type, device=DEV)
+        table_grad(shuffled, rows, d_out, grad)
+        exact = torch.from_numpy(want).to(DEV)
+        assert torch.equal(grad, exact.to(grad_type))
+        table_grad(shuffled, rows, d_out, grad, accumulate=True)
+        assert torch.equal(grad, (exact.to(grad_type).float() + exact).to(grad_type))
+
+
 def test_embedding_grad_keeps_infinities_and_nans_to_their_elements():
     n, rows, dim = 90, 12, 20
     tokens = C.draw_tokens(n, rows, 3, "distinct")
