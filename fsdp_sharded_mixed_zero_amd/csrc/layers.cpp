@@ -170,6 +170,8 @@ extern "C" int zero_embedding_grad(const void* order, int64_t n, int64_t rows, i
   if (first < 0 || count < 0 || first > total || count > total - first)
     return fail(ZERO_EINVAL, "%s: elements [%lld, +%lld) of a table of %lld", who, (long long)first, (long long)count,
                 (long long)total);
+  if (count > ZERO_LAYER_ELEMS)
+    return fail(ZERO_EINVAL, "%s: a part of %lld elements, more than 2^35", who, (long long)count);
   if (order == nullptr || workspace == nullptr) return fail(ZERO_EINVAL, "%s: NULL order or workspace", who);
   if ((uintptr_t(order) | uintptr_t(workspace)) & 15)
     return fail(ZERO_EINVAL, "%s: order or workspace is not 16-byte aligned", who);

@@ -30,7 +30,8 @@ constexpr int64_t kRankTokens = 12288;
 
 // The parts of an order, in 32-bit words from its start: the sorted tokens' rows,
 // `rows` for those outside the table, and positions; then scratch of the sort: rows
-// and positions between two passes, and per block its digits' counts.
+// and positions between two passes, and per block its digits' counts, and their
+// totals.
 struct Order {
   int64_t row, pos, row2, pos2, digits, words;
   int64_t blocks;
@@ -43,7 +44,7 @@ struct Order {
     row2 = pos + up(n) + 8;
     pos2 = row2 + scratch * up(n);
     digits = pos2 + scratch * up(n);
-    words = digits + scratch * blocks * kSortDigits;
+    words = digits + scratch * (blocks + 1) * kSortDigits;
   }
 };
 

@@ -41,7 +41,7 @@ extern "C" {
 #define ZERO_I64 3
 
 /* Limits of a call: tokens, rows of activations or of a table; elements of a row;
- * elements of all rows of activations together. */
+ * elements of all rows of activations, or of a part of a table's gradient. */
 #define ZERO_LAYER_ROWS 16777215
 #define ZERO_LAYER_DIM 1048576
 #define ZERO_LAYER_ELEMS 34359738368
@@ -86,8 +86,8 @@ int zero_token_order(const void* tokens, int32_t token_type, int64_t n, int64_t 
  * A row's terms are added in fp32 in ascending position, in pieces of consecutive
  * sorted tokens whose sums are then added in order.
  *   order       as zero_token_order has written it for the same n and rows
- *   d_out       [n, dim] with its stride, ZERO_BF16 or ZERO_F32; rows of tokens
- *               outside the table are not read
+ *   d_out       [n, dim] with its stride, ZERO_BF16 or ZERO_F32; what the rows of
+ *               tokens outside the table hold does not matter
  *   grad        the part's count elements, ZERO_BF16 or ZERO_F32
  *   workspace   at least zero_embedding_grad_workspace_bytes(n, dim) bytes,
  *               16-byte aligned

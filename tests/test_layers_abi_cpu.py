@@ -125,7 +125,7 @@ def grad_call(**over):
     (dict(out_type=I64), "element type"), (dict(grad_type=-1), "element type"), (dict(n=-1), "n ="),
     (dict(rows=1 << 24), "rows ="), (dict(dim=0), "dim ="), (dict(scale=float("inf")), "scale"),
     (dict(first=-1), "a table of 400"), (dict(count=-1), "a table of 400"), (dict(first=1), "a table of 400"),
-    (dict(first=401, count=0), "a table of 400"), (dict(first=1 << 62, count=1 << 62), "a table of 400"),
+    (dict(first=401, count=0), "a table of 400"), (dict(rows=1 << 22, dim=1 << 14, stride=1 << 14, count=(1 << 35) + 1), "2^35"), (dict(first=1 << 62, count=1 << 62), "a table of 400"),
     (dict(order=None), "NULL order"), (dict(ws=None), "NULL order or workspace"), (dict(ws=at(3) + 4), "16-byte"),
     (dict(order=at(0) + 4), "16-byte"), (dict(ws_bytes=16), "need"), (dict(d_out=None), "d_out is NULL"),
     (dict(grad=None), "grad is NULL"), (dict(grad=at(2) + 2), "misaligned"), (dict(d_out=at(1) + 1), "misaligned"),
