@@ -746,15 +746,17 @@ __device__ __forceinline__ float dpp_add(float x) {
 // lanes, then the rows and the halves of the wave by swaps.
 template <int LANES>
 __device__ __forceinline__ float lanes_sum(float x) {
-  static_assert(LANES == 16 || LANES == 64, "a row of lanes or the wave");
+  static_assert(LANES == 16 || LANES == 32 || LANES == 64, "a row of lanes, two, or the wave");
   x = dpp_add<0xB1>(x);       // quad_perm [1, 0, 3, 2]
   x = dpp_add<0x4E>(x);       // quad_perm [2, 3, 0, 1]
   x = dpp_add<0x141>(x);      // row_half_mirror
   x = dpp_add<0x140>(x);      // row_mirror
-  if constexpr (LANES == 64) {
-    auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  if constexpr (LANES >= 32) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
     x = __uint_as_float(p[0]) + __uint_as_float(p[1]);
-    p = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  }
+  if constexpr (LANES == 64) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
     x = __uint_as_float(p[0]) + __uint_as_float(p[1]);
   }
   return x;
@@ -1049,7 +1051,7 @@ __global__ __launch_bounds__(grad_threads(TPR)) void norm_grad_kernel(const zero
     }
   };
   // the next rows are on their way while these are summed
-  constexpr int kAhead = V * E > 8 ? 0 : V * E > 4 ? 1 : 2;
+  constexpr int kAhead = V * E > 4 ? 1 : 2;
   Row ring[kAhead + 1];
   int64_t row0 = int64_t(blockIdx.x) * kRows;
 #pragma unroll
@@ -1128,7 +1130,8 @@ __global__ __launch_bounds__(grad_threads(TPR)) void norm_grad_kernel(const zero
   }
 }
 
-// Rows longer than the registers: the rows' gradient in two passes over each.
+// Rows of more than 8192 elements, whose sums do not fit the registers: the rows'
+// gradient in two passes over each.
 template <typename T, typename W>
 __global__ __launch_bounds__(kLongThreads) void norm_grad_long_kernel(const zero_norm_grad_args a) {
   constexpr int E = 16 / int(sizeof(T));
@@ -1188,6 +1191,7 @@ __global__ __launch_bounds__(256) void norm_grad_columns_kernel(const zero_norm_
   const int dim = int(a.dim);
   const Span s = span_of<E>(int(blockIdx.x) * 256 + int(threadIdx.x), dim);
   float sum_w[E] = {}, sum_b[E] = {};
+#pragma unroll 4
   for (int64_t row = blockIdx.y; row < a.n; row += gridDim.y) {
     const float mean = a.rms ? 0.f : uniform_load(a.mean + row), rstd = uniform_load(a.rstd + row);
     float g[E], xh[E];
@@ -1376,7 +1380,7 @@ static int launch_norm_rows(const zero_norm_args& a, hipStream_t stream, const c
     using T = decltype(tv);
     using W = decltype(wv);
     constexpr int E = 16 / int(sizeof(T));
-    const NormShape s = norm_shape((a.dim + E - 1) / E);
+    const NormShape s = norm_shape(a.n, (a.dim + E - 1) / E);
     const uint32_t rows = s.threads == 0 || s.threads >= 256 ? 1u : 256u / uint32_t(s.threads);
     const dim3 grid{uint32_t((a.n + rows - 1) / rows)};
     const auto spread = [&](auto threads, auto vectors) {
@@ -1388,8 +1392,10 @@ static int launch_norm_rows(const zero_norm_args& a, hipStream_t stream, const c
       return;
     }
     spread(Int<16>(), Int<1>());
+    spread(Int<32>(), Int<1>());
     spread(Int<64>(), Int<1>());
     spread(Int<64>(), Int<2>());
+    spread(Int<64>(), Int<4>());
     spread(Int<256>(), Int<1>());
     spread(Int<256>(), Int<2>());
     spread(Int<256>(), Int<4>());
@@ -1444,6 +1450,7 @@ int launch_norm_grad(const zero_norm_grad_args& a, float* ws, hipStream_t stream
       return;
     }
     spread(Int<16>(), Int<1>());
+    spread(Int<32>(), Int<1>());
     spread(Int<64>(), Int<1>());
     spread(Int<128>(), Int<1>());
     spread(Int<192>(), Int<1>());
@@ -1457,7 +1464,6 @@ int launch_norm_grad(const zero_norm_grad_args& a, float* ws, hipStream_t stream
       spread(Int<768>(), Int<2>());
     }
     spread(Int<1024>(), Int<8 / E>());
-    spread(Int<1024>(), Int<16 / E>());
     if (s.threads != 0) return;
     if (sums)
       norm_grad_columns_kernel<T><<<dim3(uint32_t((dim + 256 * E - 1) / (256 * E)), uint32_t(blocks)), 256, 0, stream>>>(

@@ -56,15 +56,17 @@ inline int row_bits(int64_t rows) {
 }
 
 // How a norm's row of 16-byte vectors is spread: the threads that share it, and
-// the vectors that each takes, few of them, so that many waves share the latency
-// (8 rows of 1600 bf16: 3.6 us with 256 threads, 6.0 with a wave a row). threads 0:
-// a row too long for the registers.
+// the vectors that each takes; threads 0: a row too long for the registers. A wave
+// a row needs no barrier, up to four vectors a lane (16384 rows of 1600 bf16: 21 us,
+// 26 with 256 threads a row; rows of 2944: 38 us with six, 36 with 256 threads); few
+// rows take more threads each, for the latency (8 rows of 1600: 3.6 us instead of 6.0).
 struct NormShape {
   int threads, vectors;
 };
 
-inline NormShape norm_shape(int64_t vectors) {
-  static const NormShape shapes[] = {{16, 1}, {64, 1}, {64, 2}, {256, 1}, {256, 2}, {256, 4}, {1024, 2}, {1024, 4}};
+inline NormShape norm_shape(int64_t n, int64_t vectors) {
+  if (n >= 1024 && vectors > 128 && vectors <= 256) return {64, 4};
+  static const NormShape shapes[] = {{16, 1}, {32, 1}, {64, 1}, {64, 2}, {256, 1}, {256, 2}, {256, 4}, {1024, 2}, {1024, 4}};
   for (const NormShape& s : shapes)
     if (int64_t(s.threads) * s.vectors >= vectors) return s;
   return {0, 0};
@@ -73,16 +75,17 @@ inline NormShape norm_shape(int64_t vectors) {
 // The same for the gradient, rows of `dim` elements, `per` of them a vector. Its two
 // sums a column take 16 registers for a vector of bf16, so a thread takes one, or
 // one of fp32 (5003 rows of 1111: 20 us of a call, 21.4 with two) while 768 threads
-// suffice and two beyond; twice as many for the longest rows.
+// suffice and two beyond. Twice as many spill: rows of more than 8192 elements take
+// two kernels (4096 rows of 12000 bf16: 259 us in registers).
 inline NormShape norm_grad_shape(int64_t dim, int per) {
   const int64_t vectors = (dim + per - 1) / per;
-  if (vectors <= 16) return {16, 1};
+  if (vectors <= 32) return {vectors <= 16 ? 16 : 32, 1};
   if (per == 4)
     for (int t : {64, 128, 192, 256, 320, 384, 512, 768})
       if (t >= vectors) return {t, 1};
   for (int t : {64, 128, 192, 256, 384, 512, 768, 1024})
     if (int64_t(t) * (8 / per) >= vectors) return {t, 8 / per};   // fp32: from 512 on
-  return vectors <= 2 * 1024 * (8 / per) ? NormShape{1024, 16 / per} : NormShape{0, 0};
+  return {0, 0};
 }
 
 // Threads of a block of the gradient: as many rows at a time as 512 threads take.

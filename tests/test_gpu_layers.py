@@ -194,7 +194,7 @@ def test_embedding_grad_keeps_infinities_and_nans_to_their_elements():
 # -------------------------------------------------------------------- norm
 
 SHAPES = [(1, 1), (3, 2), (2, 7), (5, 64), (17, 100), (9, 129), (6, 512), (5, 777), (4, 1024), (3, 1600), (4, 2944),
-          (3, 4099), (2, 8192), (2, 12001), (2, 16385), (1, 20000), (2, 33000)]
+          (3, 4099), (2, 8192), (2, 12001), (2, 16385), (1, 20000), (2, 33000), (1025, 1301), (1100, 700)]
 
 
 def norm_case(n, dim, dtype, w_type, seed, offset=0.3):
@@ -278,7 +278,7 @@ def workspace(n, dim):
     return torch.full((layers.zero_norm_grad_workspace_bytes(n, dim) // 4,), float("nan"), device=DEV)
 
 
-@pytest.mark.parametrize("n,dim", SHAPES + [(700, 33), (300, 257), (1100, 1600), (600, 4099), (40, 17000)])
+@pytest.mark.parametrize("n,dim", SHAPES + [(700, 33), (300, 257), (600, 4099), (40, 17000)])
 @pytest.mark.parametrize("dtype,w_type,g_type", [(BF16, BF16, F32), (BF16, F32, BF16), (F32, BF16, BF16), (F32, F32, F32)])
 @pytest.mark.parametrize("rms", [False, True])
 def test_norm_grad(n, dim, dtype, w_type, g_type, rms):
