@@ -3,15 +3,24 @@
 //
 //   embedding_kernel         rows of a table, scaled
 //   order_rank_kernel        the sort of few tokens, by counting
-//   order_count_kernel, order_scatter_kernel
+//   order_count_kernel, order_scan_kernel, order_scatter_kernel
 //                            one pass of the sort of many tokens
 //   embedding_grad_kernel    sums of pieces of the sorted tokens, and zeros for
 //                            the rows without one
 //   embedding_join_kernel    the sums of runs that several pieces share
+//   embedding_grad_few_kernel  both in one launch
 //   norm_kernel, norm_long_kernel
 //                            the norm of rows in registers, and of longer ones
 //   norm_grad_kernel, norm_grad_long_kernel, norm_grad_columns_kernel,
 //   norm_grad_join_kernel    its gradient
+//
+// All of them do a few operations per byte, so long ones are bound by HBM (a copy of
+// 0.4 to 0.5 GB reaches 5.4 TB/s here, a fill 6.6) and short ones by their launches
+// (2.4 us of the GPU's time each at least, 3.2 us of the host's). What is read or
+// written once is not kept in the caches (cached stores: the norm of 16384 x 8192 97 us
+// instead of 94, its gradient over 16384 x 2944 79 instead of 75); weights, tokens and
+// partial sums are. Times are those of one MI355X: of a call among others, or of a
+// kernel where one is named.
 #include <type_traits>
 
 #include "layers_internal.h"
@@ -170,11 +179,15 @@ __device__ __forceinline__ int table_row(I token, int rows) {
   return token >= 0 && token < I(rows) ? int(token) : rows;
 }
 
-constexpr int kLookupRows = 4;      // rows of a wave: as many loads in flight
+// A wave takes a tile of 64 vectors of four rows: the rows are known to the whole wave
+// (scalar loads), and four loads are in flight. 16384 rows of 4096 fp32, to bf16: 41 us,
+// 5.2 TB/s of what has to move; bound by HBM.
+constexpr int kLookupRows = 4;
 
 template <typename I, typename T, typename O, int E>
-__global__ __launch_bounds__(256) void embedding_kernel(const I* __restrict__ tokens, int n, const T* __restrict__ table, int rows, int dim, int tiles,
-                                                        float scale, O* __restrict__ out, int64_t stride) {
+__global__ __launch_bounds__(256) void embedding_kernel(const I* __restrict__ tokens, int n, const T* __restrict__ table,
+                                                        int rows, int dim, int tiles, float scale, O* __restrict__ out,
+                                                        int64_t stride) {
   const uint32_t w = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t t0 = int64_t(w / uint32_t(tiles)) * kLookupRows;
   if (t0 >= n) return;
@@ -204,7 +217,10 @@ __global__ __launch_bounds__(256) void embedding_kernel(const I* __restrict__ to
 // are exact in fp32, where a comparison and its count are two instructions that
 // need no wait between them: the difference clamped to [0, 1], and the sum. A
 // block takes 32 tokens, two in each of 16 lanes; its 64 such groups take a part
-// of the tokens to compare with each, from LDS.
+// of the tokens to compare with each, from LDS. 512 tokens 3.9 us, 8192 8.5 us, bound by
+// the comparisons from some 4000 on (compared and counted as integers 12.4 us: each
+// comparison's mask takes two idle cycles to reach the count). Passes over digits take
+// 18 us at 12288 tokens, this 16.
 constexpr int kRankThreads = 1024, kRankParts = kRankThreads / 16, kRankEach = 32;
 static_assert(ZERO_LAYER_ROWS < 1 << 24, "rows and counts are exact in fp32");
 
@@ -267,7 +283,8 @@ __global__ __launch_bounds__(kRankThreads) void order_rank_kernel(const I* __res
 // Many tokens: passes over the row numbers' digits of up to 9 bits from the
 // lowest on, each of which keeps the order of equal digits. A pass counts the
 // digits of every block's 2048 tokens, then places every token behind those of
-// lower digits, those of earlier blocks and those before it in its block.
+// lower digits, those of earlier blocks and those before it in its block. Two passes
+// for up to 2^18 - 1 rows: 32768 tokens 19 us, four launches' latencies; 2^20 48 us.
 struct SortArgs {
   const void* in;          // tokens in the first pass, rows in later ones
   const int32_t* pos_in;   // of later ones
@@ -533,7 +550,8 @@ __device__ __forceinline__ void sum_piece(const EmbeddingGradArgs& a, int i0, in
     for (int k = 0; k <= kBatch; ++k) r[k] = i + k >= a.n ? -1 : k < kBatch ? r8[k % kBatch] : r9;
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const int p = i + k < i1 && r[k] >= a.row_lo && r[k] < a.row_hi ? p8[k] : 0;      // a row that is there
+      // a row that is there, also where the order is not one of these tokens
+      const uint32_t p = i + k < i1 && r[k] >= a.row_lo && r[k] < a.row_hi ? min(uint32_t(p8[k]), uint32_t(a.n - 1)) : 0u;
       x[k] = load_row<E>(static_cast<const T*>(a.d_out) + int64_t(p) * a.stride, s);
     }
     if constexpr (ADD) {
@@ -610,7 +628,13 @@ __device__ __forceinline__ void clear_rows(const EmbeddingGradArgs& a, uint32_t 
 }
 
 // Many tokens: a wave a piece and a tile of 64 vectors, its sums of shared runs in
-// the workspace for embedding_join_kernel. The blocks behind those write zeros.
+// the workspace for embedding_join_kernel; eight rows are on their way at a time, with
+// grad's old values where they are added to. So every wave has the same number of rows
+// to add, however the tokens are spread, and no atomics decide an order. The blocks
+// behind those write zeros, four rows and a tile a wave (the search for a token costs
+// one row a wave 140 us, and 16 rows a wave, farther apart than the memory likes, 82 us
+// instead of 73, for 8192 tokens of 50257 rows of 2944). That gradient in bf16 takes 53 us,
+// 6.2 TB/s; 32768 tokens added to 4000 fp32 rows of 8192 32 us, 4.5 TB/s.
 template <typename T, typename G, int E, bool ADD>
 __global__ __launch_bounds__(256) void embedding_grad_kernel(const EmbeddingGradArgs a) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -787,6 +811,10 @@ __device__ __forceinline__ void row_sum(float (&x)[K], float* lds, int turn) {
   }
 }
 
+// TPR threads a row, V vectors each: the row is read once and stays in registers, so
+// the squares are taken after the mean, and the weights are on their way with it.
+// 8192 rows of 2944 bf16 with the residual 36.5 us, 5.3 TB/s; 16384 of 8192 93 us, 5.8;
+// bound by HBM.
 template <typename T, typename W, int E, int TPR, int V>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(const zero_norm_args a) {
   constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
@@ -956,7 +984,11 @@ __device__ __forceinline__ void put_sum(void* out, int32_t type, int col, float 
 
 // A block takes every gridDim.x-th group of rows, TPR threads a row, and keeps the
 // sums of d_weight and d_bias over its rows in registers; the groups' sums meet in
-// LDS and go to the workspace, which norm_grad_join_kernel adds up.
+// LDS and go to the workspace, which norm_grad_join_kernel adds up. One vector a
+// thread: with two, or with a wave a row, the sums leave room for too few waves. The
+// next rows are read before this one's sums. 16384 rows of 2944 bf16 with the skip path
+// 68 us, 5.7 TB/s; bound by HBM. (Blocks of 1024 threads, two rows at a time that
+// wait for each other: 87 us.)
 template <typename T, typename W, int E, int TPR, int V>
 __global__ __launch_bounds__(grad_threads(TPR)) void norm_grad_kernel(const zero_norm_grad_args a, float* ws, int dim4) {
   constexpr int kThreads = grad_threads(TPR), kRows = kThreads / TPR;
