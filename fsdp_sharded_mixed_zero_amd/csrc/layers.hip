@@ -11,8 +11,9 @@
 //   embedding_grad_few_kernel  both in one launch
 //   norm_kernel, norm_long_kernel
 //                            the norm of rows in registers, and of longer ones
-//   norm_grad_kernel, norm_grad_long_kernel, norm_grad_columns_kernel,
-//   norm_grad_join_kernel    its gradient
+//   norm_grad_kernel, norm_grad_few_kernel, norm_grad_long_kernel,
+//   norm_grad_columns_kernel, norm_grad_join_kernel
+//                            its gradient
 //
 // All of them do a few operations per byte, so long ones are bound by HBM (a copy of
 // 0.4 to 0.5 GB reaches 5.4 TB/s here, a fill 6.6) and short ones by their launches
@@ -1099,38 +1100,6 @@ __global__ __launch_bounds__(grad_threads(TPR)) void norm_grad_kernel(const zero
     }
   }
   if (a.d_weight == nullptr && a.d_bias == nullptr) return;
-  if (gridDim.x == 1) {        // nothing to join: no workspace, no second launch
-    for (int which = 0; which < 2; ++which) {
-      void* out = which ? a.d_bias : a.d_weight;
-      if (out == nullptr) continue;
-      float sum[V][E];
-#pragma unroll
-      for (int k = 0; k < V; ++k)
-#pragma unroll
-        for (int e = 0; e < E; ++e) sum[k][e] = which ? sum_b[k][e] : sum_w[k][e];
-      if constexpr (kRows > 1) {
-        // the other groups' sums to the first
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < V; ++k)
-#pragma unroll
-          for (int e = 0; e < E; ++e) lds[(group * V * E + k * E + e) * TPR + t] = sum[k][e];
-        __syncthreads();
-        if (group != 0) continue;
-#pragma unroll
-        for (int k = 0; k < V; ++k)
-#pragma unroll
-          for (int e = 0; e < E; ++e)
-            for (int g = 1; g < kRows; ++g) sum[k][e] += lds[(g * V * E + k * E + e) * TPR + t];
-      }
-#pragma unroll
-      for (int k = 0; k < V; ++k)
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-          if (e >= s[k].lo) put_sum(out, a.grad_type, s[k].col + e, sum[k][e], a.accumulate);
-    }
-    return;
-  }
   float* out = ws + int64_t(blockIdx.x) * 2 * dim4;
   if constexpr (kRows == 1) {
 #pragma unroll
@@ -1159,6 +1128,111 @@ __global__ __launch_bounds__(grad_threads(TPR)) void norm_grad_kernel(const zero
         if (e >= at.lo) out[which * dim4 + at.col + e] = x;
       }
     }
+  }
+}
+
+// Few rows: the columns' sums need the rows' statistics, which are given, but not
+// their sums, so blocks of columns and blocks of rows go side by side in one launch,
+// and d_y and x are read twice. A block of columns takes a tile of 64 vectors, its 16
+// waves every sixteenth row each; a block of rows takes one. 64 rows of 768 bf16 7.2 us
+// (a launch and the binding), where two launches with a join of the blocks' sums took
+// 10.3; what bounds more rows is the latency of the columns' batches of 128 rows.
+constexpr int kFewThreads = 1024, kFewWaves = kFewThreads / 64, kFewBatch = 8;
+
+template <typename T, typename W, int E, int V>
+__global__ __launch_bounds__(kFewThreads) void norm_grad_few_kernel(const zero_norm_grad_args a, int col_blocks) {
+  __shared__ float lds[kFewWaves * 64 * E];
+  const int dim = int(a.dim), n = int(a.n), t = threadIdx.x, lane = t & 63;
+  if (int(blockIdx.x) < col_blocks) {
+    const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const Span s = span_of<E>(int(blockIdx.x) * 64 + lane, dim);
+    float sum_w[E] = {}, sum_b[E] = {};
+    for (int row0 = wave; row0 < n; row0 += kFewWaves * kFewBatch) {
+      Words<E, T> dy[kFewBatch], x[kFewBatch];
+      float mean[kFewBatch], rstd[kFewBatch];
+#pragma unroll
+      for (int k = 0; k < kFewBatch; ++k) {
+        const int64_t row = min(row0 + k * kFewWaves, n - 1);
+        dy[k] = load_row<E, false>(static_cast<const T*>(a.d_y) + row * a.d_y_stride, s);
+        x[k] = load_row<E, false>(static_cast<const T*>(a.x) + row * a.x_stride, s);
+        mean[k] = a.rms ? 0.f : uniform_load(a.mean + row);
+        rstd[k] = uniform_load(a.rstd + row);
+      }
+#pragma unroll
+      for (int k = 0; k < kFewBatch; ++k) {
+        if (row0 + k * kFewWaves < n) {
+          float g[E], xh[E];
+          widen<E, T>(dy[k], g);
+          widen<E, T>(x[k], xh);
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            sum_w[e] = fmaf(g[e], (xh[e] - mean[k]) * rstd[k], sum_w[e]);
+            sum_b[e] += g[e];
+          }
+        }
+      }
+    }
+    for (int which = 0; which < 2; ++which) {
+      void* out = which ? a.d_bias : a.d_weight;
+      if (out == nullptr) continue;
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < E; ++e) lds[(wave * E + e) * 64 + lane] = which ? sum_b[e] : sum_w[e];
+      __syncthreads();
+      if (t < 64 * E) {
+        float x = 0.f;
+#pragma unroll
+        for (int w = 0; w < kFewWaves; ++w) x += lds[w * E * 64 + t];
+        if (t / 64 >= s.lo) put_sum(out, a.grad_type, s.col + t / 64, x, a.accumulate);
+      }
+    }
+    return;
+  }
+  const int64_t row = int(blockIdx.x) - col_blocks;
+  const T* dy = static_cast<const T*>(a.d_y) + row * a.d_y_stride;
+  const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+  const T* d_total = a.d_total != nullptr ? static_cast<const T*>(a.d_total) + row * a.d_total_stride : nullptr;
+  Span s[V];
+  Words<E, T> dy_raw[V], x_raw[V], total[V];
+  Words<E, W> w_raw[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    s[k] = span_of<E>(t + k * kFewThreads, dim);
+    dy_raw[k] = load_row<E, false>(dy, s[k]);
+    x_raw[k] = load_row<E, false>(x, s[k]);
+    w_raw[k] = load_weight<E, W>(a.weight, s[k], 1.f);
+    if (d_total != nullptr) total[k] = load_row<E, false>(d_total, s[k]);
+  }
+  const float mean = a.rms ? 0.f : uniform_load(a.mean + row), rstd = uniform_load(a.rstd + row);
+  float g[V][E], xh[V][E], c[2] = {0.f, 0.f};
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    float w[E];
+    widen<E, T>(dy_raw[k], g[k]);
+    widen<E, T>(x_raw[k], xh[k]);
+    widen<E, W>(w_raw[k], w);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      g[k][e] *= w[e];
+      xh[k][e] = (xh[k][e] - mean) * rstd;
+      if (e >= s[k].lo) {
+        c[0] += g[k][e];
+        c[1] = fmaf(g[k][e], xh[k][e], c[1]);
+      }
+    }
+  }
+  row_sum<kFewThreads, 2>(c, lds, 0);
+  const float c0 = a.rms ? 0.f : c[0] / float(dim), c1 = c[1] / float(dim);
+  T* dx = static_cast<T*>(a.d_x) + row * a.d_x_stride;
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    float m[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) m[e] = 0.f;
+    if (d_total != nullptr) widen<E, T>(total[k], m);
+#pragma unroll
+    for (int e = 0; e < E; ++e) g[k][e] = fmaf(fmaf(-xh[k][e], c1, g[k][e] - c0), rstd, m[e]);
+    store_row<E>(dx, s[k], narrow<E, T>(g[k]));
   }
 }
 
@@ -1464,6 +1538,38 @@ int launch_norm(const zero_norm_args& whole, hipStream_t stream, const char* who
 }
 
 int launch_norm_grad(const zero_norm_grad_args& a, float* ws, hipStream_t stream, const char* who) {
+  if (a.n <= few_norm_rows(a.dim)) {
+    const auto few = [&](auto tv, auto wv) {
+      using T = decltype(tv);
+      using W = decltype(wv);
+      by_width<16 / int(sizeof(T))>(a.dim, [&](auto ev) {
+        constexpr int E = decltype(ev)::value;
+        const int cols = a.d_weight != nullptr || a.d_bias != nullptr ? int((a.dim + 64 * E - 1) / (64 * E)) : 0;
+        const int rows = a.d_x != nullptr ? int(a.n) : 0;
+        const auto run = [&](auto vectors) {
+          constexpr int V = decltype(vectors)::value;
+          const auto put = [&](int c, int r) {
+            if (c + r > 0) norm_grad_few_kernel<T, W, E, V><<<dim3(uint32_t(c + r)), kFewThreads, 0, stream>>>(a, c);
+          };
+          if (a.d_x == a.d_y || a.d_x == a.x) {      // the columns before the rows write over them
+            put(cols, 0);
+            put(0, rows);
+          } else {
+            put(cols, rows);
+          }
+        };
+        if constexpr (E == 4) {
+          if (a.dim > kFewThreads * E) {
+            run(Int<2>());
+            return;
+          }
+        }
+        run(Int<1>());
+      });
+    };
+    by_types(a.type, a.weight_type, few);
+    return launched(who);
+  }
   const int64_t blocks = norm_grad_blocks(a.n, a.dim);
   const int dim = int(a.dim), dim4 = (dim + 3) / 4 * 4;
   const bool sums = a.d_weight != nullptr || a.d_bias != nullptr;
@@ -1504,7 +1610,7 @@ int launch_norm_grad(const zero_norm_grad_args& a, float* ws, hipStream_t stream
       norm_grad_long_kernel<T, W><<<dim3(uint32_t(a.n)), kLongThreads, 0, stream>>>(a);
   };
   by_types(a.type, a.weight_type, go);
-  if (sums && (blocks > 1 || norm_grad_shape(a.dim, 8).threads == 0))
+  if (sums)
     norm_grad_join_kernel<<<dim3(uint32_t((dim + 63) / 64), 2), 64 * kJoinWaves, 0, stream>>>(
         ws, int(blocks), dim, dim4, a.d_weight, a.d_bias, a.grad_type, a.accumulate);
   return launched(who);

@@ -88,6 +88,12 @@ inline NormShape norm_grad_shape(int64_t dim, int per) {
   return {0, 0};
 }
 
+// Up to this many rows the gradient takes one launch, in which the columns read every
+// row again. Against two launches, us: 256 rows of 768 bf16 8.2 and 10.4, 384 10.4 and
+// 10.3, 512 13.4 and 9.9; 384 rows of 8192 bf16 13.9 and 17.0, 512 16.9 and 19.3, 1024
+// 30.5 and 30.8. Rows of more than 8192 elements have kernels of their own.
+inline int64_t few_norm_rows(int64_t dim) { return dim > 8192 ? -1 : dim > 4096 ? 512 : 256; }
+
 // Threads of a block of the gradient: as many rows at a time as 512 threads take.
 constexpr int grad_threads(int per_row) { return per_row >= 512 ? per_row : 512 / per_row * per_row; }
 
@@ -99,7 +105,6 @@ inline int64_t norm_grad_blocks(int64_t n, int64_t dim) {
   const NormShape s = norm_grad_shape(dim, 8);
   const int64_t rows = s.threads == 0 ? 16 : grad_threads(s.threads) / s.threads;
   const int64_t groups = (n + rows - 1) / rows;
-  if (groups <= 2 && s.threads != 0) return 1;         // which then needs no second launch
   return std::max<int64_t>(1, std::min<int64_t>(groups, std::min<int64_t>(512, std::max<int64_t>(256, groups / 2))));
 }
 

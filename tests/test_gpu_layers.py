@@ -302,6 +302,27 @@ def test_norm_grad(n, dim, dtype, w_type, g_type, rms):
         assert torch.isnan(whole[:, dim:]).all()
 
 
+@pytest.mark.parametrize("dim", [1, 3, 7, 8, 20, 100, 200, 400, 777, 1100, 1600, 2100, 2944, 3500, 4096, 4097, 5500, 8192])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_norm_grad_at_the_row_counts_where_kernels_change(dim, dtype):
+    """The last number of rows that one launch takes, the next one, and d_x over x there."""
+    last = 512 if dim > 4096 else 256
+    for n in (last, last + 1):
+        gen, x, w, _ = norm_case(n, dim, dtype, dtype, n + dim)
+        d_y, d_total = normal(gen, n, dim, dtype=dtype), normal(gen, n, dim, dtype=dtype)
+        _, mean, rstd = (torch.from_numpy(v).float().to(DEV) for v in O.norm(C.np64(x)))
+        d_x, d_w, d_b = torch.empty_like(x), torch.empty(dim, device=DEV), torch.empty(dim, device=DEV)
+        layers.zero_norm_grad(d_y, x, mean, rstd, d_x, workspace(n, dim), weight=w, d_weight=d_w, d_bias=d_b,
+                              d_total=d_total)
+        want, bound = C.norm_grad_want(d_y, x, mean, rstd, w, d_total, False, dtype)
+        close(d_x, want[0], bound[0], "d_x")
+        for got, v, e, what in zip((d_w, d_b), want[1:], bound[1:], ("d_weight", "d_bias")):
+            close(got, v, stored(e, v, F32), what)
+        one = torch.empty_like(d_w)
+        layers.zero_norm_grad(d_y, x, mean, rstd, x, workspace(n, dim), weight=w, d_weight=one, d_total=d_total)
+        assert torch.equal(x, d_x) and torch.equal(one, d_w)
+
+
 @pytest.mark.parametrize("dim", [50, 1000, 6000, 18000])
 def test_norm_grad_in_part_and_in_place(dim):
     """One output at a time, and d_x over each of its inputs, give the same bits."""
