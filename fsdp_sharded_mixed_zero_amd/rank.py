@@ -102,7 +102,7 @@ class RankShard:
             raise ValueError("token tables are accumulated in fp32: accum_steps > 1")
         self.tables = {}
         for i, t in (tables or {}).items():
-            if not 0 <= i < n_t or wl.sizes[i] % t["dim"]:
+            if not 0 <= i < n_t or t["dim"] < 1 or wl.sizes[i] % t["dim"]:
                 raise ValueError(f"tensor {i} is no table of rows of {t['dim']} elements")
             self.tables[i] = {"dense": False, **t, "rows": wl.sizes[i] // t["dim"]}
         by_tokens = [i for i, t in self.tables.items() if not t["dense"]]
@@ -442,6 +442,9 @@ class RankShard:
             tokens, d_out, *scale = by_tokens.get(i, t["none"])
             if tokens.numel() > t["tokens"]:
                 raise ValueError(f"tensor {i}: {tokens.numel()} tokens, the rank's table takes {t['tokens']}")
+            if d_out.shape != (tokens.numel(), t["dim"]):
+                raise ValueError(f"tensor {i}: the gradient of {tokens.numel()} rows of {t['dim']} elements expected, "
+                                 f"got {tuple(d_out.shape)}")
             layers.zero_token_order(tokens, t["rows"], t["order"], stream=stream)
             for j, s, d, n in self.segments:
                 if j == i:
@@ -456,15 +459,19 @@ class RankShard:
         fp32 norm (4) and AdamW on fp32 gradients (30). Flat buffers: the sum
         of squares (2) and AdamW (28) only. With the unpack fused into AdamW,
         AdamW also writes 2 bytes per real element to the tensors and there is
-        no unpack pass."""
+        no unpack pass. Tables whose gradients come by tokens are not packed or
+        accumulated; what their gradients move depends on the tokens and is not
+        counted."""
         if self.flat:
             return {"sqnorm": 2 * self.shard, "adamw": 28 * self.shard}
         pad = self.shard - self.real
         pack = 4 * self.real + 2 * pad
         if self.accum_steps > 1:
             K, S = self.accum_steps, self.shard
+            dense = sum(n for _, n in self.dense_pieces)
+            pack -= 4 * (S - dense)
             # accumulate: 2 + 4 bytes for the first micro-batch, 2 + 4 + 4 after
-            out = {"pack": K * pack, "accumulate": 6 * S + (K - 1) * 10 * S, "sqnorm": 4 * S,
+            out = {"pack": K * pack, "accumulate": 6 * dense + (K - 1) * 10 * dense, "sqnorm": 4 * S,
                    "adamw": 30 * S}
         else:
             out = {"adamw": 28 * self.shard}

@@ -18,6 +18,7 @@ Modules
 ``memory``  per-rank byte and communication accounting of ZeRO stages 0-3.
 ``bf16``    fp32 <-> bfloat16 conversion with round-to-nearest-even.
 ``step``    pack, sum of squares, clip coefficient, AdamW, bf16 cast, unpack.
+``layers``  token tables and norms, forward and backward.
 
 Pins
 ----

@@ -113,6 +113,8 @@ def test_tables_that_do_not_fit_are_refused():
     with pytest.raises(ValueError, match="no table"):
         RankShard(wl, accum_steps=2, tables={0: {"dim": 7, "tokens": 4}})
     with pytest.raises(ValueError, match="no table"):
+        RankShard(wl, accum_steps=2, tables={0: {"dim": 0, "tokens": 4}})
+    with pytest.raises(ValueError, match="no table"):
         RankShard(wl, accum_steps=2, tables={9: {"dim": DIM, "tokens": 4}})
     rs = RankShard(wl, accum_steps=2, tables={0: {"dim": DIM, "tokens": 4}})
     five = (torch.zeros(5, dtype=torch.int32, device=DEV), torch.zeros(5, DIM, device=DEV))
@@ -120,6 +122,26 @@ def test_tables_that_do_not_fit_are_refused():
         rs.step(1, before_micro=lambda mb: {0: five})
     with pytest.raises(ValueError, match="not among"):
         rs.step(1, before_micro=lambda mb: {1: five})
+
+
+@pytest.mark.parametrize("tokens,shape", [(3, (4, DIM)), (4, (3, DIM)), (4, (4, DIM - 1)), (4, (2, 2 * DIM)), (4, (4 * DIM,))])
+def test_a_table_gradient_of_another_shape_is_refused(tokens, shape):
+    """Also where the rank's part would fit the other shape."""
+    rs = RankShard(workload(4, 0), accum_steps=2, tables={0: {"dim": DIM, "tokens": 8}})
+    given = (torch.zeros(tokens, dtype=torch.int32, device=DEV), torch.zeros(*shape, device=DEV))
+    with pytest.raises(ValueError, match="rows of"):
+        rs.step(1, before_micro=lambda mb: {0: given})
+
+
+def test_bytes_of_a_step_leave_a_table_out():
+    wl = workload(1, 0)
+    without = RankShard(wl, accum_steps=MICRO).bytes_per_step()
+    dense, by_tokens = (RankShard(wl, accum_steps=MICRO, tables={0: {"dim": DIM, "tokens": 4, "dense": d}}).bytes_per_step()
+                        for d in (True, False))
+    assert dense == without
+    table = SIZES[0]
+    assert by_tokens == {**without, "pack": without["pack"] - MICRO * 4 * table,
+                         "accumulate": without["accumulate"] - (6 + 10 * (MICRO - 1)) * table}
 
 
 class Pass:
