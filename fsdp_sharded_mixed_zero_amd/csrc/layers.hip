@@ -3,6 +3,7 @@
 //
 //   embedding_kernel         rows of a table, scaled
 //   order_rank_kernel        the sort of few tokens, by counting
+//   order_split_kernel       of some thousand, a range of rows a block
 //   order_count_kernel, order_scan_kernel, order_scatter_kernel
 //                            one pass of the sort of many tokens
 //   embedding_grad_kernel    sums of pieces of the sorted tokens, and zeros for
@@ -221,7 +222,8 @@ __global__ __launch_bounds__(256) void embedding_kernel(const I* __restrict__ to
 // of the tokens to compare with each, from LDS. 512 tokens 3.9 us, 8192 8.5 us, bound by
 // the comparisons from some 4000 on (compared and counted as integers 12.4 us: each
 // comparison's mask takes two idle cycles to reach the count). Passes over digits take
-// 18 us at 12288 tokens, this 16.
+// 18 us at 12288 tokens, this 16; beyond 4096 only tables too long for
+// order_split_kernel come here.
 constexpr int kRankThreads = 1024, kRankParts = kRankThreads / 16, kRankEach = 32;
 static_assert(ZERO_LAYER_ROWS < 1 << 24, "rows and counts are exact in fp32");
 
@@ -278,6 +280,140 @@ __global__ __launch_bounds__(kRankThreads) void order_rank_kernel(const I* __res
     for (int k = 0; k < kRankThreads / 64; ++k) at += part[k][t];
     row[int(at)] = int(key[i0 + t]);
     pos[int(at)] = i0 + t;
+  }
+}
+
+// Some thousand tokens: each of up to 256 blocks takes `each` consecutive rows, reads all
+// tokens and keeps those of its rows; they go behind the tokens of lower rows, which it
+// counts. One launch, and no counts between blocks. A wave's tokens are consecutive: it
+// lists those that are kept, ranks them 64 at a time among those of their row (lanes
+// with the same bits), and the block sorts them in LDS and stores them in order.
+// us for 50257 rows, and where one block has all tokens (150 rows): 6000 tokens 5.9 and
+// 8.9, 8192 6.3 and 10.3, 12288 8.2 and 15.4, 16384 9.2 and 18.1; by counting 4096 5.6,
+// 8192 8.5, 12288 16; in passes 16384 18. Bound by the reading and listing of all tokens
+// by every block. 32768 tokens 16.3 and 36.4, in passes 19.5: left to these. Rows beyond
+// 512 a block go the other ways. Stored unsorted, 16384 tokens of one block took 28.
+constexpr int64_t kSplitFrom = 4096, kSplitTokens = 16384;
+constexpr int kSplitThreads = 1024, kSplitWaves = kSplitThreads / 64, kSplitBlocks = 256, kSplitEach = 512;
+static_assert(kSplitEach <= 1 << 16 && kSplitTokens <= 1 << 16, "16 bits each in a list's entry");
+
+// The lower 32 bits of a token, all ones where it has more: larger than any row, as a
+// negative one is.
+__device__ __forceinline__ uint32_t low_word(int32_t token) { return uint32_t(token); }
+__device__ __forceinline__ uint32_t low_word(int64_t token) {
+  return uint32_t(uint64_t(token) >> 32) == 0 ? uint32_t(token) : ~0u;
+}
+
+template <typename I, int N>
+__global__ __launch_bounds__(kSplitThreads) void order_split_kernel(const I* __restrict__ tokens, int n, int rows, int each,
+                                                                    int bits, int32_t* __restrict__ row_out,
+                                                                    int32_t* __restrict__ pos_out) {
+  __shared__ uint32_t list[kSplitWaves][64 * N];         // the wave's tokens that are the block's: position and row - lo
+  __shared__ uint32_t seen[kSplitWaves][kSplitEach / 2]; // how many of a row, two in a word; then where they begin
+  __shared__ int32_t lower_sum[kSplitWaves], wave_sum[kSplitWaves];
+  const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int lo = int(blockIdx.x) * each, first = wave * 64 * N;
+  I x[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) x[k] = tokens[min(first + k * 64 + lane, n - 1)];
+  for (int k = t; k < kSplitWaves * kSplitEach / 2; k += kSplitThreads) (&seen[0][0])[k] = 0;
+  int lower = 0, mine = 0;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const int left = min(max(n - first - k * 64, 0), 64);
+    const uint64_t valid = left == 0 ? 0 : ~uint64_t(0) >> (64 - left);
+    const uint32_t r = min(low_word(x[k]), uint32_t(rows)), key = r - uint32_t(lo);
+    lower += __popcll(__ballot(r < uint32_t(lo)) & valid);
+    const uint64_t there = __ballot(key < uint32_t(each)) & valid;
+    if (there == 0) continue;
+    if ((there >> lane) & 1)
+      list[wave][mine + __popcll(there & ((uint64_t(1) << lane) - 1))] = key << 16 | uint32_t(first + k * 64 + lane);
+    mine += __popcll(there);
+  }
+  if (lane == 0) lower_sum[wave] = lower;
+  __syncthreads();
+  uint32_t at[N];
+  constexpr int kAtOnce = 2;
+#pragma unroll
+  for (int k0 = 0; k0 < N; k0 += kAtOnce) {
+    if (k0 * 64 >= mine) continue;
+    uint32_t d[kAtOnce], like[kAtOnce][2];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int i = (k0 + k) * 64 + lane;
+      d[k] = list[wave][min(i, mine - 1)] >> 16;
+      const uint64_t there = __ballot(i < mine);
+      like[k][0] = uint32_t(there);
+      like[k][1] = uint32_t(there >> 32);
+    }
+    for (int b = 0; b < bits; ++b) {
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const uint32_t bit = -(d[k] >> b & 1);           // of all lanes those with the same one
+        const uint64_t m = __ballot(bit != 0);
+        like[k][0] &= ~(uint32_t(m) ^ bit);
+        like[k][1] &= ~(uint32_t(m >> 32) ^ bit);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const uint32_t before = __builtin_amdgcn_mbcnt_hi(like[k][1], __builtin_amdgcn_mbcnt_lo(like[k][0], 0));
+      // a wave's accesses to LDS are in order: what is read are the tokens of the earlier steps
+      at[k0 + k] = (seen[wave][d[k] / 2] >> (d[k] % 2 * 16) & 0xffff) + before;
+      __builtin_amdgcn_wave_barrier();
+      if (before == 0 && (k0 + k) * 64 + lane < mine)
+        atomicAdd(&seen[wave][d[k] / 2], uint32_t(__popc(like[k][0]) + __popc(like[k][1])) << (d[k] % 2 * 16));
+      __builtin_amdgcn_wave_barrier();
+    }
+  }
+  __syncthreads();
+  // a row a thread
+  using Half = uint16_t __attribute__((may_alias));
+  const auto half = [&](int w, uint32_t d) -> Half& { return reinterpret_cast<Half*>(seen[w])[d]; };
+  int total = 0;
+  if (t < each)
+#pragma unroll
+    for (int w = 0; w < kSplitWaves; ++w) total += half(w, t);
+  int up = total;
+  for (int off = 1; off < 64; off <<= 1) {
+    const int y = __shfl_up(up, off, 64);
+    if (lane >= off) up += y;
+  }
+  if (lane == 63) wave_sum[wave] = up;
+  __syncthreads();
+  int below = 0;
+#pragma unroll
+  for (int w = 0; w < kSplitWaves; ++w) below += lower_sum[w];
+  if (t < each) {
+    int begin = up - total;
+    for (int w = 0; w < wave; ++w) begin += wave_sum[w];
+#pragma unroll
+    for (int w = 0; w < kSplitWaves; ++w) {
+      const int c = half(w, t);
+      half(w, t) = uint16_t(begin);
+      begin += c;
+    }
+  }
+  int count = 0;
+#pragma unroll
+  for (int w = 0; w < kSplitWaves; ++w) count += wave_sum[w];
+  uint32_t v[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    if (k * 64 < mine) v[k] = list[wave][min(k * 64 + lane, mine - 1)];
+  }
+  __syncthreads();
+  // sorted in LDS, so that what is stored is consecutive
+  uint32_t* const sorted = &list[0][0];
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    if (k * 64 + lane < mine) sorted[half(wave, v[k] >> 16) + at[k]] = v[k];
+  }
+  __syncthreads();
+  for (int i = t; i < count; i += kSplitThreads) {
+    const uint32_t x = sorted[i];
+    row_out[below + i] = lo + int(x >> 16);
+    pos_out[below + i] = int(x & 0xffff);
   }
 }
 
@@ -1386,6 +1522,25 @@ int launch_embedding(const void* tokens, bool wide, int64_t n, const void* table
 int launch_token_order(const void* tokens, bool wide, int64_t n, int64_t rows, int32_t* order, hipStream_t stream,
                        const char* who) {
   const Order o(n);
+  // keys are the rows and, behind them, the tokens outside the table
+  const int64_t own = (rows + kSplitBlocks) / kSplitBlocks;
+  if (n > kSplitFrom && n <= kSplitTokens && own <= kSplitEach) {
+    int bits = 0;
+    while ((int64_t(1) << bits) < own) ++bits;
+    const dim3 grid{uint32_t((rows + own) / own)};
+    const auto run = [&](auto iv, auto items) {
+      using I = decltype(iv);
+      constexpr int N = decltype(items)::value;
+      order_split_kernel<I, N><<<grid, kSplitThreads, 0, stream>>>(static_cast<const I*>(tokens), int(n), int(rows),
+                                                                   int(own), bits, order + o.row, order + o.pos);
+    };
+    const auto with = [&](auto iv) {
+      if (n <= kSplitThreads * 8) run(iv, Int<8>());
+      else run(iv, Int<16>());
+    };
+    wide ? with(int64_t()) : with(int32_t());
+    return launched(who);
+  }
   if (n <= kRankTokens) {
     const auto run = [&](auto iv) {
       using I = decltype(iv);

@@ -25,7 +25,7 @@ inline int64_t embedding_pieces(int64_t n) { return (n + embedding_piece(n) - 1)
 constexpr int kSortThreads = 512, kSortItems = 4, kSortBlock = kSortThreads * kSortItems;
 constexpr int kSortBits = 9, kSortDigits = 1 << kSortBits;
 
-// Up to this many tokens are sorted by counting, in one launch.
+// Up to this many tokens are sorted in one launch whatever the table, and need no scratch.
 constexpr int64_t kRankTokens = 12288;
 
 // The parts of an order, in 32-bit words from its start: the sorted tokens' rows,

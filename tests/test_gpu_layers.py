@@ -74,6 +74,26 @@ def test_token_order(n, rows, kind):
     assert (order[len(row):n] == rows).all()
 
 
+@pytest.mark.parametrize("n", [4096, 4097, 5001, 8191, 8192, 8193, 12289, 16383, 16384, 16385])
+@pytest.mark.parametrize("rows", [1, 2, 255, 256, 257, 4000, 50257, 131071, 131072])
+def test_token_order_of_some_thousand(n, rows):
+    """Tokens spread over the table, outside it, in few of its consecutive rows, all on its last row, and in order."""
+    gen = generator(n + rows)
+    pick = lambda lo, hi: torch.randint(lo, hi, (n,), generator=gen, device=gen.device).to(DEV)  # noqa: E731
+    few = max(0, rows // 2 - 70)
+    lists = [pick(-rows // 3 - 1, rows + rows // 3 + 2), pick(few, min(rows, few + 140)), torch.full((n,), rows - 1, device=DEV),
+             torch.where(pick(0, 2) == 0, pick(0, rows), pick(0, 1) + rows // 3), pick(0, rows).sort().values]
+    lists[0][n // 2] = 2 ** 32 + rows // 2       # outside the table, whatever its lower half says
+    lists[0][n // 3] = -2 ** 32 + rows // 2
+    for k, tokens in enumerate(lists):
+        for t in (tokens, tokens.to(torch.int32)) if k else (tokens,):
+            order = order_of(t, rows).cpu().numpy()
+            row, pos = O.token_order(t.cpu().numpy(), rows)
+            up = (n + 7) // 8 * 8 + 8
+            assert order[:len(row)].tolist() == list(row) and order[up:up + len(row)].tolist() == list(pos), k
+            assert (order[len(row):n] == rows).all()
+
+
 def test_token_order_of_a_wide_table():
     """Three passes of the sort."""
     rows, n = 16_000_001, 9500
