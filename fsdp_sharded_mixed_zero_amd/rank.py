@@ -271,7 +271,9 @@ class RankShard:
         ``before_micro(mb)`` runs before each micro-batch when accumulating (to
         refill the gradients). With ``tables`` it returns their gradients, a dict by
         tensor index of (tokens, d_out) or (tokens, d_out, scale), as
-        layers.zero_token_order and zero_embedding_grad take them."""
+        layers.zero_token_order and zero_embedding_grad take them: made on ``stream``
+        or on one that it waits for, and not written to before it is done with them.
+        They need not be kept: their memory is not given out again before then."""
         hp = self.hparams(step)
         own = self.rank_sq[self.rank:self.rank + 1]
         pieces = self.pieces()
@@ -432,7 +434,15 @@ class RankShard:
     def _accumulate_tables(self, by_tokens, first, stream):
         """The micro-batch's table gradients into the accumulator: the rank's
         part of each table, written by the first micro-batch where nothing dense
-        was. A table without an entry has no tokens."""
+        was. A table without an entry has no tokens. The tokens and gradients may
+        be dropped as soon as this returns, and may come from another stream, so
+        the allocator is told of the one that reads them."""
+        if stream is None:
+            on = torch.cuda.current_stream()
+        elif isinstance(stream, int):
+            on = torch.cuda.ExternalStream(stream, device=self.device)
+        else:
+            on = stream
         for i in by_tokens:
             if i not in self.tables:
                 raise ValueError(f"tensor {i} is not among the rank's tables")
@@ -446,10 +456,12 @@ class RankShard:
                 raise ValueError(f"tensor {i}: the gradient of {tokens.numel()} rows of {t['dim']} elements expected, "
                                  f"got {tuple(d_out.shape)}")
             layers.zero_token_order(tokens, t["rows"], t["order"], stream=stream)
+            tokens.record_stream(on)
             for j, s, d, n in self.segments:
                 if j == i:
                     layers.zero_embedding_grad(t["order"], t["rows"], d_out, self.acc[d:d + n], t["workspace"],
                                                *scale, first=s, accumulate=t["dense"] or not first, stream=stream)
+                    d_out.record_stream(on)
 
     def bytes_per_step(self):
         """Algorithmic HBM bytes of one step: pack 4, sum of squares 2 (0 when
