@@ -926,8 +926,9 @@ __device__ __forceinline__ float lanes_sum(float x) {
 // The sums of K values over the TPR threads that share a row, in every one of
 // them. With TPR above 64 every thread of the block has to call it, and lds holds
 // 2 * K * (waves of the block) values, half of which a call takes (`turn`, 0 and 1
-// in turn), so one barrier a call suffices.
-template <int TPR, int K>
+// in turn), so one barrier a call suffices. LEAN: 16 waves' sums are read a lane each,
+// not all by every thread, which takes 16 registers more.
+template <int TPR, int K, bool LEAN = false>
 __device__ __forceinline__ void row_sum(float (&x)[K], float* lds, int turn) {
 #pragma unroll
   for (int k = 0; k < K; ++k) x[k] = lanes_sum<(TPR < 64 ? TPR : 64)>(x[k]);
@@ -941,12 +942,28 @@ __device__ __forceinline__ void row_sum(float (&x)[K], float* lds, int turn) {
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      x[k] = 0.f;
+      if constexpr (LEAN && kWaves == 16) {
+        x[k] = lanes_sum<16>(s[(threadIdx.x & 15) * K + k]);
+      } else {
+        x[k] = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) x[k] += s[(first + w) * K + k];
+        for (int w = 0; w < kWaves; ++w) x[k] += s[(first + w) * K + k];
+      }
     }
   }
 }
+
+// A row's mean is a sum in fp32 that was rounded. Where it is larger than the deviations
+// its error is one more deviation of all elements (a row of 4099 times 1000.1: 1.2e-4, and
+// y 0.04 instead of 0 for eps = 1e-5). There the deviations are summed as well, whose sum
+// has an error of their size: their mean is taken off each of them, as a shift of the
+// normalised values, and its square off that of their squares. Elsewhere the mean's error
+// is no larger than that of the deviations' sum. (Summed in every row: 16384 rows of 1600
+// bf16 22.2 us instead of 21.3, 2048 of 16384 28.4 instead of 27.2.) All threads of a row
+// decide alike, and not for a NaN or an infinity.
+__device__ __forceinline__ bool far_mean(float mean, float rstd) { return fabsf(mean) * rstd > 1.f; }
+
+__device__ __forceinline__ float rstd_of(float var, float eps) { return 1.f / sqrtf(var + eps); }
 
 // TPR threads a row, V vectors each: the row is read once and stays in registers, so
 // the squares are taken after the mean, and the weights are on their way with it.
@@ -1021,7 +1038,20 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(const zero_
     for (int e = 0; e < E; ++e) sum[0] = fmaf(v[k][e], v[k][e], sum[0]);
   }
   row_sum<TPR, 1>(sum, lds, 1);
-  const float rstd = 1.f / sqrtf(sum[0] / float(dim) + float(a.eps));
+  const float var = sum[0] / float(dim);
+  float rstd = rstd_of(var, float(a.eps)), shift = -0.f;
+  if (far_mean(mean, rstd)) {
+    sum[0] = 0.f;
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+#pragma unroll
+      for (int e = 0; e < E; ++e) sum[0] += v[k][e];
+    row_sum<TPR, 1, true>(sum, lds, 0);
+    const float off = sum[0] / float(dim);
+    mean += off;
+    rstd = rstd_of(fmaxf(var - off * off, 0.f), float(a.eps));
+    shift = -off * rstd;
+  }
   if (t == 0) {
     if (a.mean != nullptr) a.mean[row] = mean;
     if (a.rstd != nullptr) a.rstd[row] = rstd;
@@ -1033,7 +1063,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_kernel(const zero_
     widen<E, W>(w[k], wf);
     widen<E, W>(b[k], bf);
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[k][e] = fmaf(v[k][e] * rstd, wf[e], bf[e]);
+    for (int e = 0; e < E; ++e) v[k][e] = fmaf(fmaf(v[k][e], rstd, shift), wf[e], bf[e]);
     store_row<E>(y, s[k], narrow<E, T>(v[k]));
   }
 }
@@ -1077,6 +1107,7 @@ __global__ __launch_bounds__(kLongThreads) void norm_long_kernel(const zero_norm
     mean = sum[0] / float(dim);
   }
   sum[0] = 0.f;
+  float dev[1] = {0.f};
   for (int k = threadIdx.x; k < vectors; k += kLongThreads) {
     const Span s = span_of<E>(k, dim);
     float v[E];
@@ -1085,12 +1116,21 @@ __global__ __launch_bounds__(kLongThreads) void norm_long_kernel(const zero_norm
     for (int e = 0; e < E; ++e) v[e] -= mean;
     only_own<E>(s, v);
 #pragma unroll
-    for (int e = 0; e < E; ++e) sum[0] = fmaf(v[e], v[e], sum[0]);
+    for (int e = 0; e < E; ++e) {
+      sum[0] = fmaf(v[e], v[e], sum[0]);
+      dev[0] += v[e];
+    }
   }
   row_sum<kLongThreads, 1>(sum, lds, 1);
-  const float rstd = 1.f / sqrtf(sum[0] / float(dim) + float(a.eps));
+  const float var = sum[0] / float(dim);
+  float rstd = rstd_of(var, float(a.eps)), off = 0.f;
+  if (far_mean(mean, rstd)) {
+    row_sum<kLongThreads, 1>(dev, lds, 0);
+    off = dev[0] / float(dim);
+    rstd = rstd_of(fmaxf(var - off * off, 0.f), float(a.eps));
+  }
   if (threadIdx.x == 0) {
-    if (a.mean != nullptr) a.mean[row] = mean;
+    if (a.mean != nullptr) a.mean[row] = mean + off;
     if (a.rstd != nullptr) a.rstd[row] = rstd;
   }
   T* y = static_cast<T*>(a.y) + row * a.y_stride;
@@ -1101,7 +1141,7 @@ __global__ __launch_bounds__(kLongThreads) void norm_long_kernel(const zero_norm
     widen<E, W>(load_weight<E, W>(a.weight, s, 1.f), w);
     widen<E, W>(load_weight<E, W>(a.bias, s, 0.f), b);
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = fmaf((v[e] - mean) * rstd, w[e], b[e]);
+    for (int e = 0; e < E; ++e) v[e] = fmaf((v[e] - mean - off) * rstd, w[e], b[e]);
     store_row<E, false>(y, s, narrow<E, T>(v));
   }
 }

@@ -109,8 +109,10 @@ int zero_embedding_grad(const void* order, int64_t n, int64_t rows, int64_t dim,
  *   mean = sum(s) / dim          (0 where rms is set)
  *   rstd = 1 / sqrt(sum((s - mean)^2) / dim + eps)
  *   y = (s - mean) * rstd * weight + bias
- * Statistics are taken in fp32, the squares after the mean, from a row that stays in
- * registers, and are left in mean and rstd for the backward pass.
+ * Statistics are taken in fp32, the squares after the mean, and are left in mean and
+ * rstd for the backward pass. In a row whose mean is larger than sqrt(variance + eps),
+ * the rounding of the first mean is taken off by the sum of the deviations from it, so
+ * a row of equal values gives the bias, however large they are.
  *   type, weight_type  ZERO_BF16 or ZERO_F32: of x, residual, total and y; of weight
  *                  and bias
  *   residual, total  both or neither
