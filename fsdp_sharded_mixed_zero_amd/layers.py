@@ -81,9 +81,19 @@ def _load():
     _C, _torch = torch._C, torch
 
 
+# ctypes cuts an integer to the 64 bits of its argument: one beyond them is refused here.
+_TOP = 1 << 63
+
+
+def _fits(k, what):
+    if not -_TOP <= k < _TOP:
+        raise ValueError(f"{what} = {k} is beyond the limits of include/zero_layers.h")
+
+
 def _sized(name, *sizes):
     """Bytes of an order or a workspace."""
-    nbytes = int(getattr(_lib or library(), name)(*sizes))
+    fit = all(-_TOP <= k < _TOP for k in sizes)
+    nbytes = int(getattr(_lib or library(), name)(*sizes)) if fit else 0
     if nbytes == 0:
         raise ValueError(f"{name}: sizes {sizes} outside the limits of include/zero_layers.h")
     return nbytes
@@ -187,6 +197,7 @@ def zero_token_order(tokens, rows: int, order, stream=None):
     dev = _device()
     ids, n = _tokens(tokens, dev)
     p, nbytes = _memory(order, "order", dev)
+    _fits(rows, "rows")
     rc = _lib.zero_token_order(ids, _IDS[tokens.dtype], n, rows, p, nbytes, _stream(stream, dev))
     if rc:
         zero._check("zero_token_order", rc)
@@ -205,6 +216,8 @@ def zero_embedding_grad(order, rows: int, d_out, grad, workspace, scale: float =
     src, stride = _rows(d_out, "d_out", dev, None, _TYPES)
     n, dim = d_out.shape
     p, order_bytes = _memory(order, "order", dev)
+    _fits(rows, "rows")
+    _fits(first, "first")
     need = _lib.zero_token_order_bytes(n, rows)
     if order_bytes < need:
         raise ValueError(f"order: {order_bytes} bytes given, the call reaches {need}")
