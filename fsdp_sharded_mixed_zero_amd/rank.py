@@ -412,8 +412,7 @@ class RankShard:
             for b, n in self.dense_pieces:
                 mark("pack", lambda: zero.zero_pack_grads(self.layout, self.grad_ptrs, self.grad_shard, b, n,
                                                           stream))
-                mark("accumulate", lambda: zero.zero_accumulate_grads(self.grad_shard[b:], self.acc[b:], n,
-                                                                      mb == 0, stream))
+                mark("accumulate", lambda: self._accumulate(b, n, mb == 0, stream))
             if self.tables:
                 mark("tables", lambda: self._accumulate_tables(by_tokens or {}, mb == 0, stream))
         for k, (b, n) in enumerate(pieces):
@@ -430,6 +429,15 @@ class RankShard:
                 self.wl.n_d, stream))
             mark("unpack", lambda: zero.zero_unpack_params(self.layout, self.param_shard, self.param_ptrs,
                                                           b, n, stream))
+
+    def _accumulate(self, b, n, first, stream):
+        """The packed elements [b, b + n) into the accumulator. A piece behind a table may
+        begin at any element: the few up to the next multiple of 8 apart, since the call
+        takes vectors only where both arrays are aligned."""
+        head = min(-b % 8, n)
+        for at, count in ((b, head), (b + head, n - head)):
+            if count > 0:
+                zero.zero_accumulate_grads(self.grad_shard[at:], self.acc[at:], count, first, stream)
 
     def _accumulate_tables(self, by_tokens, first, stream):
         """The micro-batch's table gradients into the accumulator: the rank's
