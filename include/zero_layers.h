@@ -85,8 +85,10 @@ int zero_token_order(const void* tokens, int32_t token_type, int64_t n, int64_t 
  * neither read nor written.
  * A row's terms are added in fp32 in ascending position, in pieces of consecutive
  * sorted tokens whose sums are then added in order.
- *   order       as zero_token_order has written it for the same n and rows; another
- *               one gives other sums, of the same arrays
+ *   order       as zero_token_order has written it for the same n and rows, in
+ *               zero_token_order_bytes(n, rows) bytes: so many are read, which the
+ *               library cannot check (the Python binding does). Other contents of a
+ *               buffer of that size give other sums, of the same arrays
  *   d_out       [n, dim] with its stride, ZERO_BF16 or ZERO_F32; what the rows of
  *               tokens outside the table hold does not matter
  *   grad        the part's count elements, ZERO_BF16 or ZERO_F32
