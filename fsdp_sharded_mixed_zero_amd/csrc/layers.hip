@@ -1788,12 +1788,14 @@ int launch_norm_grad(const zero_norm_grad_args& a, float* ws, hipStream_t stream
     spread(Int<128>(), Int<1>());
     spread(Int<192>(), Int<1>());
     spread(Int<256>(), Int<1>());
+    spread(Int<320>(), Int<1>());
     spread(Int<384>(), Int<1>());
     spread(Int<512>(), Int<1>());
+    spread(Int<640>(), Int<1>());
     spread(Int<768>(), Int<1>());
     if constexpr (E == 4) {
-      spread(Int<320>(), Int<1>());
       spread(Int<512>(), Int<2>());
+      spread(Int<640>(), Int<2>());
       spread(Int<768>(), Int<2>());
     }
     spread(Int<1024>(), Int<8 / E>());

@@ -75,16 +75,21 @@ inline NormShape norm_shape(int64_t n, int64_t vectors) {
 // The same for the gradient, rows of `dim` elements, `per` of them a vector. Its two
 // sums a column take 16 registers for a vector of bf16, so a thread takes one, or
 // one of fp32 (5003 rows of 1111: 20 us of a call, 21.4 with two) while 768 threads
-// suffice and two beyond. Twice as many spill: rows of more than 8192 elements take
-// two kernels (4096 rows of 12000 bf16: 259 us in registers).
+// suffice and two beyond. The fewest threads of one list for both types: idle ones cost
+// a wave's share of the registers (16384 rows of 2560 bf16 with 320 threads 64.0 us, with
+// 384 65.2; of 2100 62.6 and 66.2; 8192 of 5120 with 640 71.0, with 768 72.0; 5003 of
+// 1111 fp32 with 320 23.3, with 384 23.8; 8192 of 2560 fp32 with 640 65.0, with 768 66.0).
+// With 1024 threads of 128 registers 4 spill for bf16 (20 bytes a lane) and 13 for fp32
+// (56): 8192 rows of 8192 bf16 112 us, 4.8 TB/s. Twice as many sums spill more: rows of
+// more than 8192 elements take two kernels (4096 rows of 12000 bf16: 259 us in registers).
 inline NormShape norm_grad_shape(int64_t dim, int per) {
   const int64_t vectors = (dim + per - 1) / per;
   if (vectors <= 32) return {vectors <= 16 ? 16 : 32, 1};
-  if (per == 4)
-    for (int t : {64, 128, 192, 256, 320, 384, 512, 768})
-      if (t >= vectors) return {t, 1};
-  for (int t : {64, 128, 192, 256, 384, 512, 768, 1024})
-    if (int64_t(t) * (8 / per) >= vectors) return {t, 8 / per};   // fp32: from 512 on
+  for (int v = 1; v <= 8 / per; ++v)
+    for (int t : {64, 128, 192, 256, 320, 384, 512, 640, 768, 1024}) {
+      if (t == 1024 && v < 8 / per) break;
+      if (int64_t(t) * v >= vectors) return {t, v};       // two of fp32: from 512 threads on
+    }
   return {0, 0};
 }
 
