@@ -57,9 +57,10 @@ inline int row_bits(int64_t rows) {
 
 // How a norm's row of 16-byte vectors is spread: the threads that share it, and
 // the vectors that each takes; threads 0: a row too long for the registers. A wave
-// a row needs no barrier, up to four vectors a lane (16384 rows of 1600 bf16: 21 us,
-// 26 with 256 threads a row; rows of 2944: 38 us with six, 36 with 256 threads); few
-// rows take more threads each, for the latency (8 rows of 1600: 3.6 us instead of 6.0).
+// a row needs no barrier: up to two vectors a lane, from 1024 rows on up to four (16384
+// rows of 1600 bf16: 21 us, 26 with 256 threads a row; rows of 2944: 38 us with six, 36
+// with 256 threads); fewer rows take more threads each, for the latency (8 rows of 1600:
+// 3.6 us instead of 6.0).
 struct NormShape {
   int threads, vectors;
 };

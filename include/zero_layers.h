@@ -114,7 +114,8 @@ int zero_embedding_grad(const void* order, int64_t n, int64_t rows, int64_t dim,
  * Statistics are taken in fp32, the squares after the mean, and are left in mean and
  * rstd for the backward pass. In a row whose mean is larger than sqrt(variance + eps),
  * the rounding of the first mean is taken off by the sum of the deviations from it, so
- * a row of equal values gives the bias, however large they are.
+ * a row of equal values gives the bias, however large they are. A row whose squared
+ * deviations add up to more than fp32 holds gets rstd = 0.
  *   type, weight_type  ZERO_BF16 or ZERO_F32: of x, residual, total and y; of weight
  *                  and bias
  *   residual, total  both or neither
