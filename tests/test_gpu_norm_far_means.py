@@ -108,3 +108,24 @@ def test_bad_values_keep_their_means(dim, dtype):
     layers.zero_norm(clean, alone, m, r)
     for a, b in ((y, alone), (mean, m), (rstd, r)):
         assert torch.equal(a[[0, 4]], b[[0, 4]])
+
+
+@pytest.mark.parametrize("dim", [5, 33, 100, 129, 200, 300, 777, 1600, 20000])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_far_and_near_means_side_by_side(dim, dtype):
+    """Rows that keep their first mean between rows that do not, several of them in a wave: each as if alone."""
+    n = 37
+    x = normal(generator(dim), n, dim)
+    x[::3] += 1e4 if dtype == F32 else 100.0
+    x[1::6] = 1000.1
+    x = x.to(dtype)
+    y, mean, rstd = torch.empty_like(x), torch.empty(n, device=DEV), torch.empty(n, device=DEV)
+    layers.zero_norm(x, y, mean, rstd)
+    one = torch.ones(dim, device=DEV)
+    want, bound = bounds(x, one, torch.zeros(dim, device=DEV), dtype)
+    for got, v, e, what in zip((y, mean, rstd), want, bound, ("y", "mean", "rstd")):
+        close(got, v, e, what)
+    for k in range(n):
+        y1, m1, r1 = torch.empty_like(x[:1]), torch.empty(1, device=DEV), torch.empty(1, device=DEV)
+        layers.zero_norm(x[k:k + 1], y1, m1, r1)
+        assert torch.equal(y1[0], y[k]) and torch.equal(m1[0], mean[k]) and torch.equal(r1[0], rstd[k])

@@ -38,3 +38,14 @@ def test_micro_batches_may_be_dropped_at_once(kind):
     torch.cuda.synchronize()
     assert torch.equal(here.acc, there.acc) and torch.equal(here.param_shard, there.param_shard)
     assert all(int(t.count_nonzero()) == 0 for t in junk)
+
+
+def test_a_step_on_the_default_streams_handle():
+    wl = synth.Workload("streams", SIZES, n_d=1, rank=0, align=16, grad_std=1e-2, seed=3)
+    tables = {0: {"dim": DIM, "tokens": 50}}
+    given = (draw_tokens(50, ROWS, 1), normal(generator(1), 50, DIM, dtype=torch.bfloat16))
+    a, b = RankShard(wl, accum_steps=2, tables=tables), RankShard(wl, accum_steps=2, tables=tables)
+    a.step(1, before_micro=lambda mb: {0: given})
+    b.step(1, stream=torch.cuda.default_stream().cuda_stream, before_micro=lambda mb: {0: tuple(t.clone() for t in given)})
+    torch.cuda.synchronize()
+    assert torch.equal(a.acc, b.acc) and torch.equal(a.param_shard, b.param_shard)
